@@ -15,7 +15,8 @@ _lib = None
 
 MCS_GROUP_SIZE = 128
 MCS_INFO_WORDS = 8
-MCS_OP_GROUP, MCS_OP_ANCHOR, MCS_OP_SPARSE, MCS_OP_DENSE = 0, 1, 2, 3
+MCS_OP_GROUP, MCS_OP_ANCHOR, MCS_OP_SPARSE, MCS_OP_DENSE, MCS_OP_DENSE_EX, MCS_OP_DENSE_BWD = 0, 1, 2, 3, 4, 5
+MCS_ATTN_CAUSAL = 1
 
 
 class MCSError(RuntimeError):
@@ -34,6 +35,34 @@ class Shape(ctypes.Structure):
         super().__init__(B, H, N, d, group, topk, scale)
 
 
+class AttnShape(ctypes.Structure):
+    """mcs_attn_shape: query and KV heads, lengths, scale (<= 0 selects 1/sqrt(d)), score cap (0: none), causal."""
+
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("Nq", ctypes.c_int),
+                ("Nk", ctypes.c_int), ("d", ctypes.c_int), ("scale", ctypes.c_float), ("cap", ctypes.c_float),
+                ("flags", ctypes.c_int)]
+
+    def __init__(self, B, Hq, Hkv, Nq, Nk, d, scale=0.0, cap=0.0, causal=False):
+        super().__init__(B, Hq, Hkv, Nq, Nk, d, scale, cap, MCS_ATTN_CAUSAL if causal else 0)
+
+
+class AttnOpts(ctypes.Structure):
+    """mcs_attn_opts: device pointers of the distance slopes, prefix lengths and document ids (each may be null)."""
+
+    _fields_ = [("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p), ("doc_q", ctypes.c_void_p),
+                ("doc_k", ctypes.c_void_p)]
+
+
+class DecodeShape(ctypes.Structure):
+    """mcs_decode_shape: batch, heads, cache capacity C, shared prefix length P, scale, score cap."""
+
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("C", ctypes.c_int),
+                ("P", ctypes.c_int), ("d", ctypes.c_int), ("scale", ctypes.c_float), ("cap", ctypes.c_float)]
+
+    def __init__(self, B, Hq, Hkv, C, d, P=0, scale=0.0, cap=0.0):
+        super().__init__(B, Hq, Hkv, C, P, d, scale, cap)
+
+
 def lib_path() -> str:
     return _LIB_PATH
 
@@ -49,6 +78,11 @@ def load():
     vp, sz, sp = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(Shape)
     lib.mcs_workspace_bytes.restype = sz
     lib.mcs_workspace_bytes.argtypes = [sp, ctypes.c_int]
+    ap, op, dp = ctypes.POINTER(AttnShape), ctypes.POINTER(AttnOpts), ctypes.POINTER(DecodeShape)
+    lib.mcs_attn_workspace_bytes.restype = sz
+    lib.mcs_attn_workspace_bytes.argtypes = [ap, ctypes.c_int]
+    lib.mcs_decode_workspace_bytes.restype = sz
+    lib.mcs_decode_workspace_bytes.argtypes = [dp]
     lib.mcs_meta_mask_bytes.restype = sz
     lib.mcs_meta_mask_bytes.argtypes = [sp]
     for name, args in [
@@ -59,6 +93,10 @@ def load():
         ("mcs_sparse", [sp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         ("mcs_sparse_noalloc", [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         ("mcs_dense", [sp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        ("mcs_dense_ex", [ap, op, vp, vp, vp, vp, vp, vp, sz, vp]),
+        ("mcs_dense_bwd", [ap, op, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        ("mcs_decode", [dp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        ("mcs_decode_shared", [dp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         ("mcs_sparse_host", [sp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int, vp, sz, vp, vp, vp]),
         ("mcs_meta_copy", [vp, vp, sz, ctypes.c_int, vp, vp, vp]),
         ("mcs_meta_pack", [sp, vp, vp, vp, sz, vp]),
@@ -182,6 +220,104 @@ def mcs_sparse_host(shape, q_host, k_host, v_host, perm, kv_idx, resid, o_host, 
 def mcs_dense(shape, q, k, v, o, lse, ws, stream=None):
     _check(load().mcs_dense(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(ws),
                             ws.numel(), _stream(stream)), "mcs_dense")
+
+
+def mcs_attn_workspace_bytes(shape: AttnShape, op: int) -> int:
+    return int(load().mcs_attn_workspace_bytes(ctypes.byref(shape), op))
+
+
+def attn_workspace(shape: AttnShape, op: int, device="cuda"):
+    """Zeroed workspace of mcs_dense_ex (MCS_OP_DENSE_EX) or mcs_dense_bwd (MCS_OP_DENSE_BWD)."""
+    import torch
+
+    n = mcs_attn_workspace_bytes(shape, op)
+    if n == 0:
+        raise MCSError(1, "mcs_attn_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def mcs_decode_workspace_bytes(shape: DecodeShape) -> int:
+    return int(load().mcs_decode_workspace_bytes(ctypes.byref(shape)))
+
+
+def decode_workspace(shape: DecodeShape, device="cuda"):
+    """Zeroed workspace of mcs_decode and mcs_decode_shared."""
+    import torch
+
+    n = mcs_decode_workspace_bytes(shape)
+    if n == 0:
+        raise MCSError(1, "mcs_decode_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _fits(what, **tensors):
+    """Refuse a tensor that is not what the kernels read: name=(tensor, dtype name, shape); None passes.
+
+    All tensors are contiguous and on the current CUDA device (where the stream is)."""
+    import torch
+
+    device = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype is not getattr(torch, dtype) or not t.is_contiguous() or (shape is not None and t.shape != shape):
+            raise MCSError(1, f"{what}: {name} must be contiguous {dtype} {shape if shape is not None else ''}, got "
+                              f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+        if not t.is_cuda or t.get_device() != device:
+            raise MCSError(1, f"{what}: {name} is on {t.device}, not on the current CUDA device")
+
+
+def _attn_fits(what, s, q_like, k_like, lse, ws, slopes, prefix, doc_q, doc_k):
+    qs, ks = (s.B, s.Nq, s.Hq, s.d), (s.B, s.Nk, s.Hkv, s.d)
+    _fits(what, **{n: (t, "bfloat16", qs) for n, t in q_like.items()},
+          **{n: (t, "bfloat16", ks) for n, t in k_like.items()},
+          lse=(lse, "float32", (s.B, s.Hq, s.Nq)), ws=(ws, "uint8", None), slopes=(slopes, "float32", (s.Hq,)),
+          prefix=(prefix, "int32", (s.B,)), doc_q=(doc_q, "int32", (s.B, s.Nq)), doc_k=(doc_k, "int32", (s.B, s.Nk)))
+
+
+def _opts(slopes, prefix, doc_q, doc_k):
+    if slopes is None and prefix is None and doc_q is None and doc_k is None:
+        return None
+    return ctypes.byref(AttnOpts(*(None if t is None else t.data_ptr() for t in (slopes, prefix, doc_q, doc_k))))
+
+
+def mcs_dense_ex(shape, q, k, v, o, lse, ws, slopes=None, prefix=None, doc_q=None, doc_k=None, stream=None):
+    """Attention with capped or biased scores, causal, prefix and document masks, shared KV heads."""
+    _attn_fits("mcs_dense_ex", shape, dict(q=q, o=o), dict(k=k, v=v), lse, ws, slopes, prefix, doc_q, doc_k)
+    _check(load().mcs_dense_ex(ctypes.byref(shape), _opts(slopes, prefix, doc_q, doc_k), _ptr(q), _ptr(k), _ptr(v),
+                               _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "mcs_dense_ex")
+
+
+def mcs_dense_bwd(shape, q, k, v, o, lse, d_o, dq, dk, dv, ws, slopes=None, prefix=None, doc_q=None, doc_k=None,
+                  stream=None):
+    """Gradients of mcs_dense_ex with respect to q, k and v, from its o and lse and the gradient d_o of o."""
+    _attn_fits("mcs_dense_bwd", shape, dict(q=q, o=o, d_o=d_o, dq=dq), dict(k=k, v=v, dk=dk, dv=dv), lse, ws, slopes,
+               prefix, doc_q, doc_k)
+    _check(load().mcs_dense_bwd(ctypes.byref(shape), _opts(slopes, prefix, doc_q, doc_k), _ptr(q), _ptr(k), _ptr(v),
+                                _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
+                                _stream(stream)), "mcs_dense_bwd")
+
+
+def _decode_fits(what, s, q, kp, vp, k, v, lens, o, lse, ws, slopes):
+    qs, cs, ps = (s.B, s.Hq, s.d), (s.B, s.C, s.Hkv, s.d), (s.P, s.Hkv, s.d)
+    _fits(what, q=(q, "bfloat16", qs), o=(o, "bfloat16", qs), kp=(kp, "bfloat16", ps), vp=(vp, "bfloat16", ps),
+          k=(k, "bfloat16", cs), v=(v, "bfloat16", cs), lens=(lens, "int32", (s.B,)),
+          lse=(lse, "float32", (s.B, s.Hq)), ws=(ws, "uint8", None), slopes=(slopes, "float32", (s.Hq,)))
+
+
+def mcs_decode(shape, q, k, v, lens, o, lse, ws, slopes=None, stream=None):
+    """One token per request over a cache of capacity C (request b holds lens[b] keys)."""
+    _decode_fits("mcs_decode", shape, q, None, None, k, v, lens, o, lse, ws, slopes)
+    _check(load().mcs_decode(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(lens), _ptr(slopes), _ptr(o),
+                             _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "mcs_decode")
+
+
+def mcs_decode_shared(shape, q, kp, vp, k, v, lens, o, lse, ws, slopes=None, stream=None):
+    """mcs_decode behind a prefix of P keys that all requests share, read once for the batch."""
+    _decode_fits("mcs_decode_shared", shape, q, kp, vp, k, v, lens, o, lse, ws, slopes)
+    _check(load().mcs_decode_shared(ctypes.byref(shape), _ptr(q), _ptr(kp), _ptr(vp), _ptr(k), _ptr(v), _ptr(lens),
+                                    _ptr(slopes), _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
+           "mcs_decode_shared")
 
 
 def _event(ev, must_exist: bool):

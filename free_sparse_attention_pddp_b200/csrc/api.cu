@@ -74,13 +74,6 @@ mcs_status tokens_map(CUtensorMap* m, const void* base, uint64_t tokens, int H, 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-mcs_status check_device() {
-  int dev = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MCS_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return MCS_ERR_CUDA;
-  return major == 10 ? MCS_OK : MCS_ERR_UNSUPPORTED;
-}
-
 mcs_status check_shape(const mcs_shape* s, bool need_topk) {
   if (!s) return MCS_ERR_INVALID_ARG;
   if (s->B < 1 || s->H < 1 || s->N < 1 || s->d < 1) return MCS_ERR_INVALID_ARG;
@@ -137,6 +130,13 @@ mcs_status cuda_status(cudaError_t e) { return e == cudaSuccess ? MCS_OK : MCS_E
 
 }  // namespace
 
+mcs_status check_device() {
+  int dev = 0, major = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MCS_ERR_CUDA;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return MCS_ERR_CUDA;
+  return major == 10 ? MCS_OK : MCS_ERR_UNSUPPORTED;
+}
+
 int debug_flags() { return g_debug_flags; }
 void note_launches(int n) { g_launches += n; }
 
@@ -156,6 +156,8 @@ size_t mcs_workspace_bytes(const mcs_shape* s, mcs_op op) {
       return anchor_layout(s).total;
     case MCS_OP_GROUP:
       return MCS_STATUS_BYTES + pddp_workspace_bytes(s->B, s->H, s->N, s->d);
+    default:  // the operators with a shape struct of their own
+      return 0;
   }
   return 0;
 }

@@ -1,0 +1,188 @@
+// C ABI entry points of the attention with modified scores (declared in
+// include/mcs.h): host-side validation, workspace layout and launches.
+#include <math.h>
+
+#include "mcs_internal.h"
+
+using namespace mcs;
+
+namespace {
+
+constexpr int kMaxGroup = 128;            // query heads of one KV head: one 128-row tile holds a token's
+constexpr int kMaxDocTiles = 1 << 16;     // tiles of a document mask's bitmap
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+bool finite(float x) { return x == x && !isinf(x); }
+
+mcs_status check_heads(int Hq, int Hkv, int d, float scale, float cap) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1) return MCS_ERR_INVALID_ARG;
+  if (!finite(scale) || !finite(cap) || cap < 0.f) return MCS_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return MCS_ERR_UNSUPPORTED;
+  if (Hq / Hkv > kMaxGroup) return MCS_ERR_UNSUPPORTED;
+  return MCS_OK;
+}
+
+mcs_status check_attn(const mcs_attn_shape* s) {
+  if (!s || s->B < 1 || s->Nq < 1 || s->Nk < 1) return MCS_ERR_INVALID_ARG;
+  if ((s->flags & ~MCS_ATTN_CAUSAL) != 0) return MCS_ERR_INVALID_ARG;
+  const mcs_status st = check_heads(s->Hq, s->Hkv, s->d, s->scale, s->cap);
+  if (st != MCS_OK) return st;
+  if (static_cast<long long>(s->B) * s->Nq >= (1ll << 31) / s->Hq ||
+      static_cast<long long>(s->B) * s->Nk >= (1ll << 31) / s->Hkv)
+    return MCS_ERR_INVALID_ARG;
+  return MCS_OK;
+}
+
+mcs_status check_opts(const mcs_attn_shape* s, const mcs_attn_opts* o) {
+  if (!o) return MCS_OK;
+  if (!aligned4(o->slopes) || !aligned4(o->prefix) || !aligned4(o->doc_q) || !aligned4(o->doc_k))
+    return MCS_ERR_INVALID_ARG;
+  if (o->prefix && !(s->flags & MCS_ATTN_CAUSAL)) return MCS_ERR_INVALID_ARG;
+  if ((o->doc_q == nullptr) != (o->doc_k == nullptr)) return MCS_ERR_INVALID_ARG;
+  if (o->doc_q) {
+    const int tokens = 128 / (s->Hq / s->Hkv);
+    if ((static_cast<long long>(s->Nk) + 127) / 128 > kMaxDocTiles ||
+        (static_cast<long long>(s->Nq) + tokens - 1) / tokens > kMaxDocTiles)
+      return MCS_ERR_UNSUPPORTED;
+  }
+  return MCS_OK;
+}
+
+float scale_of(float scale, int d) { return scale > 0.f ? scale : static_cast<float>(1.0 / sqrt(static_cast<double>(d))); }
+
+ExParams ex_params(const mcs_attn_shape* s, const mcs_attn_opts* o) {
+  ExParams p{};
+  p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.g = s->Hq / s->Hkv; p.Nq = s->Nq; p.Nk = s->Nk;
+  p.scale = scale_of(s->scale, s->d);
+  p.cap = s->cap;
+  p.causal = (s->flags & MCS_ATTN_CAUSAL) != 0;
+  if (o) {
+    p.slopes = o->slopes;
+    p.prefix = o->prefix;
+    p.doc_q = o->doc_q;
+    p.doc_k = o->doc_k;
+  }
+  return p;
+}
+
+mcs_status check_decode(const mcs_decode_shape* s) {
+  if (!s || s->B < 1 || s->C < 1 || s->P < 0) return MCS_ERR_INVALID_ARG;
+  const mcs_status st = check_heads(s->Hq, s->Hkv, s->d, s->scale, s->cap);
+  if (st != MCS_OK) return st;
+  if (static_cast<long long>(s->B) * s->C >= (1ll << 31) / s->Hkv || s->P >= (1ll << 31) / s->Hkv ||
+      static_cast<long long>(s->B) * s->Hq >= (1ll << 31) || static_cast<long long>(s->P) + s->C >= (1ll << 31))
+    return MCS_ERR_INVALID_ARG;
+  return MCS_OK;
+}
+
+mcs_status decode_call(const mcs_decode_shape* s, const void* q, const void* kp, const void* vp, const void* k,
+                       const void* v, const int32_t* lens, const float* slopes, void* o, float* lse, void* ws,
+                       size_t ws_bytes, cudaStream_t stream) {
+  if (!q || !k || !v || !lens || !o || !ws || (s->P > 0 && (!kp || !vp))) return MCS_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(kp) || !aligned16(vp) ||
+      !aligned4(lens) || !aligned4(slopes) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return MCS_ERR_INVALID_ARG;
+  if (ws_bytes < mcs_decode_workspace_bytes(s)) return MCS_ERR_INVALID_ARG;
+  const mcs_status st = check_device();
+  if (st != MCS_OK) return st;
+  DecodeParams p{};
+  p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.g = s->Hq / s->Hkv; p.C = s->C; p.P = s->P;
+  p.scale = scale_of(s->scale, s->d);
+  p.cap = s->cap;
+  p.q = static_cast<const uint16_t*>(q);
+  p.kp = static_cast<const uint16_t*>(kp);
+  p.vp = static_cast<const uint16_t*>(vp);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.lens = lens;
+  p.slopes = slopes;
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.status = static_cast<int*>(ws);
+  return launch_decode_rows(s->d, p, stream) == cudaSuccess ? MCS_OK : MCS_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mcs_attn_workspace_bytes(const mcs_attn_shape* s, mcs_op op) {
+  if (check_attn(s) != MCS_OK) return 0;
+  if (op == MCS_OP_DENSE_EX) return MCS_STATUS_BYTES;
+  if (op == MCS_OP_DENSE_BWD) return MCS_STATUS_BYTES + align256(static_cast<size_t>(s->B) * s->Hq * s->Nq * 4);
+  return 0;
+}
+
+mcs_status mcs_dense_ex(const mcs_attn_shape* s, const mcs_attn_opts* opts, const void* q, const void* k,
+                        const void* v, void* o, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  mcs_status st = check_attn(s);
+  if (st != MCS_OK) return st;
+  if (!q || !k || !v || !o || !ws) return MCS_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(lse) ||
+      (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return MCS_ERR_INVALID_ARG;
+  if ((st = check_opts(s, opts)) != MCS_OK) return st;
+  if (ws_bytes < mcs_attn_workspace_bytes(s, MCS_OP_DENSE_EX)) return MCS_ERR_INVALID_ARG;
+  if ((st = check_device()) != MCS_OK) return st;
+  ExParams p = ex_params(s, opts);
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.status = static_cast<int*>(ws);
+  return launch_ex_rows_fwd(s->d, p, stream) == cudaSuccess ? MCS_OK : MCS_ERR_CUDA;
+}
+
+mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, const void* q, const void* k,
+                         const void* v, const void* o, const float* lse, const void* d_o, void* dq, void* dk,
+                         void* dv, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  mcs_status st = check_attn(s);
+  if (st != MCS_OK) return st;
+  if (!q || !k || !v || !o || !lse || !d_o || !dq || !dk || !dv || !ws) return MCS_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(d_o) || !aligned16(dq) ||
+      !aligned16(dk) || !aligned16(dv) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return MCS_ERR_INVALID_ARG;
+  if ((st = check_opts(s, opts)) != MCS_OK) return st;
+  if (ws_bytes < mcs_attn_workspace_bytes(s, MCS_OP_DENSE_BWD)) return MCS_ERR_INVALID_ARG;
+  if ((st = check_device()) != MCS_OK) return st;
+  ExParams p = ex_params(s, opts);
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.o_in = static_cast<const uint16_t*>(o);
+  p.d_o = static_cast<const uint16_t*>(d_o);
+  p.lse_in = lse;
+  p.dq = static_cast<uint16_t*>(dq);
+  p.dk = static_cast<uint16_t*>(dk);
+  p.dv = static_cast<uint16_t*>(dv);
+  p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + MCS_STATUS_BYTES);
+  p.status = static_cast<int*>(ws);
+  return launch_ex_rows_bwd(s->d, p, stream) == cudaSuccess ? MCS_OK : MCS_ERR_CUDA;
+}
+
+size_t mcs_decode_workspace_bytes(const mcs_decode_shape* s) {
+  if (check_decode(s) != MCS_OK) return 0;
+  return MCS_STATUS_BYTES;
+}
+
+mcs_status mcs_decode(const mcs_decode_shape* s, const void* q, const void* k, const void* v, const int32_t* lens,
+                      const float* slopes, void* o, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const mcs_status st = check_decode(s);
+  if (st != MCS_OK) return st;
+  if (s->P != 0) return MCS_ERR_INVALID_ARG;
+  return decode_call(s, q, nullptr, nullptr, k, v, lens, slopes, o, lse, ws, ws_bytes, stream);
+}
+
+mcs_status mcs_decode_shared(const mcs_decode_shape* s, const void* q, const void* kp, const void* vp,
+                             const void* k, const void* v, const int32_t* lens, const float* slopes, void* o,
+                             float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const mcs_status st = check_decode(s);
+  if (st != MCS_OK) return st;
+  if (s->P < 1) return MCS_ERR_INVALID_ARG;
+  return decode_call(s, q, kp, vp, k, v, lens, slopes, o, lse, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -114,6 +114,44 @@ cudaError_t pddp_run(int B, int H, int N, int d, const uint16_t* q, int32_t* per
                      int* status, int krylov_steps, bool whiten, cudaStream_t s);
 size_t pddp_workspace_bytes(int B, int H, int N, int d);
 
+// ---- attention with modified scores (api_ex.cu, attn_ex*.cu) ----
+
+struct ExParams {
+  int B, Hq, Hkv, g, Nq, Nk;   // g = Hq / Hkv
+  float scale;                 // softmax scale
+  float cap;                   // 0: none
+  int causal;
+  const float* slopes;         // [Hq] or null
+  const int32_t* prefix;       // [B] or null
+  const int32_t *doc_q, *doc_k;  // [B,Nq], [B,Nk] or null
+  const uint16_t *q, *k, *v;   // bf16
+  const uint16_t *o_in, *d_o;  // backward: the forward's output and its gradient
+  const float* lse_in;         // backward: the forward's lse
+  uint16_t* o;
+  float* lse;                  // nullable
+  uint16_t *dq, *dk, *dv;
+  float* delta;                // backward: sum_c d_o o per row, [B,Hq,Nq]
+  int* status;
+};
+
+struct DecodeParams {
+  int B, Hq, Hkv, g, C, P;
+  float scale, cap;
+  const uint16_t *q, *kp, *vp, *k, *v;
+  const int32_t* lens;
+  const float* slopes;
+  uint16_t* o;
+  float* lse;
+  int* status;
+};
+
+cudaError_t launch_ex_rows_fwd(int d, const ExParams& p, cudaStream_t s);
+cudaError_t launch_ex_rows_bwd(int d, const ExParams& p, cudaStream_t s);
+cudaError_t launch_decode_rows(int d, const DecodeParams& p, cudaStream_t s);
+
+// MCS_OK when the current device is an sm_100 GPU
+mcs_status check_device();
+
 // process-wide test knobs (see mcs_debug_set in api.cu)
 int debug_flags();
 

@@ -72,7 +72,14 @@ typedef struct mcs_shape {
   float scale;
 } mcs_shape;
 
-typedef enum mcs_op { MCS_OP_GROUP = 0, MCS_OP_ANCHOR = 1, MCS_OP_SPARSE = 2, MCS_OP_DENSE = 3 } mcs_op;
+typedef enum mcs_op {
+  MCS_OP_GROUP = 0,
+  MCS_OP_ANCHOR = 1,
+  MCS_OP_SPARSE = 2,
+  MCS_OP_DENSE = 3,
+  MCS_OP_DENSE_EX = 4, /* sized by mcs_attn_workspace_bytes */
+  MCS_OP_DENSE_BWD = 5 /* sized by mcs_attn_workspace_bytes */
+} mcs_op;
 
 /* Bytes of workspace `op` needs for `shape` (>= MCS_STATUS_BYTES); 0 if the
  * shape is invalid or unsupported. */
@@ -220,6 +227,95 @@ mcs_status mcs_sparse_host(const mcs_shape* shape, const void* q_host, const voi
  */
 mcs_status mcs_dense(const mcs_shape* shape, const void* q, const void* k, const void* v, void* o, float* lse,
                      void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Attention with modified scores: mcs_dense_ex (forward), mcs_dense_bwd (its
+ * gradients), mcs_decode and mcs_decode_shared (one token per request over a
+ * cache). The pages have no counterpart to these calls.
+ *
+ * Layouts: q, o (and their gradients) bf16 [B, Nq, Hq, d]; k, v (and their
+ * gradients) bf16 [B, Nk, Hkv, d]; lse fp32 [B, Hq, Nq]. Query head h reads KV
+ * head h / (Hq / Hkv); Hkv divides Hq and Hq / Hkv <= 128. Query i stands at
+ * position p_i = i + Nk - Nq (the last query at the last key), key j at j.
+ *
+ *   x_ij = scale * q_i . k_j
+ *   s_ij = (cap > 0 ? cap * tanh(x_ij / cap) : x_ij) - slope_h * |p_i - j|
+ *   valid(i, j): (not causal, or j <= p_i, or j < prefix[b]), and
+ *                (no documents, or doc_q[b,i] == doc_k[b,j] >= 0)
+ *   o_i = sum_valid exp(s_ij - lse_i) v_j,  lse_i = log sum_valid exp(s_ij)
+ *
+ * A row without a valid key gets o = 0 and lse = -inf, and no gradient passes
+ * through it. A negative document id marks padding: a padded query's row is
+ * empty and a padded key is read by nobody, so the contents of padded rows of
+ * q, k, v and of the incoming gradient may be anything, NaN included; their
+ * gradients are 0. Every other row must be finite. Scores are fp32, P and dS
+ * are rounded to bf16 for their tensor-core products, sums are fp32.
+ * Outputs must not overlap inputs. Results are bit-identical from run to run.
+ */
+#define MCS_ATTN_CAUSAL 1
+
+typedef struct mcs_attn_shape {
+  int B, Hq, Hkv, Nq, Nk, d; /* d in {64, 128}; B*Nq*Hq and B*Nk*Hkv < 2^31 */
+  float scale;               /* <= 0 selects 1/sqrt(d) */
+  float cap;                 /* score cap; 0: none; negative or not finite: MCS_ERR_INVALID_ARG */
+  int flags;                 /* MCS_ATTN_CAUSAL or 0 */
+} mcs_attn_shape;
+
+/* Device arrays, each nullable; 4-byte aligned. Constants of the call: they get no gradient. */
+typedef struct mcs_attn_opts {
+  const float* slopes;   /* fp32 [Hq]: distance bias, finite */
+  const int32_t* prefix; /* int32 [B]: keys j < prefix[b] are valid to every query (needs MCS_ATTN_CAUSAL);
+                            values outside [0, Nk] act as the nearest bound */
+  const int32_t* doc_q;  /* int32 [B, Nq] and */
+  const int32_t* doc_k;  /* int32 [B, Nk]: document ids in any order, both given or both null (the same
+                            array may serve as both); at most 2^16 tiles of 128 keys, and of
+                            floor(128 / (Hq / Hkv)) queries, else MCS_ERR_UNSUPPORTED */
+} mcs_attn_opts;
+
+/* Bytes of workspace for op MCS_OP_DENSE_EX or MCS_OP_DENSE_BWD (with or without options); 0 if the
+ * shape is invalid or unsupported. */
+size_t mcs_attn_workspace_bytes(const mcs_attn_shape* shape, mcs_op op);
+
+/* Forward. opts nullable (no option); lse nullable. */
+mcs_status mcs_dense_ex(const mcs_attn_shape* shape, const mcs_attn_opts* opts, const void* q, const void* k,
+                        const void* v, void* o, float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Gradients of mcs_dense_ex: with the forward's inputs, its o and lse, and the
+ * gradient d_o of a scalar with respect to o, writes dq, dk and dv (summed over
+ * the query heads that share a KV head). No atomics: the sums' order is fixed.
+ */
+mcs_status mcs_dense_bwd(const mcs_attn_shape* shape, const mcs_attn_opts* opts, const void* q, const void* k,
+                         const void* v, const void* o, const float* lse, const void* d_o, void* dq, void* dk,
+                         void* dv, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * One token per request over a cache, with the scores of mcs_dense_ex (cap and
+ * distance bias). q, o: bf16 [B, Hq, d]; k, v: the caches, bf16 [B, C, Hkv, d];
+ * lens: int32 [B], the valid keys of each request (its newest token's key and
+ * value included); lse (nullable): fp32 [B, Hq]; slopes (nullable): fp32 [Hq].
+ * The query of request b stands at position P + lens[b] - 1. Cache rows from
+ * lens[b] on are never used and may hold anything. lens[b] == 0 with P == 0
+ * gives o = 0 and lse = -inf. A length outside [0, C] is recorded as
+ * MCS_ERR_BAD_INDEX in ws and acts as the nearest bound.
+ *
+ * mcs_decode needs P == 0. mcs_decode_shared adds a prefix of P >= 1 keys that
+ * all requests share, kp, vp: bf16 [P, Hkv, d] (key j at position j; cache key
+ * j at P + j), and reads it once for the whole batch.
+ */
+typedef struct mcs_decode_shape {
+  int B, Hq, Hkv, C, P, d; /* Hkv divides Hq, Hq / Hkv <= 128; B*C*Hkv, P*Hkv, B*Hq < 2^31; d in {64, 128} */
+  float scale, cap;        /* as in mcs_attn_shape */
+} mcs_decode_shape;
+
+size_t mcs_decode_workspace_bytes(const mcs_decode_shape* shape);
+
+mcs_status mcs_decode(const mcs_decode_shape* shape, const void* q, const void* k, const void* v,
+                      const int32_t* lens, const float* slopes, void* o, float* lse, void* ws, size_t ws_bytes,
+                      cudaStream_t stream);
+mcs_status mcs_decode_shared(const mcs_decode_shape* shape, const void* q, const void* kp, const void* vp,
+                             const void* k, const void* v, const int32_t* lens, const float* slopes, void* o,
+                             float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
  * Metadata offload / prefetch (aiwillknow analysis, step 5; paper Table 8):

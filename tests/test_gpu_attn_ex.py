@@ -1,0 +1,259 @@
+"""mcs_dense_ex and mcs_dense_bwd against the 64-bit reference, element by element within derived bounds."""
+import pytest
+
+import attn_ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mcs():
+    import free_sparse_attention_pddp_b200 as m
+
+    m.load()
+    return m
+
+
+def inputs(B, Hq, Hkv, Nq, Nk, d, seed=0, gain=2.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    return r(B, Nq, Hq, d) * gain, r(B, Nk, Hkv, d), r(B, Nk, Hkv, d), r(B, Nq, Hq, d)
+
+
+def guarded(t):
+    """An uninitialised-looking buffer of t's shape inside a larger one: (view, whole buffer)."""
+    pad = 512
+    whole = torch.full((t.numel() + 2 * pad,), 12345.0, dtype=t.dtype, device="cuda")
+    return whole[pad:pad + t.numel()].view(t.shape), whole
+
+
+def untouched(whole):
+    return bool((whole[:512] == whole[0]).all()) and bool((whole[-512:] == whole[0]).all()) and float(whole[0]) > 12000
+
+
+def run(mcs, shape, q, k, v, d_o=None, **opts):
+    """Forward and, with d_o, backward into guarded buffers."""
+    o, wo = guarded(q)
+    lse, wl = guarded(torch.empty(shape.B, shape.Hq, shape.Nq, device="cuda"))
+    ws = mcs.attn_workspace(shape, mcs.MCS_OP_DENSE_EX)
+    mcs.mcs_dense_ex(shape, q, k, v, o, lse, ws, **opts)
+    assert mcs.mcs_poll_status(ws)[0] == 0
+    got, guards = {"o": o, "lse": lse}, [wo, wl]
+    if d_o is not None:
+        (dq, w1), (dk, w2), (dv, w3) = guarded(q), guarded(k), guarded(v)
+        ws = mcs.attn_workspace(shape, mcs.MCS_OP_DENSE_BWD)
+        mcs.mcs_dense_bwd(shape, q, k, v, o, lse, d_o, dq, dk, dv, ws, **opts)
+        assert mcs.mcs_poll_status(ws)[0] == 0
+        got.update(dq=dq, dk=dk, dv=dv)
+        guards += [w1, w2, w3]
+    assert all(untouched(w) for w in guards)
+    return got
+
+
+def both(mcs, B, Hq, Hkv, Nq, Nk, d, cap=0.0, scale=0.0, slopes=None, causal=False, prefix=None, doc_q=None,
+         doc_k=None, seed=0, gain=2.0, tensors=None):
+    q, k, v, d_o = tensors or inputs(B, Hq, Hkv, Nq, Nk, d, seed, gain)
+    dev = lambda x, t: None if x is None else torch.as_tensor(x, dtype=t).cuda().contiguous()  # noqa: E731
+    slopes, prefix = dev(slopes, torch.float32), dev(prefix, torch.int32)
+    doc_q, doc_k = dev(doc_q, torch.int32), dev(doc_k, torch.int32)
+    shape = mcs.AttnShape(B, Hq, Hkv, Nq, Nk, d, scale=scale, cap=cap, causal=causal)
+    got = run(mcs, shape, q, k, v, d_o, slopes=slopes, prefix=prefix, doc_q=doc_q, doc_k=doc_k)
+    valid = attn_ref.valid_mask(B, Nq, Nk, causal, prefix, doc_q, doc_k, "cuda")
+    want = attn_ref.attn(q, k, v, d_o, scale=scale or None, cap=cap, slopes=slopes, valid=valid)
+    for name in ("lse", "o", "dv", "dk", "dq"):
+        attn_ref.check(got[name], want[name], name)
+    return got
+
+
+SIZES = [  # B, Hq, Hkv, Nq, Nk
+    (1, 1, 1, 1, 1), (2, 3, 3, 1, 130), (1, 2, 1, 127, 127), (1, 2, 2, 128, 128), (2, 4, 2, 129, 129),
+    (1, 8, 1, 70, 257), (1, 6, 2, 300, 640), (3, 5, 1, 33, 200), (1, 12, 1, 45, 129), (1, 128, 1, 3, 140),
+    (2, 2, 2, 513, 385), (1, 4, 4, 600, 600),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_plain(mcs, size, d):
+    both(mcs, *size, d, seed=sum(size))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_causal_cap_and_bias(mcs, size, d):
+    """Nq > Nk among the sizes: the first rows see nothing."""
+    Hq = size[1]
+    both(mcs, *size, d, cap=15.0, slopes=[2.0 ** (-8 * (h + 1) / Hq) for h in range(Hq)], causal=True, seed=sum(size))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,gain", [(50.0, 2.0), (5.0, 8.0), (0.5, 4.0), (1000.0, 4.0)])
+def test_caps_from_nearly_linear_to_saturated(mcs, cap, gain, d):
+    both(mcs, 1, 4, 2, 200, 333, d, cap=cap, gain=gain, seed=5)
+
+
+@pytest.mark.parametrize("slopes", [[0.0, 3.0], [-0.01, 0.2]])
+def test_bias_without_a_mask_is_symmetric_in_distance(mcs, slopes):
+    both(mcs, 1, 2, 1, 150, 290, 64, slopes=slopes, seed=6)
+
+
+@pytest.mark.parametrize("Nq,Nk,prefix", [(257, 257, [0, 100, 257]), (40, 600, [561, 599, 10000]), (300, 200, [-7, 1, 128]),
+                                          (1, 1, [0, 1, 2])])
+def test_prefix(mcs, Nq, Nk, prefix):
+    both(mcs, 3, 4, 2, Nq, Nk, 128, causal=True, prefix=prefix, cap=20.0, slopes=[.1, .2, .3, .4], seed=Nq)
+
+
+def packed_ids(B, N, mean, seed, pad=0, shuffle=False):
+    g = torch.Generator().manual_seed(seed)
+    ids = (torch.rand(B, N, generator=g) < 1.0 / mean).cumsum(1)
+    if shuffle:  # ids in no order: documents that interleave
+        ids = torch.randint(0, max(2, N // mean), (B, N), generator=g)
+    for b in range(B):
+        n = pad * (b + 1) // B
+        if n:
+            ids[b, N - n:] = -1
+    return ids.int()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [1, 3, 8])
+@pytest.mark.parametrize("mean,pad,shuffle,causal", [(40, 0, False, False), (200, 90, False, True), (3000, 130, False, False),
+                                                     (150, 20, True, True)])
+def test_documents(mcs, mean, pad, shuffle, causal, g, d):
+    ids = packed_ids(2, 700, mean, mean + g, pad, shuffle)
+    both(mcs, 2, 2 * g, 2, 700, 700, d, causal=causal, doc_q=ids, doc_k=ids, cap=30.0 if g == 3 else 0.0, seed=g)
+
+
+def test_documents_of_queries_and_keys_differ(mcs):
+    """Cross-attention: a query document without keys, a key document without queries, large and negative ids."""
+    dq = torch.full((1, 260), 7)
+    dk = torch.full((1, 500), 7)
+    dq[0, 100:180], dq[0, 200:] = 2 ** 31 - 1, -2 ** 31
+    dk[0, 250:300], dk[0, 300:] = 0, -5
+    r = both(mcs, 1, 4, 2, 260, 500, 64, doc_q=dq, doc_k=dk, prefix=[3], causal=True, seed=9)
+    assert torch.isneginf(r["lse"][0, :, 100:180]).all() and (r["o"][0, 100:180] == 0).all()
+
+
+def test_nothing_is_valid(mcs):
+    r = both(mcs, 2, 2, 1, 140, 300, 128, doc_q=torch.zeros(2, 140), doc_k=torch.ones(2, 300), seed=3)
+    assert torch.isneginf(r["lse"]).all() and all((r[n] == 0).all() for n in ("o", "dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [1, 5])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_padded_rows_may_hold_anything(mcs, bad, g, d):
+    ids = packed_ids(2, 420, 150, 4, pad=165)
+    ids[0, 10:13] = -1  # and padding inside a row
+    q, k, v, d_o = inputs(2, 2 * g, 2, 420, 420, d, seed=11)
+    for t in (q, k, v, d_o):
+        t[ids.cuda() < 0] = bad
+    r = both(mcs, 2, 2 * g, 2, 420, 420, d, doc_q=ids, doc_k=ids, cap=25.0, tensors=(q, k, v, d_o))
+    pad = ids.cuda() < 0
+    assert all((r[n][pad] == 0).all() for n in ("o", "dq", "dk", "dv"))
+
+
+def test_a_batch_does_not_read_its_neighbour(mcs):
+    """The last key tile of request 0 is ragged and request 1 starts with NaN."""
+    q, k, v, d_o = inputs(2, 2, 2, 200, 200, 128, seed=12)
+    for t in (q, k, v, d_o):
+        t[1] = float("nan")
+    shape = mcs.AttnShape(2, 2, 2, 200, 200, 128)
+    r = run(mcs, shape, q, k, v, d_o)
+    want = attn_ref.attn(q[:1], k[:1], v[:1], d_o[:1])
+    for name in want:
+        attn_ref.check(r[name][:1], want[name], name)
+
+
+def test_scale_and_large_scores(mcs):
+    both(mcs, 1, 2, 2, 100, 300, 64, scale=1.0, gain=1.0, seed=13)
+    both(mcs, 1, 2, 2, 100, 300, 64, scale=1e-4, gain=1.0, seed=14)
+
+
+def test_a_row_of_equal_scores(mcs):
+    """q = 0: every probability is 1 / n."""
+    q, k, v, d_o = inputs(1, 2, 1, 130, 1000, 64, seed=15)
+    both(mcs, 1, 2, 1, 130, 1000, 64, causal=True, tensors=(torch.zeros_like(q), k, v, d_o))
+
+
+def test_long_rows(mcs):
+    """Few queries over many keys, and many queries over few keys (shared heads)."""
+    both(mcs, 1, 2, 1, 5, 20011, 128, causal=True, prefix=[77], seed=16)
+    both(mcs, 1, 4, 1, 3001, 40, 64, slopes=[.01, .02, .03, .04], seed=17)
+    both(mcs, 1, 2, 2, 2050, 2050, 128, causal=True, cap=30.0, seed=18)
+
+
+def test_runs_repeat_bit_for_bit(mcs):
+    q, k, v, d_o = inputs(2, 6, 2, 500, 500, 128, seed=19)
+    ids = packed_ids(2, 500, 120, 2, 40).cuda()
+    shape = mcs.AttnShape(2, 6, 2, 500, 500, 128, cap=30.0, causal=True)
+    a, b = (run(mcs, shape, q, k, v, d_o, doc_q=ids, doc_k=ids) for _ in range(2))
+    for n in a:
+        assert torch.equal(a[n].view(torch.uint8), b[n].view(torch.uint8)), n
+
+
+def test_no_lse_and_dirty_workspace(mcs):
+    """lse is optional, and a workspace that held another call's data (its status block apart) gives the same."""
+    q, k, v, d_o = inputs(1, 4, 2, 300, 300, 64, seed=20)
+    ids = packed_ids(1, 300, 90, 3, 33).cuda()
+    shape = mcs.AttnShape(1, 4, 2, 300, 300, 64)
+    want = run(mcs, shape, q, k, v, d_o, doc_q=ids, doc_k=ids)
+    ws = mcs.attn_workspace(shape, mcs.MCS_OP_DENSE_EX)
+    wb = mcs.attn_workspace(shape, mcs.MCS_OP_DENSE_BWD)
+    ws[256:], wb[256:] = 0xff, 0xff
+    o, dq, dk, dv = (torch.empty_like(t) for t in (q, q, k, v))
+    mcs.mcs_dense_ex(shape, q, k, v, o, None, ws, doc_q=ids, doc_k=ids)
+    mcs.mcs_dense_bwd(shape, q, k, v, o, want["lse"], d_o, dq, dk, dv, wb, doc_q=ids, doc_k=ids)
+    for n, t in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv)):
+        assert torch.equal(t, want[n]), n
+    assert mcs.mcs_poll_status(ws)[0] == 0 and mcs.mcs_poll_status(wb)[0] == 0
+
+
+def test_streams_and_graphs(mcs):
+    """On a side stream, and captured once and replayed on new contents of the same buffers."""
+    shape = mcs.AttnShape(2, 4, 2, 260, 260, 64, cap=30.0, causal=True)
+    q, k, v, d_o = inputs(2, 4, 2, 260, 260, 64, seed=21)
+    ids = packed_ids(2, 260, 80, 5, 30).cuda()
+    opts = dict(doc_q=ids, doc_k=ids)
+    first = run(mcs, shape, q, k, v, d_o, **opts)
+    o, lse = torch.empty_like(q), torch.empty(2, 4, 260, device="cuda")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws, wb = (mcs.attn_workspace(shape, op) for op in (mcs.MCS_OP_DENSE_EX, mcs.MCS_OP_DENSE_BWD))
+
+    def step():
+        mcs.mcs_dense_ex(shape, q, k, v, o, lse, ws, **opts)
+        mcs.mcs_dense_bwd(shape, q, k, v, o, lse, d_o, dq, dk, dv, wb, **opts)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    got = dict(o=o, lse=lse, dq=dq, dk=dk, dv=dv)
+    assert all(torch.equal(got[n], first[n]) for n in got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    q2, k2, v2, d2 = inputs(2, 4, 2, 260, 260, 64, seed=22)
+    want = run(mcs, shape, q2, k2, v2, d2, **opts)
+    for t, n in ((q, q2), (k, k2), (v, v2), (d_o, d2)):
+        t.copy_(n)
+    for t in got.values():
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[n], want[n]) for n in got)
+
+
+def test_one_pass_equals_mcs_dense(mcs):
+    """Without options the operator is the framework's dense attention."""
+    q, k, v, _ = inputs(1, 3, 3, 400, 400, 128, seed=23)
+    got = run(mcs, mcs.AttnShape(1, 3, 3, 400, 400, 128), q, k, v)
+    s = mcs.Shape(1, 3, 400, 128)
+    o, lse = torch.empty_like(q), torch.empty(1, 3, 400, device="cuda")
+    mcs.mcs_dense(s, q, k, v, o, lse, mcs.workspace(s, mcs.MCS_OP_DENSE))
+    want = attn_ref.attn(q, k, v)
+    for n, t in (("o", o), ("lse", lse)):  # both lie within the same bound of the exact value
+        attn_ref.check(got[n], want[n], n)
+        attn_ref.check(t, want[n], n)
