@@ -23,7 +23,6 @@ std::atomic<long long> g_launches{0};
 cudaEvent_t const* g_chunk_events = nullptr;  // measurement hook: events around the anchor's chunk launches
 int g_chunk_event_count = 0;
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;    // 2 s per bounded device wait
 constexpr size_t kMassBudget = size_t(2) << 30;      // bytes of mass matrix per head chunk
 // Half-width of the fp32-mass uncertainty band around the K-th largest mass,
 // 2^-11 relative. A group's fp32 mass carries at most ~1e-4 relative error
@@ -135,6 +134,21 @@ mcs_status check_device() {
   if (cudaGetDevice(&dev) != cudaSuccess) return MCS_ERR_CUDA;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return MCS_ERR_CUDA;
   return major == 10 ? MCS_OK : MCS_ERR_UNSUPPORTED;
+}
+
+mcs_status tiles_map(CUtensorMap* m, const void* base, int B, int N, int H, int d, int heads, int tokens) {
+  const mcs_status st = encode_init();
+  if (st != MCS_OK) return st;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(N),
+                        static_cast<cuuint64_t>(B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(H) * d * 2,
+                           static_cast<cuuint64_t>(N) * H * d * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MCS_OK : MCS_ERR_CUDA;
 }
 
 int debug_flags() { return g_debug_flags; }

@@ -2,6 +2,8 @@
 // include/mcs.h): host-side validation, workspace layout and launches.
 #include <math.h>
 
+#include <algorithm>
+
 #include "mcs_internal.h"
 
 using namespace mcs;
@@ -67,6 +69,80 @@ ExParams ex_params(const mcs_attn_shape* s, const mcs_attn_opts* o) {
   return p;
 }
 
+// How the forward fills the GPU: tiles, key splits and the order of work.
+struct FwdPlan {
+  int tpt, Tq, Tk, single, nsplit, parts, chunk;
+};
+
+constexpr int kSms = 148;
+
+// One query tile and at least four key tiles: both slots of a CTA take that
+// tile. While a wave has room, the keys are split into parts of at least four
+// tiles per slot, joined by a second launch.
+FwdPlan fwd_plan(int B, int Hkv, int g, int Nq, int Nk, int d) {
+  FwdPlan f;
+  f.tpt = 128 / g;
+  f.Tq = (Nq + f.tpt - 1) / f.tpt;
+  f.Tk = (Nk + 127) / 128;
+  f.single = f.Tq == 1 && f.Tk >= 4;
+  const long long ctas = static_cast<long long>(B) * Hkv * (f.single ? 1 : (f.Tq + 1) / 2);
+  f.nsplit = 1;
+  if (2 * ctas <= kSms) {
+    const long long most = f.Tk / (f.single ? 8 : 4);
+    f.nsplit = static_cast<int>(std::max(1ll, std::min(kSms / ctas, most)));
+  }
+  f.parts = f.nsplit * (f.single ? 2 : 1);
+  // K and V of a chunk's heads take half of the 126 MB L2 at most
+  const size_t head = static_cast<size_t>(Nk) * d * 4;
+  const long long fit = static_cast<long long>((size_t(64) << 20) / head);
+  f.chunk = static_cast<int>(std::max(1ll, std::min<long long>(fit, static_cast<long long>(B) * Hkv)));
+  return f;
+}
+
+// workspace: status | document tiles | partials of the key splits
+struct FwdWs {
+  size_t k_ids, k_ranges, q_ranges, part_lse, part_o, total;
+};
+
+FwdWs fwd_layout(const FwdPlan& f, int B, int Hkv, int d) {
+  FwdWs w;
+  size_t off = MCS_STATUS_BYTES;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  w.k_ids = take(static_cast<size_t>(B) * f.Tk * 512);
+  w.k_ranges = take(static_cast<size_t>(B) * f.Tk * 16);
+  w.q_ranges = take(static_cast<size_t>(B) * f.Tq * 16);
+  const size_t rows = f.parts > 1 ? static_cast<size_t>(f.parts) * B * Hkv * f.Tq * 128 : 0;
+  w.part_lse = take(rows * 4);
+  w.part_o = take(rows * d * 4);
+  w.total = off;
+  return w;
+}
+
+ExTile tile_params(const ExParams& p, const FwdPlan& f, int d) {
+  ExTile t{};
+  t.B = p.B; t.Hq = p.Hq; t.Hkv = p.Hkv; t.g = p.g; t.tpt = f.tpt; t.Nq = p.Nq; t.Nk = p.Nk;
+  t.Tq = f.Tq; t.Tk = f.Tk;
+  t.nsplit = f.nsplit; t.single = f.single; t.chunk = f.chunk;
+  t.scale = p.scale;
+  t.mul = static_cast<float>((p.cap > 0.f ? p.cap : p.scale) * 1.4426950408889634074);
+  t.cap_k = p.cap > 0.f ? p.scale / p.cap : 0.f;
+  t.causal = p.causal;
+  t.slopes = p.slopes;
+  t.prefix = p.prefix;
+  t.doc_q = p.doc_q;
+  t.doc_k = p.doc_k;
+  t.status = p.status;
+  t.wait_limit_ns = kWaitLimitNs;
+  t.debug_flags = debug_flags();
+  return t;
+}
+
+mcs_status ok_or_cuda(cudaError_t e) { return e == cudaSuccess ? MCS_OK : MCS_ERR_CUDA; }
+
 mcs_status check_decode(const mcs_decode_shape* s) {
   if (!s || s->B < 1 || s->C < 1 || s->P < 0) return MCS_ERR_INVALID_ARG;
   const mcs_status st = check_heads(s->Hq, s->Hkv, s->d, s->scale, s->cap);
@@ -110,7 +186,8 @@ extern "C" {
 
 size_t mcs_attn_workspace_bytes(const mcs_attn_shape* s, mcs_op op) {
   if (check_attn(s) != MCS_OK) return 0;
-  if (op == MCS_OP_DENSE_EX) return MCS_STATUS_BYTES;
+  if (op == MCS_OP_DENSE_EX)
+    return fwd_layout(fwd_plan(s->B, s->Hkv, s->Hq / s->Hkv, s->Nq, s->Nk, s->d), s->B, s->Hkv, s->d).total;
   if (op == MCS_OP_DENSE_BWD) return MCS_STATUS_BYTES + align256(static_cast<size_t>(s->B) * s->Hq * s->Nq * 4);
   return 0;
 }
@@ -127,13 +204,33 @@ mcs_status mcs_dense_ex(const mcs_attn_shape* s, const mcs_attn_opts* opts, cons
   if (ws_bytes < mcs_attn_workspace_bytes(s, MCS_OP_DENSE_EX)) return MCS_ERR_INVALID_ARG;
   if ((st = check_device()) != MCS_OK) return st;
   ExParams p = ex_params(s, opts);
-  p.q = static_cast<const uint16_t*>(q);
-  p.k = static_cast<const uint16_t*>(k);
-  p.v = static_cast<const uint16_t*>(v);
-  p.o = static_cast<uint16_t*>(o);
-  p.lse = lse;
   p.status = static_cast<int*>(ws);
-  return launch_ex_rows_fwd(s->d, p, stream) == cudaSuccess ? MCS_OK : MCS_ERR_CUDA;
+  const FwdPlan f = fwd_plan(p.B, p.Hkv, p.g, p.Nq, p.Nk, s->d);
+  const FwdWs w = fwd_layout(f, p.B, p.Hkv, s->d);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  CUtensorMap tq, tk, tv;
+  if (tiles_map(&tq, q, p.B, p.Nq, p.Hq, s->d, p.g, f.tpt) != MCS_OK ||
+      tiles_map(&tk, k, p.B, p.Nk, p.Hkv, s->d, 1, 128) != MCS_OK ||
+      tiles_map(&tv, v, p.B, p.Nk, p.Hkv, s->d, 1, 128) != MCS_OK)
+    return MCS_ERR_CUDA;
+  ExTile t = tile_params(p, f, s->d);
+  t.o = static_cast<uint16_t*>(o);
+  t.lse = lse;
+  if (p.doc_q) {
+    int* ids = reinterpret_cast<int*>(base + w.k_ids);
+    int4* kr = reinterpret_cast<int4*>(base + w.k_ranges);
+    int4* qr = reinterpret_cast<int4*>(base + w.q_ranges);
+    if (launch_ex_doc_tiles(t, ids, kr, nullptr, qr, stream) != cudaSuccess) return MCS_ERR_CUDA;
+    t.k_ids = ids;
+    t.k_ranges = kr;
+    t.q_ranges = qr;
+  }
+  if (f.parts > 1) {
+    t.part_lse = reinterpret_cast<float*>(base + w.part_lse);
+    t.part_o = reinterpret_cast<float*>(base + w.part_o);
+  }
+  if (launch_ex_fwd(s->d, &tq, &tk, &tv, t, stream) != cudaSuccess) return MCS_ERR_CUDA;
+  return f.parts > 1 ? ok_or_cuda(launch_ex_combine(s->d, t, f.parts, stream)) : MCS_OK;
 }
 
 mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, const void* q, const void* k,

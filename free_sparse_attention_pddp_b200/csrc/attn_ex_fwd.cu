@@ -1,0 +1,603 @@
+// Attention with modified scores, forward (mcs_dense_ex), and the shared
+// prefix of mcs_decode_shared: online softmax over key tiles of 128, both
+// products on the tensor cores (tcgen05, operands by TMA, accumulators in
+// TMEM).
+//
+// A CTA has two slots, each with a 128-row query tile, a score tile S, an
+// output accumulator O and a softmax warpgroup (one thread per row). The UMMA
+// warp alternates between them,
+//   S_0(i) = Q_0 K^T | O_1 += P_1(i-1) V | S_1(i) = Q_1 K^T | O_0 += P_0(i) V,
+// so one slot's softmax runs while the tensor pipe computes the other's
+// products, as in attn_pair.cu. Two ways to fill the slots:
+//   pair    two consecutive query tiles that share every key tile;
+//   single  one query tile whose even key tiles go to slot 0 and odd ones to
+//           slot 1 (few rows over many keys); the halves are joined by
+//           ex_combine like any other split of the keys.
+//
+// TMEM (512 columns): S_0 | S_1 (128 each) | O_0 | O_1 (D each). P_t (bf16
+// pairs) overwrites the first 64 columns of S_t and is the TS-form A operand of
+// O_t += P_t V.
+//
+// Masks: a key tile is skipped, whole, or partial. Causal and prefix masks
+// bound the tile range and give each row a key limit; a document mask skips
+// tiles whose range of ids cannot meet the query tiles' (bitmap built at the
+// start), and compares ids element by element in partial tiles only.
+//
+// Threads (384): warp 0 issues the UMMAs, warp 1 the TMA loads, warp 2 clears
+// the V rows of padded keys (document masks), warps 4-7 and 8-11 run the
+// softmax of slot 0 and 1. setmaxnreg moves registers to the softmax.
+#include "attn_ex.cuh"
+
+namespace mcs {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168;
+constexpr int kLowRegs = 64;
+constexpr int kSoftRegs = 216;
+static_assert(128 * kLowRegs + 256 * kSoftRegs <= kThreads * kLaunchRegs, "register split");
+// A row's running maximum moves only when a tile exceeds it by this much in
+// log2 units (a factor 16): probabilities stay below 16, where bf16 is as exact
+// as below 1, and most tiles leave O alone.
+constexpr float kRescale = 4.0f;
+
+template <int D>
+struct FwdCfg {
+  static constexpr int KB = D / 64;
+  static constexpr uint32_t TILE = 128u * D * 2u;
+  static constexpr int NS = D == 128 ? 2 : 4;  // K/V stages
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = 2 * TILE;
+  static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_V + NS * TILE;
+  // q_full, k_full[NS], v_full[NS], v_ok[NS], kv_empty[NS], s_full[2], p_full[2], p_empty[2], drain
+  static constexpr uint32_t NBAR = 1 + 4 * NS + 2 + 2 + 2 + 1;
+  static constexpr uint32_t OFF_BITS = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;
+  static constexpr uint32_t SMEM = OFF_BITS + 1024;  // and 4 bytes for each 32 key tiles under a document mask
+};
+
+}  // namespace
+
+template <int D, bool MOD>
+__global__ void __launch_bounds__(kThreads, 1)
+    ex_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
+  using C = FwdCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* k_full = q_full + 1;           // [stage]
+  uint64_t* v_full = k_full + C::NS;       // [stage]
+  uint64_t* v_ok = v_full + C::NS;         // [stage]: V's padded rows are clear (document masks)
+  uint64_t* kv_empty = v_ok + C::NS;       // [stage]
+  uint64_t* s_full = kv_empty + C::NS;     // [slot]: S(i) computed
+  uint64_t* p_full = s_full + 2;           // [slot]: P(i) written (and O rescaled)
+  uint64_t* p_empty = p_full + 2;          // [slot]: O += P(i) V done
+  uint64_t* drain_bar = p_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* count = reinterpret_cast<int*>(tmem_slot + 2);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const bool single = p.single;
+  const int per = single ? 1 : 2;  // query tiles of a CTA
+  const int groups = (p.Tq + per - 1) / per;
+  // Work order: splits of one job side by side; then, for causal masks, the
+  // heads of a chunk (whose K and V fit L2 together) with the longest query
+  // tiles first, else the query tiles of one head.
+  int u = blockIdx.x;
+  const int split = u % p.nsplit;
+  u /= p.nsplit;
+  int job, bh;
+  const int BH = p.B * p.Hkv;
+  if (p.causal) {
+    const int per_chunk = p.chunk * groups;
+    const int ch = u / per_chunk, in = u % per_chunk;
+    const int heads = min(p.chunk, BH - ch * p.chunk);
+    bh = ch * p.chunk + in % heads;
+    job = groups - 1 - in / heads;
+  } else {
+    job = u % groups;
+    bh = u / groups;
+  }
+  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int qt0 = job * per;
+  const bool has1 = !single && qt0 + 1 < p.Tq;  // slot 1 has a query tile of its own
+  const int prefix = p.prefix ? p.prefix[b] : 0;
+  // keys below limit(position) pass the causal and prefix masks
+  auto limit = [&](int pos) { return p.causal ? min(p.Nk, max(max(pos + 1, prefix), 0)) : p.Nk; };
+  auto last_tok = [&](int qt) { return min(p.Nq, (qt + 1) * p.tpt) - 1; };
+  const int off = p.Nk - p.Nq;  // position of token 0
+  const int T = (limit(off + last_tok(has1 ? qt0 + 1 : qt0)) + 127) >> 7;
+  const int lo = static_cast<int>(static_cast<long long>(split) * T / p.nsplit);
+  const int hi = static_cast<int>(static_cast<long long>(split + 1) * T / p.nsplit);
+  const bool docs = p.k_ranges != nullptr;
+  const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
+  int4 r0 = none, r1 = none;
+  if (docs) {
+    r0 = p.q_ranges[b * p.Tq + qt0];
+    if (has1) r1 = p.q_ranges[b * p.Tq + qt0 + 1];
+  }
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_ok[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_full[t], 128);
+      mbar_init(&p_empty[t], 1);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    *count = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  // rows that no load writes (g does not divide 128) stay zero
+  const int rt = p.tpt * p.g;
+  if (rt < 128) {
+    for (int i = threadIdx.x; i < per * C::KB * (128 - rt) * 8; i += kThreads) {
+      const int c = i & 7, row = rt + (i >> 3) % (128 - rt), blk = (i >> 3) / (128 - rt);
+      *reinterpret_cast<uint4*>(sQ + blk * 16384 + row * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int n = hi - lo;  // key tiles of this CTA
+  if (docs) n = build_tile_bits(bits, count, p.k_ranges + static_cast<size_t>(b) * p.Tk, lo, hi, r0, r1);
+  const TileIter first{docs ? bits : nullptr, lo, lo};
+  // key tiles of the slots, in the order of the CTA's list
+  const int n0 = single ? (n + 1) >> 1 : n;
+  const int n1 = single ? n >> 1 : (has1 ? n : 0);
+  const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
+  int issued = 0;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
+    if (warp == 0) {
+      // ---------------------------------------------------------------- UMMA issuer
+      if (lane == 0 && n > 0) {
+        constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t IDESC_O = idesc_bf16_f32(128, D, false, true);
+        const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dV = sdesc_sw128(smem_u32(sV), 16384, 1024);
+        uint64_t* v_bar = docs ? v_ok : v_full;
+        // S_t = Q_t K^T with the CTA's list entry j
+        auto issue_s = [&](int t, int j) {
+          const uint64_t dQt = sdesc_advance(dQ, single ? 0 : t * C::TILE);
+          const uint64_t dKs = sdesc_advance(dK, (j % C::NS) * C::TILE);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
+            umma_bf16_ss(tmem + t * 128, sdesc_advance(dQt, o), sdesc_advance(dKs, o), IDESC_S, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[t]);
+        };
+        auto issue_o = [&](int t, int i, int j) {
+          const uint64_t dVs = sdesc_advance(dV, (j % C::NS) * C::TILE);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8, sdesc_advance(dVs, kk * 2048), IDESC_O,
+                         (i > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&p_empty[t]);
+        };
+        auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
+        bool ok = wait(q_full, 0);
+        // UMMAs run in order, so S_t(i + 1) overwrites P_t(i) only after the product that reads it
+        for (int i = 0; ok && i <= n0; ++i) {
+          const int j0 = single ? 2 * i : i;            // list entry of slot 0's step i
+          const int jp = single ? 2 * i - 1 : i - 1;    // of slot 1's step i - 1
+          const int j1 = single ? 2 * i + 1 : i;        // of slot 1's step i
+          if (i < n0) {
+            if (!wait(&k_full[j0 % C::NS], j0 / C::NS)) break;
+            tc_fence_after();
+            issue_s(0, j0);
+          }
+          if (i >= 1 && i - 1 < n1) {
+            if (single && !wait(&v_bar[jp % C::NS], jp / C::NS)) break;
+            if (!wait(&p_full[1], i - 1)) break;
+            tc_fence_after();
+            issue_o(1, i - 1, jp);
+            umma_commit(&kv_empty[jp % C::NS]);
+          }
+          if (i < n1) {
+            if (single && !wait(&k_full[j1 % C::NS], j1 / C::NS)) break;
+            tc_fence_after();
+            issue_s(1, j1);
+          }
+          if (i < n0) {
+            if (!wait(&v_bar[j0 % C::NS], j0 / C::NS)) break;
+            if (!wait(&p_full[0], i)) break;
+            tc_fence_after();
+            issue_o(0, i, j0);
+            if (!has1) umma_commit(&kv_empty[j0 % C::NS]);
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- TMA producer
+      if (lane == 0 && n > 0) {
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+        const int tiles = has1 ? 2 : 1;
+        mbar_arrive_expect_tx(q_full, tiles * C::KB * rt * 128);
+        for (int t = 0; t < tiles; ++t)
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_4d(&tm_q, q_full, sQ + t * C::TILE + kb * 16384, kb * 64, hk * p.g, (qt0 + t) * p.tpt, b);
+        TileIter it = first;
+        for (int j = 0; j < n; ++j) {
+          const int s = j % C::NS;
+          if (j >= C::NS && !mbar_wait(&kv_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+          const int kt = it.next();
+          if ((p.debug_flags & 1) && j == 0) continue;  // test knob: never deliver tile 0
+          mbar_arrive_expect_tx(&k_full[s], C::TILE);
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_4d(&tm_k, &k_full[s], sK + s * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
+          mbar_arrive_expect_tx(&v_full[s], C::TILE);
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_4d(&tm_v, &v_full[s], sV + s * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
+          issued = j + 1;
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2 && docs) {
+      // ---------------------------------------------------------------- padded keys
+      TileIter it = first;
+      for (int j = 0; j < n; ++j) {
+        const int s = j % C::NS;
+        if (!mbar_wait_warp(&v_full[s], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+        const int kt = it.next();
+        if (p.k_ranges[static_cast<size_t>(b) * p.Tk + kt].z) {
+          zero_padded_rows<C::KB>(sV + s * C::TILE, p.k_ids + (static_cast<size_t>(b) * p.Tk + kt) * 128);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_ok[s]);
+      }
+      __syncwarp();
+    }
+    named_barrier_sync<1, kThreads>();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
+  } else {
+    // ---------------------------------------------------------------- softmax + epilogue of slot t
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    const int t = (warp - 4) >> 2;
+    const int wq = warp & 3;  // TMEM lane quarter this warp may access
+    const int row = wq * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_addr + t * 128;
+    const uint32_t tO = tmem + lane_addr + 256 + t * D;
+    const int nt = t == 0 ? n0 : n1;
+    const int qt = single ? qt0 : qt0 + t;
+    const int tok = qt * p.tpt + row / p.g;
+    const int head = hk * p.g + row % p.g;
+    const bool row_valid = row < rt && tok < p.Nq && (t == 0 || single || has1);
+    const int pos = p.lens ? p.P + min(max(row_valid ? p.lens[tok] : 0, 0), p.C) - 1 : off + tok;
+    const int lim = limit(pos);
+    const int lim_all = limit(off + qt * p.tpt);  // keys that every row of the tile sees
+    const int4 mine = t == 0 || single ? r0 : r1;
+    int my_doc = docs && row_valid ? p.doc_q[static_cast<size_t>(b) * p.Nq + tok] : -2;
+    if (my_doc < 0) my_doc = -2;  // a padded query matches no key
+    const float slope = MOD && p.slopes && row_valid ? p.slopes[head] * kLog2e : 0.f;
+    const bool bias = MOD && p.slopes != nullptr;
+    const float mul = bias ? 1.f : p.mul;  // what turns a transformed score into log2 units
+    const uint64_t mul2 = f2_pack(mul, mul);
+    TileIter it = first;
+    if (single && t == 1 && nt > 0) it.next();
+    float m = -CUDART_INF_F;  // running max, log2 units
+    float l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < nt; ++i) {
+      const int kt = it.next();
+      if (single && i + 1 < nt) it.next();
+      if (!mbar_wait_warp(&s_full[t], i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float sv[128];
+#pragma unroll
+      for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(tS + c4 * 32, sv + c4 * 32);
+      tmem_wait_ld();
+      if (MOD) {
+        if (p.cap_k != 0.f) {
+#pragma unroll
+          for (int c4 = 0; c4 < 4; ++c4) tanh_scaled<32>(sv + c4 * 32, p.cap_k);
+        }
+        if (bias) add_bias<128>(sv, p.mul, slope, static_cast<float>(pos - kt * 128), 1.f);
+      }
+      const int4* ids = nullptr;
+      bool partial = (kt + 1) * 128 > lim_all;
+      if (docs) {
+        const size_t at = static_cast<size_t>(b) * p.Tk + kt;
+        if (!docs_same(mine, p.k_ranges[at])) {
+          partial = true;
+          ids = reinterpret_cast<const int4*>(p.k_ids + at * 128);
+        }
+      }
+      if (partial) {
+        const int valid = lim - kt * 128;
+        if (ids) {
+#pragma unroll
+          for (int c = 0; c < 128; c += 4) {
+            const int4 k4 = __ldg(ids + (c >> 2));  // padded keys hold -1, which no query's id equals
+            sv[c] = (c < valid && k4.x == my_doc) ? sv[c] : -CUDART_INF_F;
+            sv[c + 1] = (c + 1 < valid && k4.y == my_doc) ? sv[c + 1] : -CUDART_INF_F;
+            sv[c + 2] = (c + 2 < valid && k4.z == my_doc) ? sv[c + 2] : -CUDART_INF_F;
+            sv[c + 3] = (c + 3 < valid && k4.w == my_doc) ? sv[c + 3] : -CUDART_INF_F;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) sv[c] = c < valid ? sv[c] : -CUDART_INF_F;
+        }
+      }
+      float mc[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float a = sv[k * 16];
+#pragma unroll
+        for (int e = 1; e < 15; e += 2) a = fmax3(a, sv[k * 16 + e], sv[k * 16 + e + 1]);
+        mc[k] = fmaxf(a, sv[k * 16 + 15]);
+      }
+      const float mx =
+          fmaxf(fmax3(fmaxf(mc[0], mc[1]), mc[2], mc[3]), fmax3(fmaxf(mc[4], mc[5]), mc[6], mc[7])) * mul;
+      // a row that has seen no valid key keeps m = -inf, l = 0 and P = 0
+      const bool need = i == 0 ? mx > m : mx > m + kRescale;
+      const bool rescale = i > 0 && __any_sync(0xffffffffu, need);
+      float alpha = 1.f;
+      if (need) {
+        alpha = fast_exp2(m - mx);
+        m = mx;
+      }
+      const float ms = m == -CUDART_INF_F ? 0.f : m;
+      const uint64_t negm = f2_pack(-ms, -ms);
+#pragma unroll
+      for (int q = 0; q < 64; ++q) {
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(sv[2 * q], sv[2 * q + 1]), mul2, negm), x0, x1);
+        sv[2 * q] = fast_exp2(x0);
+        sv[2 * q + 1] = fast_exp2(x1);
+      }
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(sv[64 * h2 + 2 * c], sv[64 * h2 + 2 * c + 1]);
+        tmem_st32u(tS + h2 * 32, pk);
+      }
+      uint64_t acc[32];
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        acc[q] = f2_add(f2_pack(sv[2 * q], sv[2 * q + 1]), f2_pack(sv[2 * q + 64], sv[2 * q + 65]));
+#pragma unroll
+      for (int w = 16; w >= 1; w >>= 1) {
+#pragma unroll
+        for (int q = 0; q < w; ++q) acc[q] = f2_add(acc[q], acc[q + w]);
+      }
+      float s0, s1;
+      f2_unpack(acc[0], s0, s1);
+      l = l * alpha + (s0 + s1);
+      tmem_wait_st();
+      if (rescale) {
+        // scale O once O += P(i-1) V is done; O += P(i) V waits for p_full
+        if (!mbar_wait_warp(&p_empty[t], (i - 1) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+          tmem_st32(tO + c * 32, ov);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      mbar_arrive(&p_full[t]);
+    }
+    // ---------------------------------------------------------------- epilogue of slot t
+    const bool fin = ok && (nt == 0 || mbar_wait_warp(&p_empty[t], (nt - 1) & 1, wctx, MCS_WHERE_ATTN_EPILOGUE));
+    if (fin && (t == 0 || single || has1)) {
+      tc_fence_after();
+      const bool partial = p.part_o != nullptr;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float lse2 = l > 0.f ? m + log2f(l) : -CUDART_INF_F;
+      const size_t bht = static_cast<size_t>(bh) * p.Tq + qt;
+      const size_t slice = static_cast<size_t>(single ? 2 * split + t : split) * BH * p.Tq;
+      if (row_valid) {
+        if (partial) p.part_lse[(slice + bht) * 128 + row] = lse2;
+        else if (p.lse) p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok] = lse2 * kLn2;
+      }
+      uint16_t* orow = p.o + ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D;
+      float* prow = p.part_o + ((slice + bht) * 128 + row) * D;
+#pragma unroll
+      for (int cc = 0; cc < D / 32; ++cc) {
+        float ov[32];
+        if (nt > 0) {
+          tmem_ld32(tO + cc * 32, ov);
+          tmem_wait_ld();
+        }
+        if (!row_valid) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ov[e] = l > 0.f ? ov[e] * inv : 0.f;
+        if (partial) {
+          float4* d4 = reinterpret_cast<float4*>(prow + cc * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d4[e] = make_float4(ov[4 * e], ov[4 * e + 1], ov[4 * e + 2], ov[4 * e + 3]);
+        } else {
+          uint4* d4 = reinterpret_cast<uint4*>(orow + cc * 32);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            d4[e] = make_uint4(pack_bf16(ov[8 * e], ov[8 * e + 1]), pack_bf16(ov[8 * e + 2], ov[8 * e + 3]),
+                               pack_bf16(ov[8 * e + 4], ov[8 * e + 5]), pack_bf16(ov[8 * e + 6], ov[8 * e + 7]));
+        }
+      }
+    }
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
+    named_barrier_sync<1, kThreads>();
+  }
+
+  // ------------------------------------------------------------------ teardown
+  // All roles have left their loops. After an abort, wait (bounded) for copies
+  // and UMMAs this CTA issued, then free TMEM.
+  __syncthreads();
+  if (*abort_flag) {
+    volatile int never = 0;
+    const WaitCtx drain_ctx{&never, nullptr, 50000000ull};
+    if (threadIdx.x == 32) {
+      if (n > 0) mbar_wait(q_full, 0, drain_ctx, MCS_WHERE_DRAIN);
+      for (int j = max(0, issued - C::NS); j < issued; ++j) {
+        mbar_wait(&k_full[j % C::NS], (j / C::NS) & 1, drain_ctx, MCS_WHERE_DRAIN);
+        mbar_wait(&v_full[j % C::NS], (j / C::NS) & 1, drain_ctx, MCS_WHERE_DRAIN);
+      }
+    }
+    if (warp == 0 && lane == 0) {
+      umma_commit(drain_bar);
+      mbar_wait(drain_bar, 0, drain_ctx, MCS_WHERE_DRAIN);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+namespace {
+
+// Joins the splits of the keys: with lse2_s and o_s of split s,
+// lse2 = log2 sum_s 2^lse2_s and o = sum_s 2^(lse2_s - lse2) o_s. One warp per
+// row, lane l holds d/32 columns; the splits are summed in their order.
+template <int D>
+__global__ void __launch_bounds__(128) ex_combine(const ExTile p, int parts) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);  // (b, tok, head)
+  if (r >= static_cast<long long>(p.B) * p.Nq * p.Hq) return;
+  const int head = r % p.Hq, tok = r / p.Hq % p.Nq, b = r / p.Hq / p.Nq;
+  const size_t at = ((static_cast<size_t>(b) * p.Hkv + head / p.g) * p.Tq + tok / p.tpt) * 128 + tok % p.tpt * p.g +
+                    head % p.g;
+  const size_t slice = static_cast<size_t>(p.B) * p.Hkv * p.Tq * 128;
+  float m = -CUDART_INF_F;
+  for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_lse[s * slice + at]);
+#pragma unroll
+  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+  float l = 0.f, o[E] = {};
+  if (m > -CUDART_INF_F)
+    for (int s = 0; s < parts; ++s) {
+      const float w = fast_exp2(p.part_lse[s * slice + at] - m);
+      const float* src = p.part_o + (s * slice + at) * D + lane * E;
+      l += w;
+      if (w > 0.f) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
+      }
+    }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + static_cast<size_t>(r) * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
+  if (p.lse && lane == 0)
+    p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+}
+
+// Document ids as the tiles read them. Key tiles: ids of 128 keys (-1 past Nk and
+// for padding) and their range. Query tiles: the range over the tile's tokens
+// and, for the backward pass, the id of every packed row (-2 for padding and
+// empty rows). One CTA of 128 threads per tile.
+__global__ void __launch_bounds__(128) ex_doc_tiles(const ExTile p, int* k_ids, int4* k_ranges, int* q_ids,
+                                                    int4* q_ranges) {
+  __shared__ int s_min, s_max, s_pad;
+  const int b = blockIdx.y;
+  const bool key = static_cast<int>(blockIdx.x) < p.Tk;
+  const int tile = key ? blockIdx.x : blockIdx.x - p.Tk;
+  if (threadIdx.x == 0) s_min = 0x7fffffff, s_max = static_cast<int>(0x80000000), s_pad = 0;
+  __syncthreads();
+  const int i = threadIdx.x;
+  const int n = key ? p.Nk : p.Nq;
+  const int tok = key ? tile * 128 + i : tile * p.tpt + i / p.g;
+  const bool in = tok < n && (key || i < p.tpt * p.g);
+  const int id = in ? (key ? p.doc_k : p.doc_q)[static_cast<size_t>(b) * n + tok] : -1;
+  const size_t at = static_cast<size_t>(b) * (key ? p.Tk : p.Tq) + tile;
+  if (key) k_ids[at * 128 + i] = id < 0 ? -1 : id;
+  else if (q_ids) q_ids[at * 128 + i] = id < 0 ? -2 : id;
+  if (id >= 0) {
+    atomicMin(&s_min, id);
+    atomicMax(&s_max, id);
+  } else if (in) {
+    s_pad = 1;  // every writer writes the same
+  }
+  __syncthreads();
+  if (i == 0) (key ? k_ranges : q_ranges)[at] = make_int4(s_min, s_max, s_pad, 0);
+}
+
+template <int D, bool MOD>
+cudaError_t launch_fwd(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const ExTile& p,
+                       cudaStream_t s) {
+  auto kern = ex_fwd_kernel<D, MOD>;
+  const unsigned bits = p.k_ranges ? (p.Tk + 31) / 32 * 4u : 0u;
+  const unsigned smem = FwdCfg<D>::SMEM + bits;
+  static KernelReady ready;
+  const cudaError_t e = make_ready(ready, kern, FwdCfg<D>::SMEM + 8192, kLaunchRegs);  // 8192: 2^16 tiles
+  if (e != cudaSuccess) return e;
+  const int per = p.single ? 1 : 2;
+  const long long grid = static_cast<long long>(p.B) * p.Hkv * ((p.Tq + per - 1) / per) * p.nsplit;
+  kern<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(*tq, *tk, *tv, p);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_ex_fwd(int d, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const ExTile& p,
+                          cudaStream_t s) {
+  const bool mod = p.cap_k != 0.f || p.slopes;
+  if (d == 64) return mod ? launch_fwd<64, true>(tq, tk, tv, p, s) : launch_fwd<64, false>(tq, tk, tv, p, s);
+  return mod ? launch_fwd<128, true>(tq, tk, tv, p, s) : launch_fwd<128, false>(tq, tk, tv, p, s);
+}
+
+cudaError_t launch_ex_combine(int d, const ExTile& p, int parts, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.B) * p.Nq * p.Hq + 3) / 4);
+  if (d == 64) ex_combine<64><<<grid, 128, 0, s>>>(p, parts);
+  else ex_combine<128><<<grid, 128, 0, s>>>(p, parts);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ex_doc_tiles(const ExTile& p, int* k_ids, int4* k_ranges, int* q_ids, int4* q_ranges,
+                                cudaStream_t s) {
+  ex_doc_tiles<<<dim3(p.Tk + p.Tq, p.B), 128, 0, s>>>(p, k_ids, k_ranges, q_ids, q_ranges);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace mcs

@@ -1,5 +1,5 @@
 // Attention with modified scores, one warp per row: the plainest form of
-// mcs_dense_ex, mcs_dense_bwd, mcs_decode and mcs_decode_shared.
+// mcs_dense_bwd, mcs_decode and mcs_decode_shared.
 //
 // A warp walks its row's partners 32 at a time. Lane l forms the score of
 // partner l (an fp32 dot product over d), the warp keeps a running maximum and
@@ -82,42 +82,6 @@ struct RowAcc {
     for (int e = 0; e < E; ++e) row[lane * E + e] = to_bf(a[e] * f);
   }
 };
-
-template <int D>
-__global__ void rows_fwd(const ExParams p) {
-  __shared__ float sq[kWarps][D];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * kWarps + w;  // (b, i, h)
-  const bool live = row < static_cast<long long>(p.B) * p.Nq * p.Hq;
-  const int h = live ? row % p.Hq : 0, i = live ? row / p.Hq % p.Nq : 0, b = live ? row / p.Hq / p.Nq : 0;
-  if (live)
-    for (int c = lane; c < D; c += 32) sq[w][c] = bf(p.q[row * D + c]);
-  __syncwarp();
-  if (!live) return;
-  const int hk = h / p.g, pos = i + p.Nk - p.Nq, prefix = p.prefix ? p.prefix[b] : 0;
-  const float slope = p.slopes ? p.slopes[h] : 0.f;
-  float m = -CUDART_INF_F, l = 0.f;
-  RowAcc<D> acc;
-  for (int j0 = 0; j0 < p.Nk; j0 += 32) {
-    const int j = j0 + lane;
-    float s = -CUDART_INF_F, t;
-    if (j < p.Nk && valid_pair(p, b, i, j, prefix))
-      s = score(p.scale * dot<D>(sq[w], p.k + ((static_cast<size_t>(b) * p.Nk + j) * p.Hkv + hk) * D), p.cap, slope,
-                fabsf(static_cast<float>(pos - j)), t);
-    const float mn = fmaxf(m, warp_max(s));
-    if (mn == -CUDART_INF_F) continue;
-    const float pr = expf(s - mn), alpha = expf(m - mn);
-    m = mn;
-    l = l * alpha + warp_sum(pr);
-    acc.scale(alpha);
-    for (int e = 0; e < 32 && j0 + e < p.Nk; ++e) {
-      const float pe = __shfl_sync(0xffffffffu, pr, e);
-      if (pe != 0.f) acc.add(pe, p.v + ((static_cast<size_t>(b) * p.Nk + j0 + e) * p.Hkv + hk) * D, lane);
-    }
-  }
-  acc.store(p.o + row * D, lane, l > 0.f ? 1.f / l : 0.f);
-  if (p.lse && lane == 0) p.lse[(static_cast<size_t>(b) * p.Hq + h) * p.Nq + i] = l > 0.f ? m + logf(l) : -CUDART_INF_F;
-}
 
 // delta[b,h,i] = sum_c d_o o
 template <int D>
@@ -245,14 +209,6 @@ __global__ void rows_decode(const DecodeParams p) {
 unsigned blocks(long long rows) { return static_cast<unsigned>((rows + kWarps - 1) / kWarps); }
 
 }  // namespace
-
-cudaError_t launch_ex_rows_fwd(int d, const ExParams& p, cudaStream_t s) {
-  const unsigned n = blocks(static_cast<long long>(p.B) * p.Nq * p.Hq);
-  if (d == 64) rows_fwd<64><<<n, kWarps * 32, 0, s>>>(p);
-  else rows_fwd<128><<<n, kWarps * 32, 0, s>>>(p);
-  note_launches(1);
-  return cudaGetLastError();
-}
 
 template <int D>
 static void rows_bwd(const ExParams& p, cudaStream_t s) {

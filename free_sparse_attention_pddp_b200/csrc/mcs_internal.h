@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/mcs.h"
 
 // status block word indices (int32 words at the start of the workspace)
@@ -134,6 +136,36 @@ struct ExParams {
   int* status;
 };
 
+// The tile kernels' view of a call (attn_ex_fwd.cu, attn_ex_bwd.cu).
+struct ExTile {
+  int B, Hq, Hkv, g, tpt, Nq, Nk;  // tpt: tokens of a packed query tile
+  int Tq, Tk;                      // query and key tiles
+  int nsplit, single, chunk;       // forward: key splits, one-tile CTAs, heads per chunk of the work order
+  float mul;                       // log2 units per transformed score: scale log2 e, or cap log2 e
+  float cap_k;                     // scale / cap; 0: no cap
+  float scale;
+  int causal;
+  const float* slopes;
+  const int32_t* prefix;
+  const int32_t *doc_q, *doc_k;    // null without a document mask, and then so are the next five
+  const int4 *q_ranges, *k_ranges;  // [B,Tq], [B,Tk]: smallest and largest id, any padding
+  const int *q_ids, *k_ids;        // [B,Tq,128] (backward), [B,Tk,128]
+  const int32_t* lens;             // shared prefix: the requests' lengths give the positions
+  int P, C;
+  uint16_t* o;                     // outputs, or the partials of the splits
+  float* lse;
+  float *part_o, *part_lse;        // [parts][B,Hkv,Tq,128](,d), lse in log2 units
+  int* status;
+  uint64_t wait_limit_ns;
+  int debug_flags;
+};
+
+cudaError_t launch_ex_fwd(int d, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const ExTile& p,
+                          cudaStream_t s);
+cudaError_t launch_ex_combine(int d, const ExTile& p, int parts, cudaStream_t s);
+cudaError_t launch_ex_doc_tiles(const ExTile& p, int* k_ids, int4* k_ranges, int* q_ids, int4* q_ranges,
+                                cudaStream_t s);
+
 struct DecodeParams {
   int B, Hq, Hkv, g, C, P;
   float scale, cap;
@@ -145,12 +177,34 @@ struct DecodeParams {
   int* status;
 };
 
-cudaError_t launch_ex_rows_fwd(int d, const ExParams& p, cudaStream_t s);
 cudaError_t launch_ex_rows_bwd(int d, const ExParams& p, cudaStream_t s);
 cudaError_t launch_decode_rows(int d, const DecodeParams& p, cudaStream_t s);
 
 // MCS_OK when the current device is an sm_100 GPU
 mcs_status check_device();
+// 4-D map of a bf16 [B, N, H, d] tensor, box {64, heads, tokens, 1}, 128-byte swizzle: `tokens` consecutive
+// tokens of `heads` consecutive heads per load; tokens past N read as zero
+mcs_status tiles_map(CUtensorMap* m, const void* base, int B, int N, int H, int d, int heads, int tokens);
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per bounded device wait
+
+// Before a kernel's first launch on the current device: allow `smem` bytes of dynamic shared memory and, where
+// `regs` is not 0, check the registers per thread that its setmaxnreg split counts on. `done` is one flag per device.
+struct KernelReady {
+  std::atomic<bool> done[64] = {};
+};
+template <typename Kernel>
+cudaError_t make_ready(KernelReady& r, Kernel kern, unsigned smem, int regs) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && r.done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+  if (regs && fa.numRegs != regs) return cudaErrorInvalidKernelImage;
+  if (dev < 64) r.done[dev].store(true, std::memory_order_release);
+  return cudaSuccess;
+}
 
 // process-wide test knobs (see mcs_debug_set in api.cu)
 int debug_flags();
