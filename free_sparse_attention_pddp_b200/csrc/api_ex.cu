@@ -11,7 +11,8 @@ using namespace mcs;
 namespace {
 
 constexpr int kMaxGroup = 128;            // query heads of one KV head: one 128-row tile holds a token's
-constexpr int kMaxDocTiles = 1 << 16;     // tiles of a document mask's bitmap
+constexpr int kMaxDocQueryTiles = 1 << 16;  // tiles of a document mask's bitmaps: over query tiles
+constexpr int kMaxDocKeyTiles = 1 << 13;    // and over key tiles (the dQ kernel has 1 KB left for it)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -45,8 +46,8 @@ mcs_status check_opts(const mcs_attn_shape* s, const mcs_attn_opts* o) {
   if ((o->doc_q == nullptr) != (o->doc_k == nullptr)) return MCS_ERR_INVALID_ARG;
   if (o->doc_q) {
     const int tokens = 128 / (s->Hq / s->Hkv);
-    if ((static_cast<long long>(s->Nk) + 127) / 128 > kMaxDocTiles ||
-        (static_cast<long long>(s->Nq) + tokens - 1) / tokens > kMaxDocTiles)
+    if ((static_cast<long long>(s->Nk) + 127) / 128 > kMaxDocKeyTiles ||
+        (static_cast<long long>(s->Nq) + tokens - 1) / tokens > kMaxDocQueryTiles)
       return MCS_ERR_UNSUPPORTED;
   }
   return MCS_OK;
@@ -122,6 +123,28 @@ FwdWs fwd_layout(const FwdPlan& f, int B, int Hkv, int d) {
   return w;
 }
 
+// workspace: status | document tiles | statistics of the packed rows
+struct BwdWs {
+  size_t k_ids, k_ranges, q_ids, q_ranges, stats, total;
+};
+
+BwdWs bwd_layout(const FwdPlan& f, int B, int Hkv) {
+  BwdWs w;
+  size_t off = MCS_STATUS_BYTES;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  w.k_ids = take(static_cast<size_t>(B) * f.Tk * 512);
+  w.k_ranges = take(static_cast<size_t>(B) * f.Tk * 16);
+  w.q_ids = take(static_cast<size_t>(B) * f.Tq * 512);
+  w.q_ranges = take(static_cast<size_t>(B) * f.Tq * 16);
+  w.stats = take(static_cast<size_t>(B) * Hkv * f.Tq * 1024);
+  w.total = off;
+  return w;
+}
+
 ExTile tile_params(const ExParams& p, const FwdPlan& f, int d) {
   ExTile t{};
   t.B = p.B; t.Hq = p.Hq; t.Hkv = p.Hkv; t.g = p.g; t.tpt = f.tpt; t.Nq = p.Nq; t.Nk = p.Nk;
@@ -188,7 +211,8 @@ size_t mcs_attn_workspace_bytes(const mcs_attn_shape* s, mcs_op op) {
   if (check_attn(s) != MCS_OK) return 0;
   if (op == MCS_OP_DENSE_EX)
     return fwd_layout(fwd_plan(s->B, s->Hkv, s->Hq / s->Hkv, s->Nq, s->Nk, s->d), s->B, s->Hkv, s->d).total;
-  if (op == MCS_OP_DENSE_BWD) return MCS_STATUS_BYTES + align256(static_cast<size_t>(s->B) * s->Hq * s->Nq * 4);
+  if (op == MCS_OP_DENSE_BWD)
+    return bwd_layout(fwd_plan(s->B, s->Hkv, s->Hq / s->Hkv, s->Nq, s->Nk, s->d), s->B, s->Hkv).total;
   return 0;
 }
 
@@ -246,18 +270,37 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
   if (ws_bytes < mcs_attn_workspace_bytes(s, MCS_OP_DENSE_BWD)) return MCS_ERR_INVALID_ARG;
   if ((st = check_device()) != MCS_OK) return st;
   ExParams p = ex_params(s, opts);
-  p.q = static_cast<const uint16_t*>(q);
-  p.k = static_cast<const uint16_t*>(k);
-  p.v = static_cast<const uint16_t*>(v);
-  p.o_in = static_cast<const uint16_t*>(o);
-  p.d_o = static_cast<const uint16_t*>(d_o);
-  p.lse_in = lse;
-  p.dq = static_cast<uint16_t*>(dq);
-  p.dk = static_cast<uint16_t*>(dk);
-  p.dv = static_cast<uint16_t*>(dv);
-  p.delta = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + MCS_STATUS_BYTES);
   p.status = static_cast<int*>(ws);
-  return launch_ex_rows_bwd(s->d, p, stream) == cudaSuccess ? MCS_OK : MCS_ERR_CUDA;
+  const FwdPlan f = fwd_plan(p.B, p.Hkv, p.g, p.Nq, p.Nk, s->d);
+  const BwdWs w = bwd_layout(f, p.B, p.Hkv);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  CUtensorMap tq, tg, tk, tv;
+  if (tiles_map(&tq, q, p.B, p.Nq, p.Hq, s->d, p.g, f.tpt) != MCS_OK ||
+      tiles_map(&tg, d_o, p.B, p.Nq, p.Hq, s->d, p.g, f.tpt) != MCS_OK ||
+      tiles_map(&tk, k, p.B, p.Nk, p.Hkv, s->d, 1, 128) != MCS_OK ||
+      tiles_map(&tv, v, p.B, p.Nk, p.Hkv, s->d, 1, 128) != MCS_OK)
+    return MCS_ERR_CUDA;
+  ExTile t = tile_params(p, f, s->d);
+  t.dq = static_cast<uint16_t*>(dq);
+  t.dk = static_cast<uint16_t*>(dk);
+  t.dv = static_cast<uint16_t*>(dv);
+  float* stats = reinterpret_cast<float*>(base + w.stats);
+  t.stats = stats;
+  if (p.doc_q) {
+    int* kid = reinterpret_cast<int*>(base + w.k_ids);
+    int* qid = reinterpret_cast<int*>(base + w.q_ids);
+    int4* kr = reinterpret_cast<int4*>(base + w.k_ranges);
+    int4* qr = reinterpret_cast<int4*>(base + w.q_ranges);
+    if (launch_ex_doc_tiles(t, kid, kr, qid, qr, stream) != cudaSuccess) return MCS_ERR_CUDA;
+    t.k_ids = kid;
+    t.k_ranges = kr;
+    t.q_ids = qid;
+    t.q_ranges = qr;
+  }
+  if (launch_ex_row_stats(s->d, t, static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(d_o), lse, stats,
+                          stream) != cudaSuccess)
+    return MCS_ERR_CUDA;
+  return ok_or_cuda(launch_ex_bwd(s->d, &tq, &tg, &tk, &tv, t, stream));
 }
 
 size_t mcs_decode_workspace_bytes(const mcs_decode_shape* s) {

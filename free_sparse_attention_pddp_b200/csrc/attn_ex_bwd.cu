@@ -1,0 +1,863 @@
+// Attention with modified scores, gradients (mcs_dense_bwd), on the tensor
+// cores. With P = 2^(s - lse) and D_i = d_o_i . o_i,
+//   dP = d_o V^T,  dS = P (dP - D) (1 - t^2),
+//   dV = P^T d_o,  dK = scale dS^T Q,  dQ = scale dS K.
+//
+// Two kernels instead of one: dK and dV are sums over queries, dQ over keys,
+// so a single sweep would have to add one of them into global memory from many
+// CTAs, in an order that changes from run to run. Here every sum is one CTA's,
+// in a fixed order, at the price of seven products per tile instead of five.
+//
+//   ex_dkv_kernel: a CTA owns 128 keys of a KV head, K and V resident, and
+//     streams packed query tiles (so the heads that share the KV head are
+//     summed in the accumulators). Scores are computed transposed, keys on
+//     TMEM lanes: S^T = K Q^T, dP^T = V d_o^T. P^T and dS^T (bf16) overwrite
+//     them and are the TS-form A operands of dV += P^T d_o, dK += dS^T Q.
+//     UMMA order dV(i) S(i+1) dK(i) dP(i+1): the softmax's two phases of a tile
+//     (P from S, dS from dP) each run beside two products.
+//   ex_dq_kernel: a CTA owns one packed query tile and streams key tiles:
+//     S = Q K^T, dP = d_o V^T, dS over dP, dQ += dS K. S(i+1) and dP(i+1) are
+//     computed while the softmax works on tile i (dP has two buffers).
+//
+// Threads (384) as in the forward kernel: warp 0 UMMA, warp 1 TMA, warp 2
+// clears padded rows (document masks), warps 4-7 and 8-11 the two halves of a
+// tile's columns, one thread per row and half.
+#include "attn_ex.cuh"
+
+namespace mcs {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168;
+constexpr int kLowRegs = 64;
+constexpr int kSoftRegs = 216;
+static_assert(128 * kLowRegs + 256 * kSoftRegs <= kThreads * kLaunchRegs, "register split");
+
+template <int D>
+struct DkvCfg {
+  static constexpr int KB = D / 64;
+  static constexpr uint32_t TILE = 128u * D * 2u;
+  static constexpr int NS = D == 128 ? 2 : 4;  // stages of Q, d_o and their rows' statistics
+  static constexpr uint32_t OFF_K = 0;
+  static constexpr uint32_t OFF_V = TILE;
+  static constexpr uint32_t OFF_Q = 2 * TILE;
+  static constexpr uint32_t OFF_G = OFF_Q + NS * TILE;
+  static constexpr uint32_t OFF_STAT = OFF_G + NS * TILE;     // [stage]: -lse (log2 units) [128], D [128]
+  static constexpr uint32_t OFF_ROW = OFF_STAT + NS * 1024;   // slope [128], token in the tile [128]
+  static constexpr uint32_t OFF_BAR = OFF_ROW + 1024;
+  // kv_full, q_full[NS], q_ok[NS], q_empty[NS], s_full, dp_full, p_full, ds_full, done
+  static constexpr uint32_t NBAR = 1 + 3 * NS + 5;
+  static constexpr uint32_t OFF_BITS = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;
+  static constexpr uint32_t SMEM = OFF_BITS + 1024;
+};
+
+template <int D>
+struct DqCfg {
+  static constexpr int KB = D / 64;
+  static constexpr uint32_t TILE = 128u * D * 2u;
+  static constexpr int NK = D == 128 ? 3 : 4;  // K stages: read by S(i) and, a tile later, by dQ(i)
+  static constexpr int NV = D == 128 ? 2 : 4;  // V stages: read by dP(i) alone
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_G = TILE;
+  static constexpr uint32_t OFF_K = 2 * TILE;
+  static constexpr uint32_t OFF_V = OFF_K + NK * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_V + NV * TILE;
+  // qg_full, k_full[NK], k_ok[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full, s_read, dp_full[2], ds_full[2], done
+  static constexpr uint32_t NBAR = 1 + 3 * NK + 2 * NV + 2 + 2 + 2 + 1;
+  static constexpr uint32_t OFF_BITS = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;
+  static constexpr uint32_t SMEM = OFF_BITS + 1024;
+};
+
+// Zeroes rows rt .. 127 of `tiles` consecutive tiles (rows that no load writes).
+template <int KB>
+__device__ __forceinline__ void zero_tail_rows(uint8_t* tile, int tiles, int rt) {
+  for (int i = threadIdx.x; i < tiles * KB * (128 - rt) * 8; i += kThreads) {
+    const int c = i & 7, row = rt + (i >> 3) % (128 - rt), blk = (i >> 3) / (128 - rt);
+    *reinterpret_cast<uint4*>(tile + blk * 16384 + row * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// Stores one thread's TMEM row of D fp32 columns, times f, as bf16.
+template <int D>
+__device__ __forceinline__ void store_row(uint32_t taddr, bool have, bool valid, float f, uint16_t* dst) {
+#pragma unroll
+  for (int cc = 0; cc < D / 32; ++cc) {
+    float v[32];
+    if (have) {
+      tmem_ld32(taddr + cc * 32, v);
+      tmem_wait_ld();
+    }
+    if (!valid) continue;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = have ? v[e] * f : 0.f;
+    uint4* d4 = reinterpret_cast<uint4*>(dst + cc * 32);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      d4[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
+                         pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
+  }
+}
+
+// Frees TMEM once every role has left; after an abort, waits (bounded) for what is in flight.
+__device__ __forceinline__ void teardown(volatile int* abort_flag, uint64_t* done, uint64_t* loads, int nloads,
+                                         uint32_t tmem) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __syncthreads();
+  if (*abort_flag) {
+    volatile int never = 0;
+    const WaitCtx drain_ctx{&never, nullptr, 50000000ull};
+    if (warp == 1 && lane == 0) {
+      // both parities of every load barrier: the phase that the loads in flight complete is one of the two
+      for (int s = 0; s < nloads; ++s) {
+        mbar_wait(&loads[s], 0, drain_ctx, MCS_WHERE_DRAIN);
+        mbar_wait(&loads[s], 1, drain_ctx, MCS_WHERE_DRAIN);
+      }
+    }
+    if (warp == 0 && lane == 0) {
+      umma_commit(done);
+      mbar_wait(done, 0, drain_ctx, MCS_WHERE_DRAIN);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Per packed row: -lse in log2 units and D = d_o . o, as [B Hkv, Tq][2][128]; an empty row, like a row whose lse is
+// -inf, gets (-inf, 0), which makes its P zero. One warp per row.
+template <int D>
+__global__ void __launch_bounds__(256) ex_row_stats(const ExTile p, const uint16_t* o, const uint16_t* d_o,
+                                                    const float* lse, float* stats) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (r >= static_cast<long long>(p.B) * p.Hkv * p.Tq * 128) return;
+  const int row = r & 127, qt = (r >> 7) % p.Tq, bh = (r >> 7) / p.Tq;
+  const int tok = qt * p.tpt + row / p.g, head = bh % p.Hkv * p.g + row % p.g, b = bh / p.Hkv;
+  float nl = -CUDART_INF_F, s = 0.f;
+  if (row < p.tpt * p.g && tok < p.Nq) {
+    const float L = lse[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok];
+    const size_t at = ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D + lane * E;
+    if (L > -CUDART_INF_F) {
+      nl = -L * kLog2e;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(o + at + e);
+        const uint32_t y = *reinterpret_cast<const uint32_t*>(d_o + at + e);
+        s = fmaf(__uint_as_float(x << 16), __uint_as_float(y << 16), s);
+        s = fmaf(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u), s);
+      }
+    }
+  }
+#pragma unroll
+  for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+  if (lane == 0) {
+    stats[(r >> 7) * 256 + row] = nl;
+    stats[(r >> 7) * 256 + 128 + row] = s;
+  }
+}
+
+}  // namespace
+
+template <int D, bool MOD>
+__global__ void __launch_bounds__(kThreads, 1)
+    ex_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
+                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
+  using C = DkvCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sG = smem + C::OFF_G;
+  float* row_slope = reinterpret_cast<float*>(smem + C::OFF_ROW);
+  float* row_tok = row_slope + 128;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = kv_full + 1;        // [stage]: Q, d_o and statistics
+  uint64_t* q_ok = q_full + C::NS;       // [stage]: padded rows are clear (document masks)
+  uint64_t* q_empty = q_ok + C::NS;      // [stage]
+  uint64_t* s_full = q_empty + C::NS;
+  uint64_t* dp_full = s_full + 1;
+  uint64_t* p_full = dp_full + 1;
+  uint64_t* ds_full = p_full + 1;
+  uint64_t* done = ds_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* count = reinterpret_cast<int*>(tmem_slot + 2);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  // causal: the first key tiles meet the most queries and go first, the heads of a chunk side by side
+  const int BH = p.B * p.Hkv;
+  int kt, bh;
+  if (p.causal) {
+    const int per_chunk = p.chunk * p.Tk;
+    const int ch = blockIdx.x / per_chunk, in = blockIdx.x % per_chunk;
+    const int heads = min(p.chunk, BH - ch * p.chunk);
+    bh = ch * p.chunk + in % heads;
+    kt = in / heads;
+  } else {
+    kt = blockIdx.x % p.Tk;
+    bh = blockIdx.x / p.Tk;
+  }
+  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int off = p.Nk - p.Nq;
+  const int prefix = p.prefix ? p.prefix[b] : 0;
+  // query tiles lo .. Tq - 1 reach these keys
+  int lo = 0;
+  if (p.causal && kt * 128 >= prefix) lo = min(p.Tq, max(0, kt * 128 - off) / p.tpt);
+  const bool docs = p.k_ranges != nullptr;
+  const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
+  const int4 mine = docs ? p.k_ranges[static_cast<size_t>(b) * p.Tk + kt] : none;
+  const int rt = p.tpt * p.g;
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_ok[s], 1);
+      mbar_init(&q_empty[s], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    mbar_init(p_full, 256);
+    mbar_init(ds_full, 256);
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    *count = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x < 128) {
+    row_slope[threadIdx.x] = p.slopes ? p.slopes[hk * p.g + threadIdx.x % p.g] * kLog2e : 0.f;
+    row_tok[threadIdx.x] = static_cast<float>(threadIdx.x / p.g);
+  }
+  if (rt < 128) {
+    zero_tail_rows<C::KB>(sQ, 2 * C::NS, rt);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int n = p.Tq - lo;
+  if (docs) n = build_tile_bits(bits, count, p.q_ranges + static_cast<size_t>(b) * p.Tq, lo, p.Tq, mine, none);
+  const TileIter first{docs ? bits : nullptr, lo, lo};
+  const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
+    if (warp == 0) {
+      // ---------------------------------------------------------------- UMMA issuer
+      if (lane == 0 && n > 0) {
+        constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t IDESC_A = idesc_bf16_f32(128, D, false, true);
+        const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024), dV = sdesc_sw128(smem_u32(sV), 16, 1024);
+        const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dG = sdesc_sw128(smem_u32(sG), 16, 1024);
+        const uint64_t dQm = sdesc_sw128(smem_u32(sQ), 16384, 1024), dGm = sdesc_sw128(smem_u32(sG), 16384, 1024);
+        // D[tmem] = A B^T over d, both K-major
+        auto scores = [&](uint32_t to, uint64_t a, uint64_t bb, uint64_t* bar) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
+            umma_bf16_ss(to, sdesc_advance(a, o), sdesc_advance(bb, o), IDESC_S, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(bar);
+        };
+        // acc += A^T-form (bf16 over the score tile at `from`) times the rows of a tile
+        auto accumulate = [&](uint32_t acc, uint32_t from, uint64_t bb, int i) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16_ts(acc, from + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_advance(bb, kk * 2048), IDESC_A,
+                         (i > 0 || kk > 0) ? 1u : 0u);
+        };
+        auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
+        uint64_t* ready = docs ? q_ok : q_full;
+        bool ok = wait(kv_full, 0) && wait(&ready[0], 0);
+        if (ok) {
+          tc_fence_after();
+          scores(tmem, dK, dQ, s_full);
+          scores(tmem + 128, dV, dG, dp_full);
+        }
+        for (int i = 0; ok && i < n; ++i) {
+          const uint32_t at = (i % C::NS) * C::TILE, nx = ((i + 1) % C::NS) * C::TILE;
+          if (!wait(p_full, i)) break;
+          tc_fence_after();
+          accumulate(tmem + 256, tmem, sdesc_advance(dGm, at), i);
+          if (i + 1 < n) {
+            if (!wait(&ready[(i + 1) % C::NS], (i + 1) / C::NS)) break;
+            tc_fence_after();
+            scores(tmem, dK, sdesc_advance(dQ, nx), s_full);
+          }
+          if (!wait(ds_full, i)) break;
+          tc_fence_after();
+          accumulate(tmem + 384, tmem + 128, sdesc_advance(dQm, at), i);
+          umma_commit(&q_empty[i % C::NS]);
+          if (i + 1 < n) scores(tmem + 128, dV, sdesc_advance(dG, nx), dp_full);
+          else umma_commit(done);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- TMA producer
+      if (lane == 0 && n > 0) {
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_g);
+        mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+#pragma unroll
+        for (int kb = 0; kb < C::KB; ++kb) {
+          tma_load_4d(&tm_k, kv_full, sK + kb * 16384, kb * 64, hk, kt * 128, b);
+          tma_load_4d(&tm_v, kv_full, sV + kb * 16384, kb * 64, hk, kt * 128, b);
+        }
+        TileIter it = first;
+        for (int j = 0; j < n; ++j) {
+          const int s = j % C::NS;
+          if (j >= C::NS && !mbar_wait(&q_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+          const int qt = it.next();
+          if ((p.debug_flags & 1) && j == 0) continue;  // test knob: never deliver tile 0
+          mbar_arrive_expect_tx(&q_full[s], 2 * C::KB * rt * 128 + 1024);
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb) {
+            tma_load_4d(&tm_q, &q_full[s], sQ + s * C::TILE + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
+            tma_load_4d(&tm_g, &q_full[s], sG + s * C::TILE + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
+          }
+          bulk_load(&q_full[s], smem + C::OFF_STAT + s * 1024, p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256,
+                    1024);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2 && docs) {
+      // ---------------------------------------------------------------- padded queries
+      TileIter it = first;
+      for (int j = 0; j < n; ++j) {
+        const int s = j % C::NS;
+        if (!mbar_wait_warp(&q_full[s], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+        const size_t at = static_cast<size_t>(b) * p.Tq + it.next();
+        if (p.q_ranges[at].z) {
+          zero_padded_rows<C::KB>(sQ + s * C::TILE, p.q_ids + at * 128);
+          zero_padded_rows<C::KB>(sG + s * C::TILE, p.q_ids + at * 128);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_ok[s]);
+      }
+      __syncwarp();
+    }
+    named_barrier_sync<1, kThreads>();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
+  } else {
+    // ---------------------------------------------------------------- P and dS, then the epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    const int half = (warp - 4) >> 2;  // query rows 64 half .. 64 half + 63 of each tile
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const int key = kt * 128 + row;
+    const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_addr + half * 64;
+    const uint32_t tP = tmem + lane_addr + 128 + half * 64;
+    const bool key_valid = key < p.Nk;
+    const int my_doc = docs ? p.k_ids[(static_cast<size_t>(b) * p.Tk + kt) * 128 + row] : 0;  // padding: -1
+    const bool all_rows = !p.causal || key < prefix;
+    const bool all_keys = !p.causal || kt * 128 + 127 < prefix;
+    const bool bias = MOD && p.slopes != nullptr;
+    const uint64_t mul2 = f2_pack(p.mul, p.mul);
+    TileIter it = first;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % C::NS;
+      const int qt = it.next();
+      const float4* nl4 = reinterpret_cast<const float4*>(smem + C::OFF_STAT + s * 1024) + half * 16;
+      const float4* dl4 = nl4 + 32;
+      const float4* tok4 = reinterpret_cast<const float4*>(row_tok) + half * 16;
+      const float4* sl4 = reinterpret_cast<const float4*>(row_slope) + half * 16;
+      // this key's position in the tile's tokens: token c sees it when c >= at
+      const int at_i = key - off - qt * p.tpt;
+      const float at = static_cast<float>(at_i);
+      const int4* ids = nullptr;
+      bool partial = !all_keys && kt * 128 + 127 > off + qt * p.tpt;
+      if (docs) {
+        const size_t q_at = static_cast<size_t>(b) * p.Tq + qt;
+        if (!docs_same(mine, p.q_ranges[q_at])) {
+          partial = true;
+          ids = reinterpret_cast<const int4*>(p.q_ids + q_at * 128) + half * 16;
+        }
+      }
+      // the statistics of this stage, then the scores
+      if (!mbar_wait_warp(&q_full[s], (i / C::NS) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX) ||
+          !mbar_wait_warp(s_full, i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float pw[64];  // score, then P (1 - t^2)
+      tmem_ld32(tS, pw);
+      tmem_ld32(tS + 32, pw + 32);
+      tmem_wait_ld();
+      if (MOD && p.cap_k != 0.f) {
+        tanh_scaled<32>(pw, p.cap_k);
+        tanh_scaled<32>(pw + 32, p.cap_k);
+      }
+      const bool after = bias && __all_sync(0xffffffffu, at_i <= 0);              // every token at or after the key
+      const bool before = bias && __all_sync(0xffffffffu, at_i >= p.tpt - 1);     // every token at or before it
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 32 * h2; c < 32 * h2 + 32; c += 4) {
+          const float4 nl = nl4[c >> 2];
+          uint64_t e01 = f2_pack(nl.x, nl.y), e23 = f2_pack(nl.z, nl.w);
+          if (bias) {
+            const float4 tk = tok4[c >> 2], sl = sl4[c >> 2];
+            float d0 = at - tk.x, d1 = at - tk.y, d2 = at - tk.z, d3 = at - tk.w;  // -(distance) where after
+            if (before) d0 = -d0, d1 = -d1, d2 = -d2, d3 = -d3;
+            else if (!after) d0 = -fabsf(d0), d1 = -fabsf(d1), d2 = -fabsf(d2), d3 = -fabsf(d3);
+            e01 = f2_fma(f2_pack(sl.x, sl.y), f2_pack(d0, d1), e01);
+            e23 = f2_fma(f2_pack(sl.z, sl.w), f2_pack(d2, d3), e23);
+          }
+          float x0, x1, x2, x3;
+          f2_unpack(f2_fma(f2_pack(pw[c], pw[c + 1]), mul2, e01), x0, x1);
+          f2_unpack(f2_fma(f2_pack(pw[c + 2], pw[c + 3]), mul2, e23), x2, x3);
+          float p0 = fast_exp2(x0), p1 = fast_exp2(x1), p2 = fast_exp2(x2), p3 = fast_exp2(x3);
+          float w0 = p0, w1 = p1, w2 = p2, w3 = p3;
+          if (MOD && p.cap_k != 0.f) {
+            w0 = fmaf(-pw[c] * p0, pw[c], p0);
+            w1 = fmaf(-pw[c + 1] * p1, pw[c + 1], p1);
+            w2 = fmaf(-pw[c + 2] * p2, pw[c + 2], p2);
+            w3 = fmaf(-pw[c + 3] * p3, pw[c + 3], p3);
+          }
+          if (partial) {
+            const float4 tk = tok4[c >> 2];
+            bool v0 = all_rows || tk.x >= at, v1 = all_rows || tk.y >= at;
+            bool v2 = all_rows || tk.z >= at, v3 = all_rows || tk.w >= at;
+            if (ids) {
+              const int4 id = __ldg(ids + (c >> 2));  // padded queries hold -2, which no key's id equals
+              v0 = v0 && id.x == my_doc;
+              v1 = v1 && id.y == my_doc;
+              v2 = v2 && id.z == my_doc;
+              v3 = v3 && id.w == my_doc;
+            }
+            p0 = v0 ? p0 : 0.f, w0 = v0 ? w0 : 0.f;
+            p1 = v1 ? p1 : 0.f, w1 = v1 ? w1 : 0.f;
+            p2 = v2 ? p2 : 0.f, w2 = v2 ? w2 : 0.f;
+            p3 = v3 ? p3 : 0.f, w3 = v3 ? w3 : 0.f;
+          }
+          pk[(c - 32 * h2) / 2] = pack_bf16(p0, p1);
+          pk[(c - 32 * h2) / 2 + 1] = pack_bf16(p2, p3);
+          pw[c] = w0;
+          pw[c + 1] = w1;
+          pw[c + 2] = w2;
+          pw[c + 3] = w3;
+        }
+        tmem_st16u(tS + h2 * 16, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(p_full);
+      if (!mbar_wait_warp(dp_full, i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        float dp[32];
+        tmem_ld32(tP + h2 * 32, dp);
+        tmem_wait_ld();
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 dl = dl4[h2 * 8 + (c >> 2)];
+          const float* w = pw + h2 * 32 + c;
+          float a0, a1, a2, a3;
+          f2_unpack(f2_mul(f2_pack(w[0], w[1]), f2_sub(f2_pack(dp[c], dp[c + 1]), f2_pack(dl.x, dl.y))), a0, a1);
+          f2_unpack(f2_mul(f2_pack(w[2], w[3]), f2_sub(f2_pack(dp[c + 2], dp[c + 3]), f2_pack(dl.z, dl.w))), a2, a3);
+          if (partial) {  // a padded key's V may be NaN
+            a0 = w[0] == 0.f ? 0.f : a0;
+            a1 = w[1] == 0.f ? 0.f : a1;
+            a2 = w[2] == 0.f ? 0.f : a2;
+            a3 = w[3] == 0.f ? 0.f : a3;
+          }
+          pk[c / 2] = pack_bf16(a0, a1);
+          pk[c / 2 + 1] = pack_bf16(a2, a3);
+        }
+        tmem_st16u(tP + h2 * 16, pk);  // over dP columns that this thread has read
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(ds_full);
+    }
+    const bool fin = ok && (n == 0 || mbar_wait_warp(done, 0, wctx, MCS_WHERE_ATTN_EPILOGUE));
+    if (fin) {
+      tc_fence_after();
+      const size_t at = ((static_cast<size_t>(b) * p.Nk + key) * p.Hkv + hk) * D;
+      if (half == 0) store_row<D>(tmem + lane_addr + 256, n > 0, key_valid, 1.f, p.dv + at);
+      else store_row<D>(tmem + lane_addr + 384, n > 0, key_valid, p.scale, p.dk + at);
+    }
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
+    named_barrier_sync<1, kThreads>();
+  }
+  teardown(abort_flag, done, kv_full, n > 0 ? 1 + C::NS : 0, tmem);
+}
+
+template <int D, bool MOD>
+__global__ void __launch_bounds__(kThreads, 1)
+    ex_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
+                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
+  using C = DqCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sG = smem + C::OFF_G;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  uint64_t* qg_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* k_full = qg_full + 1;
+  uint64_t* v_full = k_full + C::NK;
+  uint64_t* k_ok = v_full + C::NV;  // K's padded rows are clear (document masks)
+  uint64_t* k_empty = k_ok + C::NK;
+  uint64_t* v_empty = k_empty + C::NK;
+  uint64_t* s_full = v_empty + C::NV;
+  uint64_t* s_read = s_full + 1;
+  uint64_t* dp_full = s_read + 1;  // [buffer]
+  uint64_t* ds_full = dp_full + 2;  // [buffer]
+  uint64_t* done = ds_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* count = reinterpret_cast<int*>(tmem_slot + 2);
+  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int BH = p.B * p.Hkv;
+  int qt, bh;
+  if (p.causal) {  // the last query tiles see the most keys and go first
+    const int per_chunk = p.chunk * p.Tq;
+    const int ch = blockIdx.x / per_chunk, in = blockIdx.x % per_chunk;
+    const int heads = min(p.chunk, BH - ch * p.chunk);
+    bh = ch * p.chunk + in % heads;
+    qt = p.Tq - 1 - in / heads;
+  } else {
+    qt = blockIdx.x % p.Tq;
+    bh = blockIdx.x / p.Tq;
+  }
+  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int off = p.Nk - p.Nq;
+  const int prefix = p.prefix ? p.prefix[b] : 0;
+  auto limit = [&](int pos) { return p.causal ? min(p.Nk, max(max(pos + 1, prefix), 0)) : p.Nk; };
+  const int hi = (limit(off + min(p.Nq, (qt + 1) * p.tpt) - 1) + 127) >> 7;
+  const bool docs = p.k_ranges != nullptr;
+  const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
+  const int4 mine = docs ? p.q_ranges[static_cast<size_t>(b) * p.Tq + qt] : none;
+  const int rt = p.tpt * p.g;
+
+  if (threadIdx.x == 0) {
+    mbar_init(qg_full, 1);
+    for (int s = 0; s < C::NK; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_ok[s], 1);
+      mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < C::NV; ++s) {
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_read, 256);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&dp_full[s], 1);
+      mbar_init(&ds_full[s], 256);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    *count = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (rt < 128) {
+    zero_tail_rows<C::KB>(sQ, 2, rt);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  int n = hi;
+  if (docs) n = build_tile_bits(bits, count, p.k_ranges + static_cast<size_t>(b) * p.Tk, 0, hi, mine, none);
+  const TileIter first{docs ? bits : nullptr, 0, 0};
+  const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
+  // TMEM: S | dP 0 | dQ | dP 1
+  const uint32_t tm_dp[2] = {tmem + 128, tmem + 384};
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
+    if (warp == 0) {
+      // ---------------------------------------------------------------- UMMA issuer
+      if (lane == 0 && n > 0) {
+        constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t IDESC_A = idesc_bf16_f32(128, D, false, true);
+        const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dG = sdesc_sw128(smem_u32(sG), 16, 1024);
+        const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024), dV = sdesc_sw128(smem_u32(sV), 16, 1024);
+        const uint64_t dKm = sdesc_sw128(smem_u32(sK), 16384, 1024);
+        auto scores = [&](uint32_t to, uint64_t a, uint64_t bb, uint64_t* bar) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk >> 2) * 16384 + (kk & 3) * 32;
+            umma_bf16_ss(to, sdesc_advance(a, o), sdesc_advance(bb, o), IDESC_S, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(bar);
+        };
+        auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
+        uint64_t* ready = docs ? k_ok : k_full;
+        // S(j) and dP(j): S is free once the softmax has read S(j - 1), dP's buffer once dQ(j - 2) was issued
+        auto both = [&](int j) {
+          if (j > 0 && !wait(s_read, j - 1)) return false;
+          if (!wait(&ready[j % C::NK], j / C::NK)) return false;
+          tc_fence_after();
+          scores(tmem, dQ, sdesc_advance(dK, (j % C::NK) * C::TILE), s_full);
+          if (!wait(&v_full[j % C::NV], j / C::NV)) return false;
+          tc_fence_after();
+          scores(tm_dp[j & 1], dG, sdesc_advance(dV, (j % C::NV) * C::TILE), &dp_full[j & 1]);
+          umma_commit(&v_empty[j % C::NV]);
+          return true;
+        };
+        bool ok = wait(qg_full, 0) && both(0);
+        for (int i = 0; ok && i < n; ++i) {
+          if (i + 1 < n && !both(i + 1)) break;
+          if (!wait(&ds_full[i & 1], i >> 1)) break;
+          tc_fence_after();
+          const uint64_t bb = sdesc_advance(dKm, (i % C::NK) * C::TILE);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16_ts(tmem + 256, tm_dp[i & 1] + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_advance(bb, kk * 2048),
+                         IDESC_A, (i > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&k_empty[i % C::NK]);
+          if (i + 1 == n) umma_commit(done);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- TMA producer
+      if (lane == 0 && n > 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+        mbar_arrive_expect_tx(qg_full, 2 * C::KB * rt * 128);
+#pragma unroll
+        for (int kb = 0; kb < C::KB; ++kb) {
+          tma_load_4d(&tm_q, qg_full, sQ + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
+          tma_load_4d(&tm_g, qg_full, sG + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
+        }
+        TileIter it = first;
+        for (int j = 0; j < n; ++j) {
+          const int sk = j % C::NK, sv = j % C::NV;
+          const int kt = it.next();
+          if (j >= C::NK && !mbar_wait(&k_empty[sk], ((j / C::NK) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+          if (!((p.debug_flags & 1) && j == 0)) {  // test knob: never deliver tile 0
+            mbar_arrive_expect_tx(&k_full[sk], C::TILE);
+#pragma unroll
+            for (int kb = 0; kb < C::KB; ++kb)
+              tma_load_4d(&tm_k, &k_full[sk], sK + sk * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
+          }
+          if (j >= C::NV && !mbar_wait(&v_empty[sv], ((j / C::NV) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+          mbar_arrive_expect_tx(&v_full[sv], C::TILE);
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_4d(&tm_v, &v_full[sv], sV + sv * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2 && docs) {
+      // ---------------------------------------------------------------- padded keys
+      TileIter it = first;
+      for (int j = 0; j < n; ++j) {
+        const int s = j % C::NK;
+        if (!mbar_wait_warp(&k_full[s], (j / C::NK) & 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+        const size_t at = static_cast<size_t>(b) * p.Tk + it.next();
+        if (p.k_ranges[at].z) {
+          zero_padded_rows<C::KB>(sK + s * C::TILE, p.k_ids + at * 128);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_ok[s]);
+      }
+      __syncwarp();
+    }
+    named_barrier_sync<1, kThreads>();
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
+  } else {
+    // ---------------------------------------------------------------- dS, then the epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    const int half = (warp - 4) >> 2;  // keys 64 half .. 64 half + 63 of each tile
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
+    const int tok = qt * p.tpt + row / p.g;
+    const int head = hk * p.g + row % p.g;
+    const bool row_valid = row < rt && tok < p.Nq;
+    const float* st = p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
+    const float negl = st[row], delta = st[128 + row];
+    const uint64_t negl2 = f2_pack(negl, negl), delta2 = f2_pack(delta, delta);
+    const int pos = off + tok;
+    const int lim = limit(pos);
+    const int lim_all = limit(off + qt * p.tpt);
+    const int my_doc = docs ? p.q_ids[(static_cast<size_t>(b) * p.Tq + qt) * 128 + row] : 0;  // padding: -2
+    const bool bias = MOD && p.slopes != nullptr;
+    const float slope = bias ? p.slopes[head < p.Hq ? head : 0] * kLog2e : 0.f;
+    const float mul = p.mul;
+    const uint64_t mul2 = f2_pack(mul, mul);
+    TileIter it = first;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const int kt = it.next();
+      const int4* ids = nullptr;
+      bool partial = (kt + 1) * 128 > lim_all;
+      if (docs) {
+        const size_t at = static_cast<size_t>(b) * p.Tk + kt;
+        if (!docs_same(mine, p.k_ranges[at])) {
+          partial = true;
+          ids = reinterpret_cast<const int4*>(p.k_ids + at * 128) + half * 16;
+        }
+      }
+      if (!mbar_wait_warp(s_full, i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float pw[64];
+      tmem_ld32(tmem + lane_addr + half * 64, pw);
+      tmem_ld32(tmem + lane_addr + half * 64 + 32, pw + 32);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(s_read);
+      if (MOD && p.cap_k != 0.f) {
+        tanh_scaled<32>(pw, p.cap_k);
+        tanh_scaled<32>(pw + 32, p.cap_k);
+      }
+      const int valid = lim - kt * 128 - half * 64;
+      const float base = static_cast<float>(pos - kt * 128 - half * 64);
+      const bool after = bias && __all_sync(0xffffffffu, base >= 63.f);
+      const bool before = bias && __all_sync(0xffffffffu, base <= 0.f);
+#pragma unroll
+      for (int c = 0; c < 64; c += 2) {
+        uint64_t e = negl2;
+        if (bias) {
+          float d0 = static_cast<float>(c) - base, d1 = static_cast<float>(c + 1) - base;  // -(distance) where after
+          if (before) d0 = -d0, d1 = -d1;
+          else if (!after) d0 = -fabsf(d0), d1 = -fabsf(d1);
+          e = f2_fma(f2_pack(slope, slope), f2_pack(d0, d1), e);
+        }
+        float x0, x1;
+        f2_unpack(f2_fma(f2_pack(pw[c], pw[c + 1]), mul2, e), x0, x1);
+        float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+        if (MOD && p.cap_k != 0.f) {
+          p0 = fmaf(-pw[c] * p0, pw[c], p0);
+          p1 = fmaf(-pw[c + 1] * p1, pw[c + 1], p1);
+        }
+        pw[c] = p0;
+        pw[c + 1] = p1;
+      }
+      if (partial) {
+        if (ids) {
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            const int4 id = __ldg(ids + (c >> 2));
+            pw[c] = (c < valid && id.x == my_doc) ? pw[c] : 0.f;
+            pw[c + 1] = (c + 1 < valid && id.y == my_doc) ? pw[c + 1] : 0.f;
+            pw[c + 2] = (c + 2 < valid && id.z == my_doc) ? pw[c + 2] : 0.f;
+            pw[c + 3] = (c + 3 < valid && id.w == my_doc) ? pw[c + 3] : 0.f;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) pw[c] = c < valid ? pw[c] : 0.f;
+        }
+      }
+      const uint32_t tP = tm_dp[i & 1] + lane_addr + half * 64;
+      if (!mbar_wait_warp(&dp_full[i & 1], (i >> 1) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        float dp[32];
+        tmem_ld32(tP + h2 * 32, dp);
+        tmem_wait_ld();
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const float w0 = pw[h2 * 32 + c], w1 = pw[h2 * 32 + c + 1];
+          float a0, a1;
+          f2_unpack(f2_mul(f2_pack(w0, w1), f2_sub(f2_pack(dp[c], dp[c + 1]), delta2)), a0, a1);
+          if (partial) {  // a padded key's V, a padded query's d_o may be NaN
+            a0 = w0 == 0.f ? 0.f : a0;
+            a1 = w1 == 0.f ? 0.f : a1;
+          }
+          pk[c / 2] = pack_bf16(a0, a1);
+        }
+        tmem_st16u(tP + h2 * 16, pk);  // over dP columns that this thread has read
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&ds_full[i & 1]);
+    }
+    const bool fin = ok && (n == 0 || mbar_wait_warp(done, 0, wctx, MCS_WHERE_ATTN_EPILOGUE));
+    if (fin) {
+      tc_fence_after();
+      // the two halves of the warps store the two halves of the columns
+      uint16_t* dst = p.dq + ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D + half * (D / 2);
+      store_row<D / 2>(tmem + lane_addr + 256 + half * (D / 2), n > 0, row_valid, p.scale, dst);
+    }
+    __syncwarp();
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
+    named_barrier_sync<1, kThreads>();
+  }
+  teardown(abort_flag, done, qg_full, n > 0 ? 1 + C::NK + C::NV : 0, tmem);
+}
+
+namespace {
+
+template <int D, bool MOD>
+cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk, const CUtensorMap* tv,
+                       const ExTile& p, cudaStream_t s) {
+  static KernelReady ready_kv, ready_q;
+  cudaError_t e = make_ready(ready_kv, ex_dkv_kernel<D, MOD>, DkvCfg<D>::SMEM + 8192, kLaunchRegs);
+  if (e != cudaSuccess) return e;
+  if ((e = make_ready(ready_q, ex_dq_kernel<D, MOD>, DqCfg<D>::SMEM + 1024, kLaunchRegs)) != cudaSuccess) return e;
+  const unsigned bits_q = p.k_ranges ? (p.Tq + 31) / 32 * 4u : 0u, bits_k = p.k_ranges ? (p.Tk + 31) / 32 * 4u : 0u;
+  ex_dkv_kernel<D, MOD><<<p.B * p.Hkv * p.Tk, kThreads, DkvCfg<D>::SMEM + bits_q, s>>>(*tq, *tg, *tk, *tv, p);
+  ex_dq_kernel<D, MOD><<<p.B * p.Hkv * p.Tq, kThreads, DqCfg<D>::SMEM + bits_k, s>>>(*tq, *tg, *tk, *tv, p);
+  note_launches(2);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_ex_row_stats(int d, const ExTile& p, const uint16_t* o, const uint16_t* d_o, const float* lse,
+                                float* stats, cudaStream_t s) {
+  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.Tq * 128;
+  const unsigned grid = static_cast<unsigned>(rows / 8);
+  if (d == 64) ex_row_stats<64><<<grid, 256, 0, s>>>(p, o, d_o, lse, stats);
+  else ex_row_stats<128><<<grid, 256, 0, s>>>(p, o, d_o, lse, stats);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ex_bwd(int d, const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk,
+                          const CUtensorMap* tv, const ExTile& p, cudaStream_t s) {
+  const bool mod = p.cap_k != 0.f || p.slopes;
+  if (d == 64) return mod ? launch_bwd<64, true>(tq, tg, tk, tv, p, s) : launch_bwd<64, false>(tq, tg, tk, tv, p, s);
+  return mod ? launch_bwd<128, true>(tq, tg, tk, tv, p, s) : launch_bwd<128, false>(tq, tg, tk, tv, p, s);
+}
+
+}  // namespace mcs

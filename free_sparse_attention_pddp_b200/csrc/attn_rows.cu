@@ -1,5 +1,5 @@
-// Attention with modified scores, one warp per row: the plainest form of
-// mcs_dense_bwd, mcs_decode and mcs_decode_shared.
+// Single tokens over a cache, one warp per row: the plainest form of
+// mcs_decode and mcs_decode_shared.
 //
 // A warp walks its row's partners 32 at a time. Lane l forms the score of
 // partner l (an fp32 dot product over d), the warp keeps a running maximum and
@@ -56,15 +56,6 @@ __device__ __forceinline__ float score(float x, float cap, float slope, float di
   return x - slope * dist;
 }
 
-__device__ __forceinline__ bool valid_pair(const ExParams& p, int b, int i, int j, int prefix) {
-  bool ok = !p.causal || j <= i + p.Nk - p.Nq || j < prefix;
-  if (p.doc_q) {
-    const int dq = p.doc_q[static_cast<size_t>(b) * p.Nq + i];
-    ok = ok && dq >= 0 && dq == p.doc_k[static_cast<size_t>(b) * p.Nk + j];
-  }
-  return ok;
-}
-
 template <int D>
 struct RowAcc {
   static constexpr int E = D / 32;  // columns of a lane
@@ -82,88 +73,6 @@ struct RowAcc {
     for (int e = 0; e < E; ++e) row[lane * E + e] = to_bf(a[e] * f);
   }
 };
-
-// delta[b,h,i] = sum_c d_o o
-template <int D>
-__global__ void rows_delta(const ExParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.B) * p.Nq * p.Hq) return;
-  float s = 0.f;
-  for (int c = lane; c < D; c += 32) s = fmaf(bf(p.d_o[row * D + c]), bf(p.o_in[row * D + c]), s);
-  s = warp_sum(s);
-  const int h = row % p.Hq, i = row / p.Hq % p.Nq, b = row / p.Hq / p.Nq;
-  if (lane == 0) p.delta[(static_cast<size_t>(b) * p.Hq + h) * p.Nq + i] = s;
-}
-
-template <int D>
-__global__ void rows_dq(const ExParams p) {
-  __shared__ float sq[kWarps][D], sg[kWarps][D];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * kWarps + w;
-  if (row >= static_cast<long long>(p.B) * p.Nq * p.Hq) return;
-  const int h = row % p.Hq, i = row / p.Hq % p.Nq, b = row / p.Hq / p.Nq;
-  for (int c = lane; c < D; c += 32) sq[w][c] = bf(p.q[row * D + c]), sg[w][c] = bf(p.d_o[row * D + c]);
-  __syncwarp();
-  const int hk = h / p.g, pos = i + p.Nk - p.Nq, prefix = p.prefix ? p.prefix[b] : 0;
-  const float slope = p.slopes ? p.slopes[h] : 0.f;
-  const size_t at = (static_cast<size_t>(b) * p.Hq + h) * p.Nq + i;
-  const float lse = p.lse_in[at], delta = p.delta[at];
-  RowAcc<D> acc;
-  for (int j0 = 0; j0 < p.Nk; j0 += 32) {
-    const int j = j0 + lane;
-    float ds = 0.f;
-    if (j < p.Nk && valid_pair(p, b, i, j, prefix)) {
-      const size_t kr = ((static_cast<size_t>(b) * p.Nk + j) * p.Hkv + hk) * D;
-      float t;
-      const float s = score(p.scale * dot<D>(sq[w], p.k + kr), p.cap, slope, fabsf(static_cast<float>(pos - j)), t);
-      ds = expf(s - lse) * (dot<D>(sg[w], p.v + kr) - delta) * (1.f - t * t);
-    }
-    for (int e = 0; e < 32 && j0 + e < p.Nk; ++e) {
-      const float de = __shfl_sync(0xffffffffu, ds, e);
-      if (de != 0.f) acc.add(de, p.k + ((static_cast<size_t>(b) * p.Nk + j0 + e) * p.Hkv + hk) * D, lane);
-    }
-  }
-  acc.store(p.dq + row * D, lane, p.scale);
-}
-
-template <int D>
-__global__ void rows_dkv(const ExParams p) {
-  __shared__ float sk[kWarps][D], sv[kWarps][D];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long key = static_cast<long long>(blockIdx.x) * kWarps + w;  // (b, j, hk)
-  if (key >= static_cast<long long>(p.B) * p.Nk * p.Hkv) return;
-  const int hk = key % p.Hkv, j = key / p.Hkv % p.Nk, b = key / p.Hkv / p.Nk;
-  for (int c = lane; c < D; c += 32) sk[w][c] = bf(p.k[key * D + c]), sv[w][c] = bf(p.v[key * D + c]);
-  __syncwarp();
-  const int prefix = p.prefix ? p.prefix[b] : 0;
-  RowAcc<D> dk, dv;
-  for (int h = hk * p.g; h < (hk + 1) * p.g; ++h) {
-    const float slope = p.slopes ? p.slopes[h] : 0.f;
-    for (int i0 = 0; i0 < p.Nq; i0 += 32) {
-      const int i = i0 + lane;
-      float pr = 0.f, ds = 0.f;
-      if (i < p.Nq && valid_pair(p, b, i, j, prefix)) {
-        const size_t qr = ((static_cast<size_t>(b) * p.Nq + i) * p.Hq + h) * D;
-        const size_t at = (static_cast<size_t>(b) * p.Hq + h) * p.Nq + i;
-        float t;
-        const float s = score(p.scale * dot<D>(sk[w], p.q + qr), p.cap, slope,
-                              fabsf(static_cast<float>(i + p.Nk - p.Nq - j)), t);
-        pr = expf(s - p.lse_in[at]);
-        ds = pr * (dot<D>(sv[w], p.d_o + qr) - p.delta[at]) * (1.f - t * t);
-      }
-      for (int e = 0; e < 32 && i0 + e < p.Nq; ++e) {
-        const float pe = __shfl_sync(0xffffffffu, pr, e), de = __shfl_sync(0xffffffffu, ds, e);
-        if (pe == 0.f) continue;
-        const size_t qr = ((static_cast<size_t>(b) * p.Nq + i0 + e) * p.Hq + h) * D;
-        dv.add(pe, p.d_o + qr, lane);
-        dk.add(de, p.q + qr, lane);
-      }
-    }
-  }
-  dk.store(p.dk + key * D, lane, p.scale);
-  dv.store(p.dv + key * D, lane, 1.f);
-}
 
 template <int D>
 __global__ void rows_decode(const DecodeParams p) {
@@ -209,21 +118,6 @@ __global__ void rows_decode(const DecodeParams p) {
 unsigned blocks(long long rows) { return static_cast<unsigned>((rows + kWarps - 1) / kWarps); }
 
 }  // namespace
-
-template <int D>
-static void rows_bwd(const ExParams& p, cudaStream_t s) {
-  const unsigned n = blocks(static_cast<long long>(p.B) * p.Nq * p.Hq);
-  rows_delta<D><<<n, kWarps * 32, 0, s>>>(p);
-  rows_dq<D><<<n, kWarps * 32, 0, s>>>(p);
-  rows_dkv<D><<<blocks(static_cast<long long>(p.B) * p.Nk * p.Hkv), kWarps * 32, 0, s>>>(p);
-}
-
-cudaError_t launch_ex_rows_bwd(int d, const ExParams& p, cudaStream_t s) {
-  if (d == 64) rows_bwd<64>(p, s);
-  else rows_bwd<128>(p, s);
-  note_launches(3);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_decode_rows(int d, const DecodeParams& p, cudaStream_t s) {
   const unsigned n = blocks(static_cast<long long>(p.B) * p.Hq);

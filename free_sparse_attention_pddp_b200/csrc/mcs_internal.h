@@ -126,13 +126,6 @@ struct ExParams {
   const float* slopes;         // [Hq] or null
   const int32_t* prefix;       // [B] or null
   const int32_t *doc_q, *doc_k;  // [B,Nq], [B,Nk] or null
-  const uint16_t *q, *k, *v;   // bf16
-  const uint16_t *o_in, *d_o;  // backward: the forward's output and its gradient
-  const float* lse_in;         // backward: the forward's lse
-  uint16_t* o;
-  float* lse;                  // nullable
-  uint16_t *dq, *dk, *dv;
-  float* delta;                // backward: sum_c d_o o per row, [B,Hq,Nq]
   int* status;
 };
 
@@ -154,6 +147,8 @@ struct ExTile {
   int P, C;
   uint16_t* o;                     // outputs, or the partials of the splits
   float* lse;
+  const float* stats;              // backward: [B,Hkv,Tq][2][128], -lse in log2 units and d_o . o
+  uint16_t *dq, *dk, *dv;
   float *part_o, *part_lse;        // [parts][B,Hkv,Tq,128](,d), lse in log2 units
   int* status;
   uint64_t wait_limit_ns;
@@ -163,6 +158,11 @@ struct ExTile {
 cudaError_t launch_ex_fwd(int d, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const ExTile& p,
                           cudaStream_t s);
 cudaError_t launch_ex_combine(int d, const ExTile& p, int parts, cudaStream_t s);
+// packed rows' statistics, then the gradients; tg: the map of d_o
+cudaError_t launch_ex_row_stats(int d, const ExTile& p, const uint16_t* o, const uint16_t* d_o, const float* lse,
+                                float* stats, cudaStream_t s);
+cudaError_t launch_ex_bwd(int d, const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk,
+                          const CUtensorMap* tv, const ExTile& p, cudaStream_t s);
 cudaError_t launch_ex_doc_tiles(const ExTile& p, int* k_ids, int4* k_ranges, int* q_ids, int4* q_ranges,
                                 cudaStream_t s);
 
@@ -177,7 +177,6 @@ struct DecodeParams {
   int* status;
 };
 
-cudaError_t launch_ex_rows_bwd(int d, const ExParams& p, cudaStream_t s);
 cudaError_t launch_decode_rows(int d, const DecodeParams& p, cudaStream_t s);
 
 // MCS_OK when the current device is an sm_100 GPU
