@@ -176,6 +176,54 @@ mcs_status check_decode(const mcs_decode_shape* s) {
   return MCS_OK;
 }
 
+// How single tokens fill the GPU. Two CTAs to an SM; the keys are cut so that
+// about eight waves of them cover the batch (lengths differ, and a late long
+// request should not run alone), in chunks of at least 256 keys, less only
+// where the batch would not fill one wave.
+struct DecodePlan {
+  int gsplit, chunk, nsplit;
+  FwdPlan pre;
+};
+
+DecodePlan decode_plan(const mcs_decode_shape* s) {
+  DecodePlan f{};
+  const int g = s->Hq / s->Hkv;
+  f.gsplit = (g + 31) / 32;
+  const long long jobs = static_cast<long long>(s->B) * s->Hkv * f.gsplit, slots = 2 * kSms;
+  auto cut = [&](long long ctas) {  // chunk for about `ctas` CTAs, whole blocks of the four warps
+    const long long per_job = std::max(1ll, ctas / jobs);
+    return ((s->C + per_job - 1) / per_job + 63) / 64 * 64;
+  };
+  f.chunk = static_cast<int>(std::max(64ll, std::max(cut(8 * slots), std::min(256ll, cut(slots)))));
+  f.nsplit = (s->C + f.chunk - 1) / f.chunk;
+  if (s->P > 0) f.pre = fwd_plan(1, s->Hkv, g, s->B, s->P, s->d);
+  return f;
+}
+
+// workspace: status | parts of the cache's keys | parts of the prefix
+struct DecodeWs {
+  size_t part_lse, part_o, pre_lse, pre_o, total;
+};
+
+DecodeWs decode_layout(const DecodePlan& f, const mcs_decode_shape* s) {
+  DecodeWs w;
+  size_t off = MCS_STATUS_BYTES;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  const bool parts = f.nsplit > 1 || s->P > 0;
+  const size_t rows = parts ? static_cast<size_t>(s->B) * s->Hq * f.nsplit : 0;
+  const size_t pre = s->P > 0 ? static_cast<size_t>(f.pre.parts) * s->Hkv * f.pre.Tq * 128 : 0;
+  w.part_lse = take(rows * 4);
+  w.part_o = take(rows * s->d * 4);
+  w.pre_lse = take(pre * 4);
+  w.pre_o = take(pre * s->d * 4);
+  w.total = off;
+  return w;
+}
+
 mcs_status decode_call(const mcs_decode_shape* s, const void* q, const void* kp, const void* vp, const void* k,
                        const void* v, const int32_t* lens, const float* slopes, void* o, float* lse, void* ws,
                        size_t ws_bytes, cudaStream_t stream) {
@@ -183,16 +231,19 @@ mcs_status decode_call(const mcs_decode_shape* s, const void* q, const void* kp,
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(kp) || !aligned16(vp) ||
       !aligned4(lens) || !aligned4(slopes) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return MCS_ERR_INVALID_ARG;
-  if (ws_bytes < mcs_decode_workspace_bytes(s)) return MCS_ERR_INVALID_ARG;
+  const DecodePlan f = decode_plan(s);
+  const DecodeWs w = decode_layout(f, s);
+  if (ws_bytes < w.total) return MCS_ERR_INVALID_ARG;
   const mcs_status st = check_device();
   if (st != MCS_OK) return st;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  const float scale = scale_of(s->scale, s->d);
   DecodeParams p{};
-  p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.g = s->Hq / s->Hkv; p.C = s->C; p.P = s->P;
-  p.scale = scale_of(s->scale, s->d);
-  p.cap = s->cap;
+  p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.g = s->Hq / s->Hkv; p.C = s->C;
+  p.nsplit = f.nsplit; p.chunk = f.chunk; p.gsplit = f.gsplit;
+  p.mul = static_cast<float>((s->cap > 0.f ? s->cap : scale) * 1.4426950408889634074);
+  p.cap_k = s->cap > 0.f ? scale / s->cap : 0.f;
   p.q = static_cast<const uint16_t*>(q);
-  p.kp = static_cast<const uint16_t*>(kp);
-  p.vp = static_cast<const uint16_t*>(vp);
   p.k = static_cast<const uint16_t*>(k);
   p.v = static_cast<const uint16_t*>(v);
   p.lens = lens;
@@ -200,7 +251,39 @@ mcs_status decode_call(const mcs_decode_shape* s, const void* q, const void* kp,
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
   p.status = static_cast<int*>(ws);
-  return launch_decode_rows(s->d, p, stream) == cudaSuccess ? MCS_OK : MCS_ERR_CUDA;
+  const bool parts = f.nsplit > 1 || s->P > 0;
+  if (parts) {
+    p.part_lse = reinterpret_cast<float*>(base + w.part_lse);
+    p.part_o = reinterpret_cast<float*>(base + w.part_o);
+  }
+  if (s->P > 0) {
+    // the prefix: one batch row whose tokens are the requests, every key valid
+    ExParams e{};
+    e.B = 1; e.Hq = s->Hq; e.Hkv = s->Hkv; e.g = p.g; e.Nq = s->B; e.Nk = s->P;
+    e.scale = scale;
+    e.cap = s->cap;
+    e.slopes = slopes;
+    e.status = p.status;
+    CUtensorMap tq, tk, tv;
+    if (tiles_map(&tq, q, 1, s->B, s->Hq, s->d, p.g, f.pre.tpt) != MCS_OK ||
+        tiles_map(&tk, kp, 1, s->P, s->Hkv, s->d, 1, 128) != MCS_OK ||
+        tiles_map(&tv, vp, 1, s->P, s->Hkv, s->d, 1, 128) != MCS_OK)
+      return MCS_ERR_CUDA;
+    ExTile t = tile_params(e, f.pre, s->d);
+    t.lens = lens;
+    t.P = s->P;
+    t.C = s->C;
+    t.part_lse = reinterpret_cast<float*>(base + w.pre_lse);
+    t.part_o = reinterpret_cast<float*>(base + w.pre_o);
+    if (launch_ex_fwd(s->d, &tq, &tk, &tv, t, stream) != cudaSuccess) return MCS_ERR_CUDA;
+    p.pre_lse = t.part_lse;
+    p.pre_o = t.part_o;
+    p.pre_parts = f.pre.parts;
+    p.pre_tiles = f.pre.Tq;
+    p.pre_tpt = f.pre.tpt;
+  }
+  if (launch_decode(s->d, p, stream) != cudaSuccess) return MCS_ERR_CUDA;
+  return parts ? ok_or_cuda(launch_decode_combine(s->d, p, stream)) : MCS_OK;
 }
 
 }  // namespace
@@ -305,7 +388,7 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
 
 size_t mcs_decode_workspace_bytes(const mcs_decode_shape* s) {
   if (check_decode(s) != MCS_OK) return 0;
-  return MCS_STATUS_BYTES;
+  return decode_layout(decode_plan(s), s).total;
 }
 
 mcs_status mcs_decode(const mcs_decode_shape* s, const void* q, const void* k, const void* v, const int32_t* lens,

@@ -167,17 +167,23 @@ cudaError_t launch_ex_doc_tiles(const ExTile& p, int* k_ids, int4* k_ranges, int
                                 cudaStream_t s);
 
 struct DecodeParams {
-  int B, Hq, Hkv, g, C, P;
-  float scale, cap;
-  const uint16_t *q, *kp, *vp, *k, *v;
+  int B, Hq, Hkv, g, C;
+  int nsplit, chunk;               // chunks of the keys, keys of a chunk
+  int gsplit;                      // parts of a head group (32 heads each)
+  float mul, cap_k;                // as in ExTile
+  const uint16_t *q, *k, *v;
   const int32_t* lens;
   const float* slopes;
   uint16_t* o;
   float* lse;
+  float *part_o, *part_lse;        // [B,Hq,nsplit](,d), lse in log2 units; null: o and lse directly
+  const float *pre_o, *pre_lse;    // the shared prefix's parts, in ExTile's layout
+  int pre_parts, pre_tiles, pre_tpt;
   int* status;
 };
 
-cudaError_t launch_decode_rows(int d, const DecodeParams& p, cudaStream_t s);
+cudaError_t launch_decode(int d, const DecodeParams& p, cudaStream_t s);
+cudaError_t launch_decode_combine(int d, const DecodeParams& p, cudaStream_t s);
 
 // MCS_OK when the current device is an sm_100 GPU
 mcs_status check_device();
