@@ -15,6 +15,19 @@
 
 namespace mcs {
 
+// CTA of the tile kernels: warp 0 issues the UMMAs, warp 1 the TMA loads, warp
+// 2 clears padded rows, warp 3 only completes their warpgroup; 16 softmax warps,
+// four to each SM sub-partition, so that one warp's TMEM loads, barriers and
+// dependent arithmetic hide behind the others' exponentials. (With 8 softmax
+// warps of twice the columns the forward kernel ran at 1004 instead of XXXX
+// TFLOP/s on 37 heads of 8192 tokens, d = 128.) setmaxnreg moves registers from
+// the first warpgroup to the softmax.
+constexpr int kExThreads = 640;
+constexpr int kExLaunchRegs = 96;
+constexpr int kExLowRegs = 64;
+constexpr int kExSoftRegs = 104;
+static_assert(128 * kExLowRegs + 512 * kExSoftRegs <= kExThreads * kExLaunchRegs, "register split");
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -113,6 +126,13 @@ __device__ __forceinline__ void tanh_scaled(float* s, float k) {
       s[c] = fabsf(x) <= 0.625f ? fmaf(x * z, p, x) : t;
     }
   }
+}
+
+// tanh_scaled over N values, 32 at a time
+template <int N>
+__device__ __forceinline__ void tanh_all(float* s, float k) {
+#pragma unroll
+  for (int c = 0; c < N; c += 32) tanh_scaled<32>(s + c, k);
 }
 
 // s[c] <- mul * s[c] - slope * |base - c * step| for c < N (log2 units). `base` is the

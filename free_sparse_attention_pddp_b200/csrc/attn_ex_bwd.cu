@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* count = reinterpret_cast<int*>(tmem_slot + 2);
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform to the compiler too
   const int lane = threadIdx.x & 31;
   // causal: the first key tiles meet the most queries and go first, the heads of a chunk side by side
   const int BH = p.B * p.Hkv;
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
     if (warp == 0) {
       // ---------------------------------------------------------------- UMMA issuer
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t IDESC_A = idesc_bf16_f32(128, D, false, true);
         const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024), dV = sdesc_sw128(smem_u32(sV), 16, 1024);
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------------- TMA producer
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_g);
         mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* count = reinterpret_cast<int*>(tmem_slot + 2);
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const int BH = p.B * p.Hkv;
   int qt, bh;
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
     if (warp == 0) {
       // ---------------------------------------------------------------- UMMA issuer
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t IDESC_A = idesc_bf16_f32(128, D, false, true);
         const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dG = sdesc_sw128(smem_u32(sG), 16, 1024);
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------------- TMA producer
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
         mbar_arrive_expect_tx(qg_full, 2 * C::KB * rt * 128);

@@ -4,11 +4,11 @@
 // TMEM).
 //
 // A CTA has two slots, each with a 128-row query tile, a score tile S, an
-// output accumulator O and a softmax warpgroup (one thread per row). The UMMA
+// output accumulator O and eight softmax warps. The UMMA
 // warp alternates between them,
 //   S_0(i) = Q_0 K^T | O_1 += P_1(i-1) V | S_1(i) = Q_1 K^T | O_0 += P_0(i) V,
 // so one slot's softmax runs while the tensor pipe computes the other's
-// products, as in attn_pair.cu. Two ways to fill the slots:
+// products. Two ways to fill the slots:
 //   pair    two consecutive query tiles that share every key tile;
 //   single  one query tile whose even key tiles go to slot 0 and odd ones to
 //           slot 1 (few rows over many keys); the halves are joined by
@@ -23,20 +23,18 @@
 // tiles whose range of ids cannot meet the query tiles' (bitmap built at the
 // start), and compares ids element by element in partial tiles only.
 //
-// Threads (384): warp 0 issues the UMMAs, warp 1 the TMA loads, warp 2 clears
-// the V rows of padded keys (document masks), warps 4-7 and 8-11 run the
-// softmax of slot 0 and 1. setmaxnreg moves registers to the softmax.
+// Softmax: eight warps per slot, two threads per row (64 keys of the tile each),
+// whose maxima meet in shared memory so that both use one running maximum.
 #include "attn_ex.cuh"
 
 namespace mcs {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168;
-constexpr int kLowRegs = 64;
-constexpr int kSoftRegs = 216;
-static_assert(128 * kLowRegs + 256 * kSoftRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kThreads = kExThreads;
+constexpr int kLaunchRegs = kExLaunchRegs;
+constexpr int kLowRegs = kExLowRegs;
+constexpr int kSoftRegs = kExSoftRegs;
 // A row's running maximum moves only when a tile exceeds it by this much in
 // log2 units (a factor 16): probabilities stay below 16, where bf16 is as exact
 // as below 1, and most tiles leave O alone.
@@ -51,9 +49,10 @@ struct FwdCfg {
   static constexpr uint32_t OFF_K = 2 * TILE;
   static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
   static constexpr uint32_t OFF_BAR = OFF_V + NS * TILE;
-  // q_full, k_full[NS], v_full[NS], v_ok[NS], kv_empty[NS], s_full[2], p_full[2], p_empty[2], drain
-  static constexpr uint32_t NBAR = 1 + 4 * NS + 2 + 2 + 2 + 1;
-  static constexpr uint32_t OFF_BITS = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;
+  // q_full, k_full[NS], v_full[NS], v_ok[NS], k_empty[NS], v_empty[NS], s_full[2], p_full[2], p_empty[2], drain
+  static constexpr uint32_t NBAR = 1 + 5 * NS + 2 + 2 + 2 + 1;
+  static constexpr uint32_t OFF_MAX = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;  // [parity][slot][half][row]
+  static constexpr uint32_t OFF_BITS = OFF_MAX + 2 * 2 * 2 * 128 * 8;
   static constexpr uint32_t SMEM = OFF_BITS + 1024;  // and 4 bytes for each 32 key tiles under a document mask
 };
 
@@ -73,17 +72,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_full = q_full + 1;           // [stage]
   uint64_t* v_full = k_full + C::NS;       // [stage]
   uint64_t* v_ok = v_full + C::NS;         // [stage]: V's padded rows are clear (document masks)
-  uint64_t* kv_empty = v_ok + C::NS;       // [stage]
-  uint64_t* s_full = kv_empty + C::NS;     // [slot]: S(i) computed
+  uint64_t* k_empty = v_ok + C::NS;        // [stage]: every S from it is computed
+  uint64_t* v_empty = k_empty + C::NS;     // [stage]: every O += P V from it is done
+  uint64_t* s_full = v_empty + C::NS;      // [slot]: S(i) computed
   uint64_t* p_full = s_full + 2;           // [slot]: P(i) written (and O rescaled)
   uint64_t* p_empty = p_full + 2;          // [slot]: O += P(i) V done
   uint64_t* drain_bar = p_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* count = reinterpret_cast<int*>(tmem_slot + 2);
+  float2* row_max = reinterpret_cast<float2*>(smem + C::OFF_MAX);
   uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform to the compiler too
   const int lane = threadIdx.x & 31;
   const bool single = p.single;
   const int per = single ? 1 : 2;  // query tiles of a CTA
@@ -131,11 +132,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&k_full[s], 1);
       mbar_init(&v_full[s], 1);
       mbar_init(&v_ok[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_empty[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 128);
+      mbar_init(&p_full[t], 256);
       mbar_init(&p_empty[t], 1);
     }
     mbar_init(drain_bar, 1);
@@ -167,13 +169,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n0 = single ? (n + 1) >> 1 : n;
   const int n1 = single ? n >> 1 : (has1 ? n : 0);
   const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
-  int issued = 0;
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
     if (warp == 0) {
       // ---------------------------------------------------------------- UMMA issuer
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false);
         constexpr uint32_t IDESC_O = idesc_bf16_f32(128, D, false, true);
         const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
@@ -195,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t dVs = sdesc_advance(dV, (j % C::NS) * C::TILE);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8, sdesc_advance(dVs, kk * 2048), IDESC_O,
+            umma_bf16_ts(tmem + 256 + t * D, tmem + t * 128 + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_advance(dVs, kk * 2048),
+                         IDESC_O,
                          (i > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&p_empty[t]);
         };
@@ -210,32 +212,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(&k_full[j0 % C::NS], j0 / C::NS)) break;
             tc_fence_after();
             issue_s(0, j0);
+            if (!has1) umma_commit(&k_empty[j0 % C::NS]);
           }
           if (i >= 1 && i - 1 < n1) {
             if (single && !wait(&v_bar[jp % C::NS], jp / C::NS)) break;
             if (!wait(&p_full[1], i - 1)) break;
             tc_fence_after();
             issue_o(1, i - 1, jp);
-            umma_commit(&kv_empty[jp % C::NS]);
+            umma_commit(&v_empty[jp % C::NS]);
           }
           if (i < n1) {
             if (single && !wait(&k_full[j1 % C::NS], j1 / C::NS)) break;
             tc_fence_after();
             issue_s(1, j1);
+            umma_commit(&k_empty[j1 % C::NS]);
           }
           if (i < n0) {
             if (!wait(&v_bar[j0 % C::NS], j0 / C::NS)) break;
             if (!wait(&p_full[0], i)) break;
             tc_fence_after();
             issue_o(0, i, j0);
-            if (!has1) umma_commit(&kv_empty[j0 % C::NS]);
+            if (!has1) umma_commit(&v_empty[j0 % C::NS]);
           }
         }
       }
       __syncwarp();
     } else if (warp == 1) {
       // ---------------------------------------------------------------- TMA producer
-      if (lane == 0 && n > 0) {
+      if (n > 0 && elect_one()) {
         prefetch_tensormap(&tm_q);
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
@@ -248,18 +252,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         TileIter it = first;
         for (int j = 0; j < n; ++j) {
           const int s = j % C::NS;
-          if (j >= C::NS && !mbar_wait(&kv_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
           const int kt = it.next();
           if ((p.debug_flags & 1) && j == 0) continue;  // test knob: never deliver tile 0
+          if (j >= C::NS && !mbar_wait(&k_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
           mbar_arrive_expect_tx(&k_full[s], C::TILE);
 #pragma unroll
           for (int kb = 0; kb < C::KB; ++kb)
             tma_load_4d(&tm_k, &k_full[s], sK + s * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
+          if (j >= C::NS && !mbar_wait(&v_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
           mbar_arrive_expect_tx(&v_full[s], C::TILE);
 #pragma unroll
           for (int kb = 0; kb < C::KB; ++kb)
             tma_load_4d(&tm_v, &v_full[s], sV + s * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
-          issued = j + 1;
         }
       }
       __syncwarp();
@@ -284,19 +288,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------------------------------------------------------- softmax + epilogue of slot t
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int t = (warp - 4) >> 2;
-    const int wq = warp & 3;  // TMEM lane quarter this warp may access
+    const int t = (warp - 4) >> 3;           // slot
+    const int half = ((warp - 4) >> 2) & 1;  // keys 64 half .. 64 half + 63 of each tile
+    const int wq = warp & 3;                 // TMEM lane quarter this warp may access
     const int row = wq * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_addr + t * 128;
-    const uint32_t tO = tmem + lane_addr + 256 + t * D;
+    const uint32_t tS = tmem + lane_addr + t * 128 + half * 64;
+    const uint32_t tO = tmem + lane_addr + 256 + t * D + half * (D / 2);  // this half's output columns
     const int nt = t == 0 ? n0 : n1;
     const int qt = single ? qt0 : qt0 + t;
     const int tok = qt * p.tpt + row / p.g;
     const int head = hk * p.g + row % p.g;
     const bool row_valid = row < rt && tok < p.Nq && (t == 0 || single || has1);
     const int pos = p.lens ? p.P + min(max(row_valid ? p.lens[tok] : 0, 0), p.C) - 1 : off + tok;
-    const int lim = limit(pos);
+    const int lim = limit(pos) - half * 64;
     const int lim_all = limit(off + qt * p.tpt);  // keys that every row of the tile sees
     const int4 mine = t == 0 || single ? r0 : r1;
     int my_doc = docs && row_valid ? p.doc_q[static_cast<size_t>(b) * p.Nq + tok] : -2;
@@ -305,29 +310,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool bias = MOD && p.slopes != nullptr;
     const float mul = bias ? 1.f : p.mul;  // what turns a transformed score into log2 units
     const uint64_t mul2 = f2_pack(mul, mul);
+    float2* my_max = row_max + (t * 2 + half) * 128 + row;
+    const float2* other_max = row_max + (t * 2 + (half ^ 1)) * 128 + row;
+    const int pair_bar = 2 + t * 4 + wq;  // the two warps that share these rows
     TileIter it = first;
     if (single && t == 1 && nt > 0) it.next();
-    float m = -CUDART_INF_F;  // running max, log2 units
-    float l = 0.f;
+    float m = -CUDART_INF_F;  // running max, log2 units (the same in both halves)
+    float l = 0.f;            // this half's sum
     bool ok = true;
     for (int i = 0; i < nt; ++i) {
       const int kt = it.next();
       if (single && i + 1 < nt) it.next();
-      if (!mbar_wait_warp(&s_full[t], i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
-        ok = false;
-        break;
-      }
+      ok = ok && mbar_wait_warp(&s_full[t], i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX);
       tc_fence_after();
-      float sv[128];
-#pragma unroll
-      for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(tS + c4 * 32, sv + c4 * 32);
+      float sv[64];  // after a failed wait: whatever the columns hold
+      tmem_ld32(tS, sv);
+      tmem_ld32(tS + 32, sv + 32);
       tmem_wait_ld();
       if (MOD) {
-        if (p.cap_k != 0.f) {
-#pragma unroll
-          for (int c4 = 0; c4 < 4; ++c4) tanh_scaled<32>(sv + c4 * 32, p.cap_k);
-        }
-        if (bias) add_bias<128>(sv, p.mul, slope, static_cast<float>(pos - kt * 128), 1.f);
+        if (p.cap_k != 0.f) tanh_all<64>(sv, p.cap_k);
+        if (bias) add_bias<64>(sv, p.mul, slope, static_cast<float>(pos - kt * 128 - half * 64), 1.f);
       }
       const int4* ids = nullptr;
       bool partial = (kt + 1) * 128 > lim_all;
@@ -335,14 +337,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t at = static_cast<size_t>(b) * p.Tk + kt;
         if (!docs_same(mine, p.k_ranges[at])) {
           partial = true;
-          ids = reinterpret_cast<const int4*>(p.k_ids + at * 128);
+          ids = reinterpret_cast<const int4*>(p.k_ids + at * 128) + half * 16;
         }
       }
       if (partial) {
         const int valid = lim - kt * 128;
         if (ids) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 4) {
+          for (int c = 0; c < 64; c += 4) {
             const int4 k4 = __ldg(ids + (c >> 2));  // padded keys hold -1, which no query's id equals
             sv[c] = (c < valid && k4.x == my_doc) ? sv[c] : -CUDART_INF_F;
             sv[c + 1] = (c + 1 < valid && k4.y == my_doc) ? sv[c + 1] : -CUDART_INF_F;
@@ -351,19 +353,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < 128; ++c) sv[c] = c < valid ? sv[c] : -CUDART_INF_F;
+          for (int c = 0; c < 64; ++c) sv[c] = c < valid ? sv[c] : -CUDART_INF_F;
         }
       }
-      float mc[8];
+      float mc[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 4; ++k) {
         float a = sv[k * 16];
 #pragma unroll
         for (int e = 1; e < 15; e += 2) a = fmax3(a, sv[k * 16 + e], sv[k * 16 + e + 1]);
         mc[k] = fmaxf(a, sv[k * 16 + 15]);
       }
-      const float mx =
-          fmaxf(fmax3(fmaxf(mc[0], mc[1]), mc[2], mc[3]), fmax3(fmaxf(mc[4], mc[5]), mc[6], mc[7])) * mul;
+      const float half_max = fmaxf(fmax3(mc[0], mc[1], mc[2]), mc[3]);
+      // Both warps meet here in every step, with the step's own word on whether their waits held, and leave the loop
+      // in the same step if one did not.
+      my_max[(i & 1) * 512] = make_float2(half_max, ok ? 0.f : 1.f);
+      asm volatile("barrier.sync %0, 64;" ::"r"(pair_bar) : "memory");
+      const float2 other = other_max[(i & 1) * 512];
+      ok = ok && other.y == 0.f;
+      if (!ok) break;
+      const float mx = fmaxf(half_max, other.x) * mul;
       // a row that has seen no valid key keeps m = -inf, l = 0 and P = 0
       const bool need = i == 0 ? mx > m : mx > m + kRescale;
       const bool rescale = i > 0 && __any_sync(0xffffffffu, need);
@@ -375,41 +384,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float ms = m == -CUDART_INF_F ? 0.f : m;
       const uint64_t negm = f2_pack(-ms, -ms);
 #pragma unroll
-      for (int q = 0; q < 64; ++q) {
-        float x0, x1;
-        f2_unpack(f2_fma(f2_pack(sv[2 * q], sv[2 * q + 1]), mul2, negm), x0, x1);
-        sv[2 * q] = fast_exp2(x0);
-        sv[2 * q + 1] = fast_exp2(x1);
-      }
-#pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
-        uint32_t pk[32];
+        uint32_t pk[16];
+        float* v = sv + 32 * h2;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) pk[c] = pack_bf16(sv[64 * h2 + 2 * c], sv[64 * h2 + 2 * c + 1]);
-        tmem_st32u(tS + h2 * 32, pk);
+        for (int q = 0; q < 16; ++q) {
+          float x0, x1;
+          f2_unpack(f2_fma(f2_pack(v[2 * q], v[2 * q + 1]), mul2, negm), x0, x1);
+          v[2 * q] = fast_exp2(x0);
+          v[2 * q + 1] = fast_exp2(x1);
+          pk[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
+        }
+        tmem_st16u(tS + h2 * 16, pk);
       }
-      uint64_t acc[32];
+      {
+        uint64_t a[16];
 #pragma unroll
-      for (int q = 0; q < 32; ++q)
-        acc[q] = f2_add(f2_pack(sv[2 * q], sv[2 * q + 1]), f2_pack(sv[2 * q + 64], sv[2 * q + 65]));
+        for (int q = 0; q < 16; ++q)
+          a[q] = f2_add(f2_pack(sv[2 * q], sv[2 * q + 1]), f2_pack(sv[2 * q + 32], sv[2 * q + 33]));
 #pragma unroll
-      for (int w = 16; w >= 1; w >>= 1) {
+        for (int w = 8; w >= 1; w >>= 1) {
 #pragma unroll
-        for (int q = 0; q < w; ++q) acc[q] = f2_add(acc[q], acc[q + w]);
+          for (int q = 0; q < w; ++q) a[q] = f2_add(a[q], a[q + w]);
+        }
+        float s0, s1;
+        f2_unpack(a[0], s0, s1);
+        l = l * alpha + (s0 + s1);
       }
-      float s0, s1;
-      f2_unpack(acc[0], s0, s1);
-      l = l * alpha + (s0 + s1);
       tmem_wait_st();
       if (rescale) {
         // scale O once O += P(i-1) V is done; O += P(i) V waits for p_full
-        if (!mbar_wait_warp(&p_empty[t], (i - 1) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
-          ok = false;
-          break;
-        }
+        ok = mbar_wait_warp(&p_empty[t], (i - 1) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX);
+        if (!ok) continue;  // the other half learns of it in the next step
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 64; ++c) {
           float ov[32];
           tmem_ld32(tO + c * 32, ov);
           tmem_wait_ld();
@@ -424,6 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // ---------------------------------------------------------------- epilogue of slot t
     const bool fin = ok && (nt == 0 || mbar_wait_warp(&p_empty[t], (nt - 1) & 1, wctx, MCS_WHERE_ATTN_EPILOGUE));
+    // the row's sum: both halves', exchanged like the maxima (every warp takes part, whatever happened)
+    // a loop left early wrote the other parity's words
+    my_max[(nt & 1) * 512] = make_float2(l, 0.f);
+    asm volatile("barrier.sync %0, 64;" ::"r"(pair_bar) : "memory");
+    l += other_max[(nt & 1) * 512].x;
     if (fin && (t == 0 || single || has1)) {
       tc_fence_after();
       const bool partial = p.part_o != nullptr;
@@ -431,14 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float lse2 = l > 0.f ? m + log2f(l) : -CUDART_INF_F;
       const size_t bht = static_cast<size_t>(bh) * p.Tq + qt;
       const size_t slice = static_cast<size_t>(single ? 2 * split + t : split) * BH * p.Tq;
-      if (row_valid) {
+      if (row_valid && half == 0) {
         if (partial) p.part_lse[(slice + bht) * 128 + row] = lse2;
         else if (p.lse) p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok] = lse2 * kLn2;
       }
-      uint16_t* orow = p.o + ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D;
-      float* prow = p.part_o + ((slice + bht) * 128 + row) * D;
+      uint16_t* orow = p.o + ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D + half * (D / 2);
+      float* prow = p.part_o + ((slice + bht) * 128 + row) * D + half * (D / 2);
 #pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc) {
+      for (int cc = 0; cc < D / 64; ++cc) {
         float ov[32];
         if (nt > 0) {
           tmem_ld32(tO + cc * 32, ov);
@@ -461,6 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+    // the softmax warps return their registers before the first warpgroup takes its own back
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
     named_barrier_sync<1, kThreads>();
   }
@@ -472,11 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (*abort_flag) {
     volatile int never = 0;
     const WaitCtx drain_ctx{&never, nullptr, 50000000ull};
-    if (threadIdx.x == 32) {
-      if (n > 0) mbar_wait(q_full, 0, drain_ctx, MCS_WHERE_DRAIN);
-      for (int j = max(0, issued - C::NS); j < issued; ++j) {
-        mbar_wait(&k_full[j % C::NS], (j / C::NS) & 1, drain_ctx, MCS_WHERE_DRAIN);
-        mbar_wait(&v_full[j % C::NS], (j / C::NS) & 1, drain_ctx, MCS_WHERE_DRAIN);
+    if (threadIdx.x == 32 && n > 0) {
+      // both parities of every load barrier: the phase that a load in flight completes is one of the two
+      for (int j = 0; j < 1 + 2 * C::NS; ++j) {
+        mbar_wait(&q_full[j], 0, drain_ctx, MCS_WHERE_DRAIN);
+        mbar_wait(&q_full[j], 1, drain_ctx, MCS_WHERE_DRAIN);
       }
     }
     if (warp == 0 && lane == 0) {

@@ -273,6 +273,14 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
+// True in one lane of a converged warp. The compiler knows that one thread runs
+// what this guards, so the operands of the UMMAs inside stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
 // Warp-converged forms: every lane of the issuing warp executes these and only
 // lanes with `issue` set (one lane) issue the operation. Keeping the UMMA warp
 // converged, rather than running one lane while the other 31 wait at a warp
