@@ -19,20 +19,18 @@
 //     S = Q K^T, dP = d_o V^T, dS over dP, dQ += dS K. S(i+1) and dP(i+1) are
 //     computed while the softmax works on tile i (dP has two buffers).
 //
-// Threads (384) as in the forward kernel: warp 0 UMMA, warp 1 TMA, warp 2
-// clears padded rows (document masks), warps 4-7 and 8-11 the two halves of a
-// tile's columns, one thread per row and half.
+// Four threads work on a row of a tile, 32 of its columns each.
 #include "attn_ex.cuh"
 
 namespace mcs {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168;
-constexpr int kLowRegs = 64;
-constexpr int kSoftRegs = 216;
-static_assert(128 * kLowRegs + 256 * kSoftRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kThreads = kExThreads;
+constexpr int kLaunchRegs = kExLaunchRegs;
+constexpr int kLowRegs = kExLowRegs;
+constexpr int kSoftRegs = kExSoftRegs;
+constexpr int kSoftThreads = 512;
 
 template <int D>
 struct DkvCfg {
@@ -46,8 +44,8 @@ struct DkvCfg {
   static constexpr uint32_t OFF_STAT = OFF_G + NS * TILE;     // [stage]: -lse (log2 units) [128], D [128]
   static constexpr uint32_t OFF_ROW = OFF_STAT + NS * 1024;   // slope [128], token in the tile [128]
   static constexpr uint32_t OFF_BAR = OFF_ROW + 1024;
-  // kv_full, q_full[NS], q_ok[NS], q_empty[NS], s_full, dp_full, p_full, ds_full, done
-  static constexpr uint32_t NBAR = 1 + 3 * NS + 5;
+  // kv_full, q_full[NS], g_full[NS], qg_ok[NS], q_empty[NS], g_empty[NS], s_full, dp_full, p_full, ds_full, done
+  static constexpr uint32_t NBAR = 1 + 5 * NS + 5;
   static constexpr uint32_t OFF_BITS = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;
   static constexpr uint32_t SMEM = OFF_BITS + 1024;
 };
@@ -78,22 +76,24 @@ __device__ __forceinline__ void zero_tail_rows(uint8_t* tile, int tiles, int rt)
   }
 }
 
-// Stores one thread's TMEM row of D fp32 columns, times f, as bf16.
-template <int D>
+// Stores N fp32 columns of one thread's TMEM row, times f, as bf16.
+template <int N>
 __device__ __forceinline__ void store_row(uint32_t taddr, bool have, bool valid, float f, uint16_t* dst) {
+  constexpr int W = N < 32 ? N : 32;
 #pragma unroll
-  for (int cc = 0; cc < D / 32; ++cc) {
-    float v[32];
+  for (int cc = 0; cc < N / W; ++cc) {
+    float v[W];
     if (have) {
-      tmem_ld32(taddr + cc * 32, v);
+      if constexpr (W == 32) tmem_ld32(taddr + cc * 32, v);
+      else tmem_ld16(taddr, v);
       tmem_wait_ld();
     }
     if (!valid) continue;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = have ? v[e] * f : 0.f;
+    for (int e = 0; e < W; ++e) v[e] = have ? v[e] * f : 0.f;
     uint4* d4 = reinterpret_cast<uint4*>(dst + cc * 32);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int e = 0; e < W / 8; ++e)
       d4[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
                          pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
   }
@@ -177,10 +177,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* row_slope = reinterpret_cast<float*>(smem + C::OFF_ROW);
   float* row_tok = row_slope + 128;
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* q_full = kv_full + 1;        // [stage]: Q, d_o and statistics
-  uint64_t* q_ok = q_full + C::NS;       // [stage]: padded rows are clear (document masks)
-  uint64_t* q_empty = q_ok + C::NS;      // [stage]
-  uint64_t* s_full = q_empty + C::NS;
+  uint64_t* q_full = kv_full + 1;        // [stage]: Q and the statistics
+  uint64_t* g_full = q_full + C::NS;     // [stage]: d_o
+  uint64_t* qg_ok = g_full + C::NS;      // [stage]: padded rows of both are clear (document masks)
+  uint64_t* q_empty = qg_ok + C::NS;     // [stage]
+  uint64_t* g_empty = q_empty + C::NS;   // [stage]
+  uint64_t* s_full = g_empty + C::NS;
   uint64_t* dp_full = s_full + 1;
   uint64_t* p_full = dp_full + 1;
   uint64_t* ds_full = p_full + 1;
@@ -220,13 +222,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(kv_full, 1);
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(&q_full[s], 1);
-      mbar_init(&q_ok[s], 1);
+      mbar_init(&g_full[s], 1);
+      mbar_init(&qg_ok[s], 1);
       mbar_init(&q_empty[s], 1);
+      mbar_init(&g_empty[s], 1);
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    mbar_init(p_full, 256);
-    mbar_init(ds_full, 256);
+    mbar_init(p_full, kSoftThreads);
+    mbar_init(ds_full, kSoftThreads);
     mbar_init(done, 1);
     *abort_flag = 0;
     *count = 0;
@@ -276,15 +280,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto accumulate = [&](uint32_t acc, uint32_t from, uint64_t bb, int i) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(acc, from + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_advance(bb, kk * 2048), IDESC_A,
+            umma_bf16_ts(acc, from + (kk >> 1) * 32 + (kk & 1) * 8, sdesc_advance(bb, kk * 2048), IDESC_A,
                          (i > 0 || kk > 0) ? 1u : 0u);
         };
         auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
-        uint64_t* ready = docs ? q_ok : q_full;
-        bool ok = wait(kv_full, 0) && wait(&ready[0], 0);
+        uint64_t* q_ready = docs ? qg_ok : q_full;
+        uint64_t* g_ready = docs ? qg_ok : g_full;
+        bool ok = wait(kv_full, 0) && wait(&q_ready[0], 0);
         if (ok) {
           tc_fence_after();
           scores(tmem, dK, dQ, s_full);
+          ok = wait(&g_ready[0], 0);
+        }
+        if (ok) {
+          tc_fence_after();
           scores(tmem + 128, dV, dG, dp_full);
         }
         for (int i = 0; ok && i < n; ++i) {
@@ -292,8 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(p_full, i)) break;
           tc_fence_after();
           accumulate(tmem + 256, tmem, sdesc_advance(dGm, at), i);
+          umma_commit(&g_empty[i % C::NS]);
           if (i + 1 < n) {
-            if (!wait(&ready[(i + 1) % C::NS], (i + 1) / C::NS)) break;
+            if (!wait(&q_ready[(i + 1) % C::NS], (i + 1) / C::NS)) break;
             tc_fence_after();
             scores(tmem, dK, sdesc_advance(dQ, nx), s_full);
           }
@@ -301,8 +311,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           accumulate(tmem + 384, tmem + 128, sdesc_advance(dQm, at), i);
           umma_commit(&q_empty[i % C::NS]);
-          if (i + 1 < n) scores(tmem + 128, dV, sdesc_advance(dG, nx), dp_full);
-          else umma_commit(done);
+          if (i + 1 < n) {
+            if (!wait(&g_ready[(i + 1) % C::NS], (i + 1) / C::NS)) break;
+            tc_fence_after();
+            scores(tmem + 128, dV, sdesc_advance(dG, nx), dp_full);
+          } else {
+            umma_commit(done);
+          }
         }
       }
       __syncwarp();
@@ -320,17 +335,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         TileIter it = first;
         for (int j = 0; j < n; ++j) {
           const int s = j % C::NS;
-          if (j >= C::NS && !mbar_wait(&q_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
           const int qt = it.next();
           if ((p.debug_flags & 1) && j == 0) continue;  // test knob: never deliver tile 0
-          mbar_arrive_expect_tx(&q_full[s], 2 * C::KB * rt * 128 + 1024);
+          if (j >= C::NS && !mbar_wait(&q_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+          mbar_arrive_expect_tx(&q_full[s], C::KB * rt * 128 + 1024);
 #pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb) {
+          for (int kb = 0; kb < C::KB; ++kb)
             tma_load_4d(&tm_q, &q_full[s], sQ + s * C::TILE + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
-            tma_load_4d(&tm_g, &q_full[s], sG + s * C::TILE + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
-          }
           bulk_load(&q_full[s], smem + C::OFF_STAT + s * 1024, p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256,
                     1024);
+          if (j >= C::NS && !mbar_wait(&g_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+          mbar_arrive_expect_tx(&g_full[s], C::KB * rt * 128);
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb)
+            tma_load_4d(&tm_g, &g_full[s], sG + s * C::TILE + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
         }
       }
       __syncwarp();
@@ -339,7 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       TileIter it = first;
       for (int j = 0; j < n; ++j) {
         const int s = j % C::NS;
-        if (!mbar_wait_warp(&q_full[s], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+        if (!mbar_wait_warp(&q_full[s], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER) ||
+            !mbar_wait_warp(&g_full[s], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER))
+          break;
         const size_t at = static_cast<size_t>(b) * p.Tq + it.next();
         if (p.q_ranges[at].z) {
           zero_padded_rows<C::KB>(sQ + s * C::TILE, p.q_ids + at * 128);
@@ -347,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_ok[s]);
+        if (lane == 0) mbar_arrive(&qg_ok[s]);
       }
       __syncwarp();
     }
@@ -356,29 +376,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------------------------------------------------------- P and dS, then the epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int half = (warp - 4) >> 2;  // query rows 64 half .. 64 half + 63 of each tile
+    const int quarter = (warp - 4) >> 2;  // query rows 32 quarter .. 32 quarter + 31 of each tile
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
     const int key = kt * 128 + row;
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_addr + half * 64;
-    const uint32_t tP = tmem + lane_addr + 128 + half * 64;
+    const uint32_t tS = tmem + lane_addr + quarter * 32;
+    const uint32_t tP = tS + 128;
     const bool key_valid = key < p.Nk;
     const int my_doc = docs ? p.k_ids[(static_cast<size_t>(b) * p.Tk + kt) * 128 + row] : 0;  // padding: -1
     const bool all_rows = !p.causal || key < prefix;
     const bool all_keys = !p.causal || kt * 128 + 127 < prefix;
+    const bool cap = MOD && p.cap_k != 0.f;
     const bool bias = MOD && p.slopes != nullptr;
-    const uint64_t mul2 = f2_pack(p.mul, p.mul);
+    const float mul = bias ? 1.f : p.mul;
+    const uint64_t mul2 = f2_pack(mul, mul);
+    const float4* tok4 = reinterpret_cast<const float4*>(row_tok) + quarter * 8;
+    const float4* sl4 = reinterpret_cast<const float4*>(row_slope) + quarter * 8;
     TileIter it = first;
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const int s = i % C::NS;
       const int qt = it.next();
-      const float4* nl4 = reinterpret_cast<const float4*>(smem + C::OFF_STAT + s * 1024) + half * 16;
+      const float4* nl4 = reinterpret_cast<const float4*>(smem + C::OFF_STAT + s * 1024) + quarter * 8;
       const float4* dl4 = nl4 + 32;
-      const float4* tok4 = reinterpret_cast<const float4*>(row_tok) + half * 16;
-      const float4* sl4 = reinterpret_cast<const float4*>(row_slope) + half * 16;
-      // this key's position in the tile's tokens: token c sees it when c >= at
+      // this key's place among the tile's tokens: token c sees it when c >= at
       const int at_i = key - off - qt * p.tpt;
       const float at = static_cast<float>(at_i);
       const int4* ids = nullptr;
@@ -387,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t q_at = static_cast<size_t>(b) * p.Tq + qt;
         if (!docs_same(mine, p.q_ranges[q_at])) {
           partial = true;
-          ids = reinterpret_cast<const int4*>(p.q_ids + q_at * 128) + half * 16;
+          ids = reinterpret_cast<const int4*>(p.q_ids + q_at * 128) + quarter * 8;
         }
       }
       // the statistics of this stage, then the scores
@@ -397,66 +419,86 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      float pw[64];  // score, then P (1 - t^2)
-      tmem_ld32(tS, pw);
-      tmem_ld32(tS + 32, pw + 32);
+      float pv[32];  // score, P, then P (1 - t^2)
+      float w[32];   // 1 - t^2
+      tmem_ld32(tS, pv);
       tmem_wait_ld();
-      if (MOD && p.cap_k != 0.f) {
-        tanh_scaled<32>(pw, p.cap_k);
-        tanh_scaled<32>(pw + 32, p.cap_k);
-      }
-      const bool after = bias && __all_sync(0xffffffffu, at_i <= 0);              // every token at or after the key
-      const bool before = bias && __all_sync(0xffffffffu, at_i >= p.tpt - 1);     // every token at or before it
+      if (cap) {
+        tanh_scaled<32>(pv, p.cap_k);
 #pragma unroll
-      for (int h2 = 0; h2 < 2; ++h2) {
+        for (int c = 0; c < 32; c += 2) {
+          const uint64_t t2 = f2_pack(pv[c], pv[c + 1]);
+          f2_unpack(f2_fma(f2_mul(t2, f2_pack(-1.f, -1.f)), t2, f2_pack(1.f, 1.f)), w[c], w[c + 1]);
+        }
+      }
+      if (bias) {
+        const bool after = __all_sync(0xffffffffu, at_i <= 0);           // every token at or after the key
+        const bool before = __all_sync(0xffffffffu, at_i >= p.tpt - 1);  // every token at or before it
+        const float sign = before ? -1.f : 1.f;
+        const uint64_t pm2 = f2_pack(p.mul, p.mul);
+        if (after || before) {
+          const uint64_t sg2 = f2_pack(sign, sign), off2 = f2_pack(-sign * at, -sign * at);
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 tk = tok4[c >> 2], sl = sl4[c >> 2];
+            // slope times sign (token - key), the distance
+            const uint64_t d01 = f2_mul(f2_pack(-sl.x, -sl.y), f2_fma(f2_pack(tk.x, tk.y), sg2, off2));
+            const uint64_t d23 = f2_mul(f2_pack(-sl.z, -sl.w), f2_fma(f2_pack(tk.z, tk.w), sg2, off2));
+            f2_unpack(f2_fma(f2_pack(pv[c], pv[c + 1]), pm2, d01), pv[c], pv[c + 1]);
+            f2_unpack(f2_fma(f2_pack(pv[c + 2], pv[c + 3]), pm2, d23), pv[c + 2], pv[c + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 tk = tok4[c >> 2], sl = sl4[c >> 2];
+            pv[c] = fmaf(pv[c], p.mul, -sl.x * fabsf(tk.x - at));
+            pv[c + 1] = fmaf(pv[c + 1], p.mul, -sl.y * fabsf(tk.y - at));
+            pv[c + 2] = fmaf(pv[c + 2], p.mul, -sl.z * fabsf(tk.z - at));
+            pv[c + 3] = fmaf(pv[c + 3], p.mul, -sl.w * fabsf(tk.w - at));
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 nl = nl4[c >> 2];
+        float x0, x1, x2, x3;
+        f2_unpack(f2_fma(f2_pack(pv[c], pv[c + 1]), mul2, f2_pack(nl.x, nl.y)), x0, x1);
+        f2_unpack(f2_fma(f2_pack(pv[c + 2], pv[c + 3]), mul2, f2_pack(nl.z, nl.w)), x2, x3);
+        pv[c] = fast_exp2(x0);
+        pv[c + 1] = fast_exp2(x1);
+        pv[c + 2] = fast_exp2(x2);
+        pv[c + 3] = fast_exp2(x3);
+      }
+      if (partial) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 tk = tok4[c >> 2];
+          int4 id = make_int4(my_doc, my_doc, my_doc, my_doc);
+          if (ids) id = __ldg(ids + (c >> 2));  // padded queries hold -2, which no key's id equals
+          const bool v0 = (all_rows || tk.x >= at) && id.x == my_doc, v1 = (all_rows || tk.y >= at) && id.y == my_doc;
+          const bool v2 = (all_rows || tk.z >= at) && id.z == my_doc, v3 = (all_rows || tk.w >= at) && id.w == my_doc;
+          pv[c] = v0 ? pv[c] : 0.f;
+          pv[c + 1] = v1 ? pv[c + 1] : 0.f;
+          pv[c + 2] = v2 ? pv[c + 2] : 0.f;
+          pv[c + 3] = v3 ? pv[c + 3] : 0.f;
+          if (cap) {  // a padded key's scores may be NaN
+            w[c] = v0 ? w[c] : 0.f;
+            w[c + 1] = v1 ? w[c + 1] : 0.f;
+            w[c + 2] = v2 ? w[c + 2] : 0.f;
+            w[c + 3] = v3 ? w[c + 3] : 0.f;
+          }
+        }
+      }
+      {
         uint32_t pk[16];
 #pragma unroll
-        for (int c = 32 * h2; c < 32 * h2 + 32; c += 4) {
-          const float4 nl = nl4[c >> 2];
-          uint64_t e01 = f2_pack(nl.x, nl.y), e23 = f2_pack(nl.z, nl.w);
-          if (bias) {
-            const float4 tk = tok4[c >> 2], sl = sl4[c >> 2];
-            float d0 = at - tk.x, d1 = at - tk.y, d2 = at - tk.z, d3 = at - tk.w;  // -(distance) where after
-            if (before) d0 = -d0, d1 = -d1, d2 = -d2, d3 = -d3;
-            else if (!after) d0 = -fabsf(d0), d1 = -fabsf(d1), d2 = -fabsf(d2), d3 = -fabsf(d3);
-            e01 = f2_fma(f2_pack(sl.x, sl.y), f2_pack(d0, d1), e01);
-            e23 = f2_fma(f2_pack(sl.z, sl.w), f2_pack(d2, d3), e23);
-          }
-          float x0, x1, x2, x3;
-          f2_unpack(f2_fma(f2_pack(pw[c], pw[c + 1]), mul2, e01), x0, x1);
-          f2_unpack(f2_fma(f2_pack(pw[c + 2], pw[c + 3]), mul2, e23), x2, x3);
-          float p0 = fast_exp2(x0), p1 = fast_exp2(x1), p2 = fast_exp2(x2), p3 = fast_exp2(x3);
-          float w0 = p0, w1 = p1, w2 = p2, w3 = p3;
-          if (MOD && p.cap_k != 0.f) {
-            w0 = fmaf(-pw[c] * p0, pw[c], p0);
-            w1 = fmaf(-pw[c + 1] * p1, pw[c + 1], p1);
-            w2 = fmaf(-pw[c + 2] * p2, pw[c + 2], p2);
-            w3 = fmaf(-pw[c + 3] * p3, pw[c + 3], p3);
-          }
-          if (partial) {
-            const float4 tk = tok4[c >> 2];
-            bool v0 = all_rows || tk.x >= at, v1 = all_rows || tk.y >= at;
-            bool v2 = all_rows || tk.z >= at, v3 = all_rows || tk.w >= at;
-            if (ids) {
-              const int4 id = __ldg(ids + (c >> 2));  // padded queries hold -2, which no key's id equals
-              v0 = v0 && id.x == my_doc;
-              v1 = v1 && id.y == my_doc;
-              v2 = v2 && id.z == my_doc;
-              v3 = v3 && id.w == my_doc;
-            }
-            p0 = v0 ? p0 : 0.f, w0 = v0 ? w0 : 0.f;
-            p1 = v1 ? p1 : 0.f, w1 = v1 ? w1 : 0.f;
-            p2 = v2 ? p2 : 0.f, w2 = v2 ? w2 : 0.f;
-            p3 = v3 ? p3 : 0.f, w3 = v3 ? w3 : 0.f;
-          }
-          pk[(c - 32 * h2) / 2] = pack_bf16(p0, p1);
-          pk[(c - 32 * h2) / 2 + 1] = pack_bf16(p2, p3);
-          pw[c] = w0;
-          pw[c + 1] = w1;
-          pw[c + 2] = w2;
-          pw[c + 3] = w3;
-        }
-        tmem_st16u(tS + h2 * 16, pk);
+        for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(pv[2 * c], pv[2 * c + 1]);
+        tmem_st16u(tS, pk);  // over scores that this thread has read
+      }
+      if (cap) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2)
+          f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_pack(w[c], w[c + 1])), pv[c], pv[c + 1]);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -466,29 +508,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
+      tmem_ld32(tP, w);
+      tmem_wait_ld();
 #pragma unroll
-      for (int h2 = 0; h2 < 2; ++h2) {
-        float dp[32];
-        tmem_ld32(tP + h2 * 32, dp);
-        tmem_wait_ld();
+      for (int c = 0; c < 32; c += 4) {
+        const float4 dl = dl4[c >> 2];
+        f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_sub(f2_pack(w[c], w[c + 1]), f2_pack(dl.x, dl.y))), w[c],
+                  w[c + 1]);
+        f2_unpack(f2_mul(f2_pack(pv[c + 2], pv[c + 3]), f2_sub(f2_pack(w[c + 2], w[c + 3]), f2_pack(dl.z, dl.w))),
+                  w[c + 2], w[c + 3]);
+      }
+      if (partial) {  // a padded key's V may be NaN
+#pragma unroll
+        for (int c = 0; c < 32; ++c) w[c] = pv[c] == 0.f ? 0.f : w[c];
+      }
+      {
         uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 dl = dl4[h2 * 8 + (c >> 2)];
-          const float* w = pw + h2 * 32 + c;
-          float a0, a1, a2, a3;
-          f2_unpack(f2_mul(f2_pack(w[0], w[1]), f2_sub(f2_pack(dp[c], dp[c + 1]), f2_pack(dl.x, dl.y))), a0, a1);
-          f2_unpack(f2_mul(f2_pack(w[2], w[3]), f2_sub(f2_pack(dp[c + 2], dp[c + 3]), f2_pack(dl.z, dl.w))), a2, a3);
-          if (partial) {  // a padded key's V may be NaN
-            a0 = w[0] == 0.f ? 0.f : a0;
-            a1 = w[1] == 0.f ? 0.f : a1;
-            a2 = w[2] == 0.f ? 0.f : a2;
-            a3 = w[3] == 0.f ? 0.f : a3;
-          }
-          pk[c / 2] = pack_bf16(a0, a1);
-          pk[c / 2 + 1] = pack_bf16(a2, a3);
-        }
-        tmem_st16u(tP + h2 * 16, pk);  // over dP columns that this thread has read
+        for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(w[2 * c], w[2 * c + 1]);
+        tmem_st16u(tP, pk);
       }
       tmem_wait_st();
       tc_fence_before();
@@ -498,14 +536,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (fin) {
       tc_fence_after();
       const size_t at = ((static_cast<size_t>(b) * p.Nk + key) * p.Hkv + hk) * D;
-      if (half == 0) store_row<D>(tmem + lane_addr + 256, n > 0, key_valid, 1.f, p.dv + at);
-      else store_row<D>(tmem + lane_addr + 384, n > 0, key_valid, p.scale, p.dk + at);
+      // quarters 0 and 1 store the two halves of dV's columns, 2 and 3 those of dK's
+      const int c0 = (quarter & 1) * (D / 2);
+      if (quarter < 2) store_row<D / 2>(tmem + lane_addr + 256 + c0, n > 0, key_valid, 1.f, p.dv + at + c0);
+      else store_row<D / 2>(tmem + lane_addr + 384 + c0, n > 0, key_valid, p.scale, p.dk + at + c0);
     }
     __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
     named_barrier_sync<1, kThreads>();
   }
-  teardown(abort_flag, done, kv_full, n > 0 ? 1 + C::NS : 0, tmem);
+  teardown(abort_flag, done, kv_full, n > 0 ? 1 + 2 * C::NS : 0, tmem);
 }
 
 template <int D, bool MOD>
@@ -571,10 +611,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_empty[s], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_read, 256);
+    mbar_init(s_read, kSoftThreads);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&dp_full[s], 1);
-      mbar_init(&ds_full[s], 256);
+      mbar_init(&ds_full[s], kSoftThreads);
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -598,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const TileIter first{docs ? bits : nullptr, 0, 0};
   const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
   // TMEM: S | dP 0 | dQ | dP 1
-  const uint32_t tm_dp[2] = {tmem + 128, tmem + 384};
+  auto dp_buf = [&](int i) { return tmem + ((i & 1) ? 384u : 128u); };
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
@@ -628,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           scores(tmem, dQ, sdesc_advance(dK, (j % C::NK) * C::TILE), s_full);
           if (!wait(&v_full[j % C::NV], j / C::NV)) return false;
           tc_fence_after();
-          scores(tm_dp[j & 1], dG, sdesc_advance(dV, (j % C::NV) * C::TILE), &dp_full[j & 1]);
+          scores(dp_buf(j), dG, sdesc_advance(dV, (j % C::NV) * C::TILE), &dp_full[j & 1]);
           umma_commit(&v_empty[j % C::NV]);
           return true;
         };
@@ -640,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t bb = sdesc_advance(dKm, (i % C::NK) * C::TILE);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(tmem + 256, tm_dp[i & 1] + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_advance(bb, kk * 2048),
+            umma_bf16_ts(tmem + 256, dp_buf(i) + (kk >> 1) * 32 + (kk & 1) * 8, sdesc_advance(bb, kk * 2048),
                          IDESC_A, (i > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&k_empty[i % C::NK]);
           if (i + 1 == n) umma_commit(done);
@@ -698,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------------------------------------------------------- dS, then the epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    const int half = (warp - 4) >> 2;  // keys 64 half .. 64 half + 63 of each tile
+    const int quarter = (warp - 4) >> 2;  // keys 32 quarter .. 32 quarter + 31 of each tile
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
@@ -709,12 +749,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float negl = st[row], delta = st[128 + row];
     const uint64_t negl2 = f2_pack(negl, negl), delta2 = f2_pack(delta, delta);
     const int pos = off + tok;
-    const int lim = limit(pos);
+    const int lim = limit(pos) - quarter * 32;
     const int lim_all = limit(off + qt * p.tpt);
     const int my_doc = docs ? p.q_ids[(static_cast<size_t>(b) * p.Tq + qt) * 128 + row] : 0;  // padding: -2
+    const bool cap = MOD && p.cap_k != 0.f;
     const bool bias = MOD && p.slopes != nullptr;
-    const float slope = bias ? p.slopes[head < p.Hq ? head : 0] * kLog2e : 0.f;
-    const float mul = p.mul;
+    const float slope = bias && row_valid ? p.slopes[head] * kLog2e : 0.f;
+    const float mul = bias ? 1.f : p.mul;
     const uint64_t mul2 = f2_pack(mul, mul);
     TileIter it = first;
     bool ok = true;
@@ -726,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const size_t at = static_cast<size_t>(b) * p.Tk + kt;
         if (!docs_same(mine, p.k_ranges[at])) {
           partial = true;
-          ids = reinterpret_cast<const int4*>(p.k_ids + at * 128) + half * 16;
+          ids = reinterpret_cast<const int4*>(p.k_ids + at * 128) + quarter * 8;
         }
       }
       if (!mbar_wait_warp(s_full, i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
@@ -734,79 +775,68 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      float pw[64];
-      tmem_ld32(tmem + lane_addr + half * 64, pw);
-      tmem_ld32(tmem + lane_addr + half * 64 + 32, pw + 32);
+      float pv[32];  // score, P, then P (1 - t^2)
+      float w[32];   // 1 - t^2
+      tmem_ld32(tmem + lane_addr + quarter * 32, pv);
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(s_read);
-      if (MOD && p.cap_k != 0.f) {
-        tanh_scaled<32>(pw, p.cap_k);
-        tanh_scaled<32>(pw + 32, p.cap_k);
-      }
-      const int valid = lim - kt * 128 - half * 64;
-      const float base = static_cast<float>(pos - kt * 128 - half * 64);
-      const bool after = bias && __all_sync(0xffffffffu, base >= 63.f);
-      const bool before = bias && __all_sync(0xffffffffu, base <= 0.f);
+      if (cap) {
+        tanh_scaled<32>(pv, p.cap_k);
 #pragma unroll
-      for (int c = 0; c < 64; c += 2) {
-        uint64_t e = negl2;
-        if (bias) {
-          float d0 = static_cast<float>(c) - base, d1 = static_cast<float>(c + 1) - base;  // -(distance) where after
-          if (before) d0 = -d0, d1 = -d1;
-          else if (!after) d0 = -fabsf(d0), d1 = -fabsf(d1);
-          e = f2_fma(f2_pack(slope, slope), f2_pack(d0, d1), e);
+        for (int c = 0; c < 32; c += 2) {
+          const uint64_t t2 = f2_pack(pv[c], pv[c + 1]);
+          f2_unpack(f2_fma(f2_mul(t2, f2_pack(-1.f, -1.f)), t2, f2_pack(1.f, 1.f)), w[c], w[c + 1]);
         }
+      }
+      if (bias) add_bias<32>(pv, p.mul, slope, static_cast<float>(pos - kt * 128 - quarter * 32), 1.f);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
         float x0, x1;
-        f2_unpack(f2_fma(f2_pack(pw[c], pw[c + 1]), mul2, e), x0, x1);
-        float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-        if (MOD && p.cap_k != 0.f) {
-          p0 = fmaf(-pw[c] * p0, pw[c], p0);
-          p1 = fmaf(-pw[c + 1] * p1, pw[c + 1], p1);
-        }
-        pw[c] = p0;
-        pw[c + 1] = p1;
+        f2_unpack(f2_fma(f2_pack(pv[c], pv[c + 1]), mul2, negl2), x0, x1);
+        pv[c] = fast_exp2(x0);
+        pv[c + 1] = fast_exp2(x1);
+      }
+      if (cap) {
+#pragma unroll
+        for (int c = 0; c < 32; c += 2)
+          f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_pack(w[c], w[c + 1])), pv[c], pv[c + 1]);
       }
       if (partial) {
+        const int valid = lim - kt * 128;
         if (ids) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
+          for (int c = 0; c < 32; c += 4) {
             const int4 id = __ldg(ids + (c >> 2));
-            pw[c] = (c < valid && id.x == my_doc) ? pw[c] : 0.f;
-            pw[c + 1] = (c + 1 < valid && id.y == my_doc) ? pw[c + 1] : 0.f;
-            pw[c + 2] = (c + 2 < valid && id.z == my_doc) ? pw[c + 2] : 0.f;
-            pw[c + 3] = (c + 3 < valid && id.w == my_doc) ? pw[c + 3] : 0.f;
+            pv[c] = (c < valid && id.x == my_doc) ? pv[c] : 0.f;
+            pv[c + 1] = (c + 1 < valid && id.y == my_doc) ? pv[c + 1] : 0.f;
+            pv[c + 2] = (c + 2 < valid && id.z == my_doc) ? pv[c + 2] : 0.f;
+            pv[c + 3] = (c + 3 < valid && id.w == my_doc) ? pv[c + 3] : 0.f;
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) pw[c] = c < valid ? pw[c] : 0.f;
+          for (int c = 0; c < 32; ++c) pv[c] = c < valid ? pv[c] : 0.f;
         }
       }
-      const uint32_t tP = tm_dp[i & 1] + lane_addr + half * 64;
+      const uint32_t tP = dp_buf(i) + lane_addr + quarter * 32;
       if (!mbar_wait_warp(&dp_full[i & 1], (i >> 1) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      tmem_ld32(tP, w);
+      tmem_wait_ld();
 #pragma unroll
-      for (int h2 = 0; h2 < 2; ++h2) {
-        float dp[32];
-        tmem_ld32(tP + h2 * 32, dp);
-        tmem_wait_ld();
-        uint32_t pk[16];
+      for (int c = 0; c < 32; c += 2)
+        f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_sub(f2_pack(w[c], w[c + 1]), delta2)), w[c], w[c + 1]);
+      if (partial) {  // a padded key's V, a padded query's d_o may be NaN
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const float w0 = pw[h2 * 32 + c], w1 = pw[h2 * 32 + c + 1];
-          float a0, a1;
-          f2_unpack(f2_mul(f2_pack(w0, w1), f2_sub(f2_pack(dp[c], dp[c + 1]), delta2)), a0, a1);
-          if (partial) {  // a padded key's V, a padded query's d_o may be NaN
-            a0 = w0 == 0.f ? 0.f : a0;
-            a1 = w1 == 0.f ? 0.f : a1;
-          }
-          pk[c / 2] = pack_bf16(a0, a1);
-        }
-        tmem_st16u(tP + h2 * 16, pk);  // over dP columns that this thread has read
+        for (int c = 0; c < 32; ++c) w[c] = pv[c] == 0.f ? 0.f : w[c];
       }
+      uint32_t pk[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(w[2 * c], w[2 * c + 1]);
+      tmem_st16u(tP, pk);  // over dP columns that this thread has read
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&ds_full[i & 1]);
@@ -814,9 +844,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool fin = ok && (n == 0 || mbar_wait_warp(done, 0, wctx, MCS_WHERE_ATTN_EPILOGUE));
     if (fin) {
       tc_fence_after();
-      // the two halves of the warps store the two halves of the columns
-      uint16_t* dst = p.dq + ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D + half * (D / 2);
-      store_row<D / 2>(tmem + lane_addr + 256 + half * (D / 2), n > 0, row_valid, p.scale, dst);
+      // each quarter of the warps stores its quarter of the columns
+      const int c0 = quarter * (D / 4);
+      uint16_t* dst = p.dq + ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D + c0;
+      store_row<D / 4>(tmem + lane_addr + 256 + c0, n > 0, row_valid, p.scale, dst);
     }
     __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
