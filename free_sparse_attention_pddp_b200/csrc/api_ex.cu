@@ -358,12 +358,14 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
   const BwdWs w = bwd_layout(f, p.B, p.Hkv);
   uint8_t* base = static_cast<uint8_t*>(ws);
   CUtensorMap tq, tg, tk, tv;
-  if (tiles_map(&tq, q, p.B, p.Nq, p.Hq, s->d, p.g, f.tpt) != MCS_OK ||
-      tiles_map(&tg, d_o, p.B, p.Nq, p.Hq, s->d, p.g, f.tpt) != MCS_OK ||
+  const int qbox = 64 % p.g == 0 ? f.tpt / 2 : f.tpt;
+  if (tiles_map(&tq, q, p.B, p.Nq, p.Hq, s->d, p.g, qbox) != MCS_OK ||
+      tiles_map(&tg, d_o, p.B, p.Nq, p.Hq, s->d, p.g, qbox) != MCS_OK ||
       tiles_map(&tk, k, p.B, p.Nk, p.Hkv, s->d, 1, 128) != MCS_OK ||
       tiles_map(&tv, v, p.B, p.Nk, p.Hkv, s->d, 1, 128) != MCS_OK)
     return MCS_ERR_CUDA;
   ExTile t = tile_params(p, f, s->d);
+  t.qbox = qbox;
   t.dq = static_cast<uint16_t*>(dq);
   t.dk = static_cast<uint16_t*>(dk);
   t.dv = static_cast<uint16_t*>(dv);

@@ -13,8 +13,12 @@
 //     summed in the accumulators). Scores are computed transposed, keys on
 //     TMEM lanes: S^T = K Q^T, dP^T = V d_o^T. P^T and dS^T (bf16) overwrite
 //     them and are the TS-form A operands of dV += P^T d_o, dK += dS^T Q.
-//     UMMA order dV(i) S(i+1) dK(i) dP(i+1): the softmax's two phases of a tile
-//     (P from S, dS from dP) each run beside two products.
+//     The tile's two halves of 64 query rows take turns, each with its own
+//     columns of S^T and dP^T: dV_h(i) S_h(i+1) dK_h(i) dP_h(i+1) for h = 0, 1, so
+//     that a half's chain (P from S, dS from dP, and their barriers) runs beside
+//     the other half's products. With whole tiles in one chain the tensor pipe
+//     waited 1500 of every 3500 cycles; halves cost the N = 64 products 48
+//     cycles for 32 cycles of work.
 //   ex_dq_kernel: a CTA owns one packed query tile and streams key tiles:
 //     S = Q K^T, dP = d_o V^T, dS over dP, dQ += dS K. S(i+1) and dP(i+1) are
 //     computed while the softmax works on tile i (dP has two buffers).
@@ -44,8 +48,9 @@ struct DkvCfg {
   static constexpr uint32_t OFF_STAT = OFF_G + NS * TILE;     // [stage]: -lse (log2 units) [128], D [128]
   static constexpr uint32_t OFF_ROW = OFF_STAT + NS * 1024;   // slope [128], token in the tile [128]
   static constexpr uint32_t OFF_BAR = OFF_ROW + 1024;
-  // kv_full, q_full[NS], g_full[NS], qg_ok[NS], q_empty[NS], g_empty[NS], s_full, dp_full, p_full, ds_full, done
-  static constexpr uint32_t NBAR = 1 + 5 * NS + 5;
+  // kv_full, q_full[NS][2], g_full[NS][2], q_empty[NS][2], g_empty[NS][2], qg_ok[NS], s_full[2], dp_full[2],
+  // p_full[2], ds_full[2], done
+  static constexpr uint32_t NBAR = 1 + 9 * NS + 9;
   static constexpr uint32_t OFF_BITS = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;
   static constexpr uint32_t SMEM = OFF_BITS + 1024;
 };
@@ -177,16 +182,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* row_slope = reinterpret_cast<float*>(smem + C::OFF_ROW);
   float* row_tok = row_slope + 128;
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* q_full = kv_full + 1;        // [stage]: Q and the statistics
-  uint64_t* g_full = q_full + C::NS;     // [stage]: d_o
-  uint64_t* qg_ok = g_full + C::NS;      // [stage]: padded rows of both are clear (document masks)
-  uint64_t* q_empty = qg_ok + C::NS;     // [stage]
-  uint64_t* g_empty = q_empty + C::NS;   // [stage]
-  uint64_t* s_full = g_empty + C::NS;
-  uint64_t* dp_full = s_full + 1;
-  uint64_t* p_full = dp_full + 1;
-  uint64_t* ds_full = p_full + 1;
-  uint64_t* done = ds_full + 1;
+  uint64_t* q_full = kv_full + 1;           // [stage][half of the tile's rows]: Q and the statistics
+  uint64_t* g_full = q_full + 2 * C::NS;    // [stage][half]: d_o
+  uint64_t* q_empty = g_full + 2 * C::NS;   // [stage][half]
+  uint64_t* g_empty = q_empty + 2 * C::NS;  // [stage][half]
+  uint64_t* qg_ok = g_empty + 2 * C::NS;    // [stage]: padded rows of Q and d_o are clear (document masks)
+  uint64_t* s_full = qg_ok + C::NS;         // [half], as the next three
+  uint64_t* dp_full = s_full + 2;
+  uint64_t* p_full = dp_full + 2;
+  uint64_t* ds_full = p_full + 2;
+  uint64_t* done = ds_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* count = reinterpret_cast<int*>(tmem_slot + 2);
@@ -217,20 +222,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
   const int4 mine = docs ? p.k_ranges[static_cast<size_t>(b) * p.Tk + kt] : none;
   const int rt = p.tpt * p.g;
+  const bool halves = p.qbox < p.tpt;  // a tile loads as two boxes of 64 rows
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
     for (int s = 0; s < C::NS; ++s) {
-      mbar_init(&q_full[s], 1);
-      mbar_init(&g_full[s], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&q_full[2 * s + h], 1);
+        mbar_init(&g_full[2 * s + h], 1);
+        mbar_init(&q_empty[2 * s + h], 1);
+        mbar_init(&g_empty[2 * s + h], 1);
+      }
       mbar_init(&qg_ok[s], 1);
-      mbar_init(&q_empty[s], 1);
-      mbar_init(&g_empty[s], 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(dp_full, 1);
-    mbar_init(p_full, kSoftThreads);
-    mbar_init(ds_full, kSoftThreads);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&s_full[h], 1);
+      mbar_init(&dp_full[h], 1);
+      mbar_init(&p_full[h], kSoftThreads / 2);
+      mbar_init(&ds_full[h], kSoftThreads / 2);
+    }
     mbar_init(done, 1);
     *abort_flag = 0;
     *count = 0;
@@ -262,12 +272,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // ---------------------------------------------------------------- UMMA issuer
       if (n > 0 && elect_one()) {
-        constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 128, false, false);
+        constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64, false, false);
         constexpr uint32_t IDESC_A = idesc_bf16_f32(128, D, false, true);
         const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024), dV = sdesc_sw128(smem_u32(sV), 16, 1024);
         const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024), dG = sdesc_sw128(smem_u32(sG), 16, 1024);
         const uint64_t dQm = sdesc_sw128(smem_u32(sQ), 16384, 1024), dGm = sdesc_sw128(smem_u32(sG), 16384, 1024);
-        // D[tmem] = A B^T over d, both K-major
+        // 64 columns at `to` = A B^T over d (both K-major), B the 64 query rows at `bb`
         auto scores = [&](uint32_t to, uint64_t a, uint64_t bb, uint64_t* bar) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -276,47 +286,51 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           umma_commit(bar);
         };
-        // acc += A^T-form (bf16 over the score tile at `from`) times the rows of a tile
-        auto accumulate = [&](uint32_t acc, uint32_t from, uint64_t bb, int i) {
+        // acc += (the bf16 tile over the 64 score columns at `from`) times the 64 query rows at `bb`
+        auto accumulate = [&](uint32_t acc, uint32_t from, uint64_t bb, bool start) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 0; kk < 4; ++kk)
             umma_bf16_ts(acc, from + (kk >> 1) * 32 + (kk & 1) * 8, sdesc_advance(bb, kk * 2048), IDESC_A,
-                         (i > 0 || kk > 0) ? 1u : 0u);
+                         (!start || kk > 0) ? 1u : 0u);
         };
         auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
-        uint64_t* q_ready = docs ? qg_ok : q_full;
-        uint64_t* g_ready = docs ? qg_ok : g_full;
-        bool ok = wait(kv_full, 0) && wait(&q_ready[0], 0);
-        if (ok) {
+        // Q or d_o of list entry j, half h
+        auto ready = [&](uint64_t* full, int j, int h) {
+          const int s = j % C::NS;
+          const bool there = wait(docs ? &qg_ok[s] : &full[halves ? 2 * s + h : 2 * s], j / C::NS);
           tc_fence_after();
-          scores(tmem, dK, dQ, s_full);
-          ok = wait(&g_ready[0], 0);
-        }
-        if (ok) {
-          tc_fence_after();
-          scores(tmem + 128, dV, dG, dp_full);
+          return there;
+        };
+        bool ok = wait(kv_full, 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || !(ok = ready(q_full, 0, h))) break;
+          scores(tmem + h * 64, dK, sdesc_advance(dQ, h * 8192), &s_full[h]);
+          if (!(ok = ready(g_full, 0, h))) break;
+          scores(tmem + 128 + h * 64, dV, sdesc_advance(dG, h * 8192), &dp_full[h]);
         }
         for (int i = 0; ok && i < n; ++i) {
           const uint32_t at = (i % C::NS) * C::TILE, nx = ((i + 1) % C::NS) * C::TILE;
-          if (!wait(p_full, i)) break;
-          tc_fence_after();
-          accumulate(tmem + 256, tmem, sdesc_advance(dGm, at), i);
-          umma_commit(&g_empty[i % C::NS]);
-          if (i + 1 < n) {
-            if (!wait(&q_ready[(i + 1) % C::NS], (i + 1) / C::NS)) break;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!(ok = wait(&p_full[h], i))) break;
             tc_fence_after();
-            scores(tmem, dK, sdesc_advance(dQ, nx), s_full);
-          }
-          if (!wait(ds_full, i)) break;
-          tc_fence_after();
-          accumulate(tmem + 384, tmem + 128, sdesc_advance(dQm, at), i);
-          umma_commit(&q_empty[i % C::NS]);
-          if (i + 1 < n) {
-            if (!wait(&g_ready[(i + 1) % C::NS], (i + 1) / C::NS)) break;
+            accumulate(tmem + 256, tmem + h * 64, sdesc_advance(dGm, at + h * 8192), i == 0 && h == 0);
+            umma_commit(&g_empty[2 * (i % C::NS) + h]);
+            if (i + 1 < n) {
+              if (!(ok = ready(q_full, i + 1, h))) break;
+              scores(tmem + h * 64, dK, sdesc_advance(dQ, nx + h * 8192), &s_full[h]);
+            }
+            if (!(ok = wait(&ds_full[h], i))) break;
             tc_fence_after();
-            scores(tmem + 128, dV, sdesc_advance(dG, nx), dp_full);
-          } else {
-            umma_commit(done);
+            accumulate(tmem + 384, tmem + 128 + h * 64, sdesc_advance(dQm, at + h * 8192), i == 0 && h == 0);
+            umma_commit(&q_empty[2 * (i % C::NS) + h]);
+            if (i + 1 < n) {
+              if (!(ok = ready(g_full, i + 1, h))) break;
+              scores(tmem + 128 + h * 64, dV, sdesc_advance(dG, nx + h * 8192), &dp_full[h]);
+            } else if (h == 1) {
+              umma_commit(done);
+            }
           }
         }
       }
@@ -333,22 +347,44 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_4d(&tm_v, kv_full, sV + kb * 16384, kb * 64, hk, kt * 128, b);
         }
         TileIter it = first;
-        for (int j = 0; j < n; ++j) {
+        bool ok = true;
+        for (int j = 0; j < n && ok; ++j) {
           const int s = j % C::NS;
           const int qt = it.next();
           if ((p.debug_flags & 1) && j == 0) continue;  // test knob: never deliver tile 0
-          if (j >= C::NS && !mbar_wait(&q_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
-          mbar_arrive_expect_tx(&q_full[s], C::KB * rt * 128 + 1024);
+          const uint32_t parity = ((j / C::NS) & 1) ^ 1;
+          const float* stats = p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
+          uint8_t* sS = smem + C::OFF_STAT + s * 1024;
+          auto free = [&](uint64_t* empty, int h) {
+            return j < C::NS || mbar_wait(&empty[2 * s + h], parity, wctx, MCS_WHERE_ATTN_PRODUCER);
+          };
+          auto box = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int h) {
 #pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_4d(&tm_q, &q_full[s], sQ + s * C::TILE + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
-          bulk_load(&q_full[s], smem + C::OFF_STAT + s * 1024, p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256,
-                    1024);
-          if (j >= C::NS && !mbar_wait(&g_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
-          mbar_arrive_expect_tx(&g_full[s], C::KB * rt * 128);
+            for (int kb = 0; kb < C::KB; ++kb)
+              tma_load_4d(map, bar, dst + s * C::TILE + kb * 16384 + h * 8192, kb * 64, hk * p.g,
+                          qt * p.tpt + h * p.qbox, b);
+          };
+          if (halves) {
 #pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_4d(&tm_g, &g_full[s], sG + s * C::TILE + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
+            for (int h = 0; h < 2 && ok; ++h) {
+              if (!(ok = free(q_empty, h))) break;
+              mbar_arrive_expect_tx(&q_full[2 * s + h], C::KB * 8192 + 512);
+              box(&tm_q, &q_full[2 * s + h], sQ, h);
+              bulk_load(&q_full[2 * s + h], sS + h * 256, stats + h * 64, 256);
+              bulk_load(&q_full[2 * s + h], sS + 512 + h * 256, stats + 128 + h * 64, 256);
+              if (!(ok = free(g_empty, h))) break;
+              mbar_arrive_expect_tx(&g_full[2 * s + h], C::KB * 8192);
+              box(&tm_g, &g_full[2 * s + h], sG, h);
+            }
+          } else {  // a half's border cuts a token: the first half's barriers take the whole tile
+            if (!(ok = free(q_empty, 0) && free(q_empty, 1))) break;
+            mbar_arrive_expect_tx(&q_full[2 * s], C::KB * rt * 128 + 1024);
+            box(&tm_q, &q_full[2 * s], sQ, 0);
+            bulk_load(&q_full[2 * s], sS, stats, 1024);
+            if (!(ok = free(g_empty, 0) && free(g_empty, 1))) break;
+            mbar_arrive_expect_tx(&g_full[2 * s], C::KB * rt * 128);
+            box(&tm_g, &g_full[2 * s], sG, 0);
+          }
         }
       }
       __syncwarp();
@@ -357,9 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       TileIter it = first;
       for (int j = 0; j < n; ++j) {
         const int s = j % C::NS;
-        if (!mbar_wait_warp(&q_full[s], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER) ||
-            !mbar_wait_warp(&g_full[s], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER))
-          break;
+        bool there = true;
+        for (int h = 0; h < (halves ? 2 : 1) && there; ++h)
+          there = mbar_wait_warp(&q_full[2 * s + h], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER) &&
+                  mbar_wait_warp(&g_full[2 * s + h], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER);
+        if (!there) break;
         const size_t at = static_cast<size_t>(b) * p.Tq + it.next();
         if (p.q_ranges[at].z) {
           zero_padded_rows<C::KB>(sQ + s * C::TILE, p.q_ids + at * 128);
@@ -377,6 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- P and dS, then the epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int quarter = (warp - 4) >> 2;  // query rows 32 quarter .. 32 quarter + 31 of each tile
+    const int half = quarter >> 1;
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
     const int key = kt * 128 + row;
@@ -413,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // the statistics of this stage, then the scores
-      if (!mbar_wait_warp(&q_full[s], (i / C::NS) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX) ||
-          !mbar_wait_warp(s_full, i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
+      if (!mbar_wait_warp(&q_full[halves ? 2 * s + half : 2 * s], (i / C::NS) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX) ||
+          !mbar_wait_warp(&s_full[half], i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
         ok = false;
         break;
       }
@@ -502,8 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(p_full);
-      if (!mbar_wait_warp(dp_full, i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
+      mbar_arrive(&p_full[half]);
+      if (!mbar_wait_warp(&dp_full[half], i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
         ok = false;
         break;
       }
@@ -530,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(ds_full);
+      mbar_arrive(&ds_full[half]);
     }
     const bool fin = ok && (n == 0 || mbar_wait_warp(done, 0, wctx, MCS_WHERE_ATTN_EPILOGUE));
     if (fin) {
@@ -545,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
     named_barrier_sync<1, kThreads>();
   }
-  teardown(abort_flag, done, kv_full, n > 0 ? 1 + 2 * C::NS : 0, tmem);
+  teardown(abort_flag, done, kv_full, n > 0 ? 1 + 4 * C::NS : 0, tmem);
 }
 
 template <int D, bool MOD>
@@ -694,10 +733,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&tm_v);
         mbar_arrive_expect_tx(qg_full, 2 * C::KB * rt * 128);
 #pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb) {
-          tma_load_4d(&tm_q, qg_full, sQ + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
-          tma_load_4d(&tm_g, qg_full, sG + kb * 16384, kb * 64, hk * p.g, qt * p.tpt, b);
-        }
+        for (int kb = 0; kb < C::KB; ++kb)
+          for (int h = 0; h < p.tpt / p.qbox; ++h) {
+            const int tok = qt * p.tpt + h * p.qbox;
+            tma_load_4d(&tm_q, qg_full, sQ + kb * 16384 + h * 8192, kb * 64, hk * p.g, tok, b);
+            tma_load_4d(&tm_g, qg_full, sG + kb * 16384 + h * 8192, kb * 64, hk * p.g, tok, b);
+          }
         TileIter it = first;
         for (int j = 0; j < n; ++j) {
           const int sk = j % C::NK, sv = j % C::NV;

@@ -132,6 +132,7 @@ struct ExParams {
 // The tile kernels' view of a call (attn_ex_fwd.cu, attn_ex_bwd.cu).
 struct ExTile {
   int B, Hq, Hkv, g, tpt, Nq, Nk;  // tpt: tokens of a packed query tile
+  int qbox;                        // backward: tokens of a query map's box, tpt or (64 rows) tpt / 2
   int Tq, Tk;                      // query and key tiles
   int nsplit, single, chunk;       // forward: key splits, one-tile CTAs, heads per chunk of the work order
   float mul;                       // log2 units per transformed score: scale log2 e, or cap log2 e
