@@ -55,6 +55,27 @@ mcs_status check_opts(const mcs_attn_shape* s, const mcs_attn_opts* o) {
 
 float scale_of(float scale, int d) { return scale > 0.f ? scale : static_cast<float>(1.0 / sqrt(static_cast<double>(d))); }
 
+CapFn cap_fn(float scale, float cap) {
+  CapFn f{};
+  if (!(cap > 0.f)) return f;
+  f.on = 1;
+  const double k = static_cast<double>(scale) / cap, cl = cap * 1.4426950408889634074;
+  f.k = static_cast<float>(k);
+  f.cl = static_cast<float>(cl);
+  const double p3[5] = {1.0, kTanhP0, kTanhP1, kTanhP2, kTanhP3}, p2[4] = {1.0, kTanhR0, kTanhR1, kTanhR2};
+  bool fits = true;
+  double pow = cl * k;
+  for (int i = 0; i < 5; ++i, pow *= k * k) {
+    f.a[i] = static_cast<float>(p3[i] * pow);
+    fits = fits && finite(f.a[i]);
+    if (i < 4) f.b[i] = static_cast<float>(p2[i] * pow);
+  }
+  f.z2 = fits ? static_cast<float>((0.4 / k) * (0.4 / k)) : -1.f;
+  f.z3 = fits ? static_cast<float>((0.625 / k) * (0.625 / k)) : -1.f;
+  f.neg_icl2 = static_cast<float>(-1.0 / (cl * cl));
+  return f;
+}
+
 ExParams ex_params(const mcs_attn_shape* s, const mcs_attn_opts* o) {
   ExParams p{};
   p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.g = s->Hq / s->Hkv; p.Nq = s->Nq; p.Nk = s->Nk;
@@ -151,8 +172,8 @@ ExTile tile_params(const ExParams& p, const FwdPlan& f, int d) {
   t.Tq = f.Tq; t.Tk = f.Tk;
   t.nsplit = f.nsplit; t.single = f.single; t.chunk = f.chunk;
   t.scale = p.scale;
-  t.mul = static_cast<float>((p.cap > 0.f ? p.cap : p.scale) * 1.4426950408889634074);
-  t.cap_k = p.cap > 0.f ? p.scale / p.cap : 0.f;
+  t.cap = cap_fn(p.scale, p.cap);
+  t.mul = t.cap.on ? 1.f : static_cast<float>(p.scale * 1.4426950408889634074);
   t.causal = p.causal;
   t.slopes = p.slopes;
   t.prefix = p.prefix;
@@ -241,8 +262,8 @@ mcs_status decode_call(const mcs_decode_shape* s, const void* q, const void* kp,
   DecodeParams p{};
   p.B = s->B; p.Hq = s->Hq; p.Hkv = s->Hkv; p.g = s->Hq / s->Hkv; p.C = s->C;
   p.nsplit = f.nsplit; p.chunk = f.chunk; p.gsplit = f.gsplit;
-  p.mul = static_cast<float>((s->cap > 0.f ? s->cap : scale) * 1.4426950408889634074);
-  p.cap_k = s->cap > 0.f ? scale / s->cap : 0.f;
+  p.cap = cap_fn(scale, s->cap);
+  p.mul = p.cap.on ? 1.f : static_cast<float>(scale * 1.4426950408889634074);
   p.q = static_cast<const uint16_t*>(q);
   p.k = static_cast<const uint16_t*>(k);
   p.v = static_cast<const uint16_t*>(v);
@@ -371,6 +392,7 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
   t.dv = static_cast<uint16_t*>(dv);
   float* stats = reinterpret_cast<float*>(base + w.stats);
   t.stats = stats;
+  t.lse_in = lse;
   if (p.doc_q) {
     int* kid = reinterpret_cast<int*>(base + w.k_ids);
     int* qid = reinterpret_cast<int*>(base + w.q_ids);

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
     uint32_t hi[MT][4], lo[MT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      if (p.cap_k != 0.f) tanh_scaled<8>(s[m], p.cap_k);
+      if (p.cap.on) cap_scores<8>(s[m], p.cap);
       // element e: row (e >> 1) & 1, key 8 (e >> 2) + 2 (lane & 3) + (e & 1); in log2 units
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

@@ -90,71 +90,83 @@ __device__ __forceinline__ int build_tile_bits(uint32_t* bits, int* count, const
   return *count;
 }
 
-// tanh(x) of 2 n arguments that are k times the values of s, in place.
-// |x| <= 0.625: x + x z P(z), z = x^2, P of degree 3 fitted to (tanh(x)/x - 1)/z
-// by iteratively reweighted least squares on the relative error of tanh
-// (1.3e-7 at most); beyond, 1 - 2 / (1 + 2^(2 x log2 e)), whose approximate
-// exponential and reciprocal leave about 2e-7. A warp takes the second form
-// only if one of its values needs it: scores of trained models mostly lie well
-// inside the cap, and the polynomial costs no MUFU slot (two for the other
-// form, in kernels that already use one per score).
+// s[c] <- cap log2(e) tanh(k s[c]), the capped score in log2 units, in place.
+// |k s| <= 0.625: s Q(s^2) with Q from x + x z P(z), z = x^2, P of degree 3
+// fitted to (tanh(x)/x - 1)/z by iteratively reweighted least squares on the
+// relative error of tanh (1.3e-7 at most); up to 0.4 degree 2 is as exact. The
+// factors k and cap log2(e) are in Q's coefficients: six (five) packed FMAs per
+// pair. Beyond, 1 - 2 / (1 + 2^(2 |x| log2 e)), whose approximate exponential and
+// reciprocal leave about 2e-7. A warp takes the widest form that one of its 16
+// columns needs: scores of trained models mostly lie well inside the cap, and
+// the polynomials cost no MUFU slot (two for the last form, in kernels that
+// already use one per score).
 template <int N>
-__device__ __forceinline__ void tanh_scaled(float* s, float k) {
-  float big = 0.f;
+__device__ __forceinline__ void cap_scores(float* s, const CapFn& f) {
+  constexpr int W = N < 16 ? N : 16;
 #pragma unroll
-  for (int c = 0; c < N; ++c) big = fmaxf(big, fabsf(s[c]));
-  const bool far = __any_sync(0xffffffffu, !(big * k <= 0.625f));
-  const uint64_t kk = f2_pack(k, k);
-  const uint64_t c0 = f2_pack(-0.333323412f, -0.333323412f), c1 = f2_pack(0.133081745f, 0.133081745f);
-  const uint64_t c2 = f2_pack(-0.0519478787f, -0.0519478787f), c3 = f2_pack(0.0151953385f, 0.0151953385f);
-  if (!far) {
+  for (int c0 = 0; c0 < N; c0 += W) {
+    float* v = s + c0;
+    uint64_t z[W / 2];
+    float big = 0.f;
 #pragma unroll
-    for (int c = 0; c < N; c += 2) {
-      const uint64_t x = f2_mul(f2_pack(s[c], s[c + 1]), kk);
-      const uint64_t z = f2_mul(x, x);
-      const uint64_t p = f2_fma(f2_fma(f2_fma(c3, z, c2), z, c1), z, c0);
-      f2_unpack(f2_fma(f2_mul(x, z), p, x), s[c], s[c + 1]);
+    for (int c = 0; c < W / 2; ++c) {
+      const uint64_t x = f2_pack(v[2 * c], v[2 * c + 1]);
+      z[c] = f2_mul(x, x);
+      float z0, z1;
+      f2_unpack(z[c], z0, z1);
+      big = fmax3(big, z0, z1);
     }
-  } else {
+    if (__all_sync(0xffffffffu, big <= f.z2)) {
+      const uint64_t b0 = f2_pack(f.b[0], f.b[0]), b1 = f2_pack(f.b[1], f.b[1]);
+      const uint64_t b2 = f2_pack(f.b[2], f.b[2]), b3 = f2_pack(f.b[3], f.b[3]);
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
-      const float x = s[c] * k, z = x * x;
-      const float p = fmaf(fmaf(fmaf(0.0151953385f, z, -0.0519478787f), z, 0.133081745f), z, -0.333323412f);
-      float r;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(fabsf(x) * (2.f * kLog2e))));
-      const float t = copysignf(fmaf(-2.f, r, 1.f), x);
-      s[c] = fabsf(x) <= 0.625f ? fmaf(x * z, p, x) : t;
+      for (int c = 0; c < W / 2; ++c)
+        f2_unpack(f2_mul(f2_pack(v[2 * c], v[2 * c + 1]), f2_fma(f2_fma(f2_fma(b3, z[c], b2), z[c], b1), z[c], b0)),
+                  v[2 * c], v[2 * c + 1]);
+    } else if (__all_sync(0xffffffffu, big <= f.z3)) {
+      const uint64_t a0 = f2_pack(f.a[0], f.a[0]), a1 = f2_pack(f.a[1], f.a[1]), a2 = f2_pack(f.a[2], f.a[2]);
+      const uint64_t a3 = f2_pack(f.a[3], f.a[3]), a4 = f2_pack(f.a[4], f.a[4]);
+#pragma unroll
+      for (int c = 0; c < W / 2; ++c)
+        f2_unpack(f2_mul(f2_pack(v[2 * c], v[2 * c + 1]),
+                         f2_fma(f2_fma(f2_fma(f2_fma(a4, z[c], a3), z[c], a2), z[c], a1), z[c], a0)),
+                  v[2 * c], v[2 * c + 1]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < W; ++c) {
+        const float x = v[c] * f.k, y = x * x;
+        const float q = fmaf(fmaf(fmaf(kTanhP3, y, kTanhP2), y, kTanhP1), y, kTanhP0);
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(fabsf(x) * (2.f * kLog2e))));
+        const float t = copysignf(fmaf(-2.f, r, 1.f), x);
+        v[c] = f.cl * (fabsf(x) <= 0.625f ? fmaf(x * y, q, x) : t);
+      }
     }
   }
 }
 
-// tanh_scaled over N values, 32 at a time
-template <int N>
-__device__ __forceinline__ void tanh_all(float* s, float k) {
-#pragma unroll
-  for (int c = 0; c < N; c += 32) tanh_scaled<32>(s + c, k);
+// 1 - tanh^2 from a capped score
+__device__ __forceinline__ uint64_t cap_slope2(uint64_t y, const CapFn& f) {
+  return f2_fma(f2_mul(y, f2_pack(f.neg_icl2, f.neg_icl2)), y, f2_pack(1.f, 1.f));
 }
 
-// s[c] <- mul * s[c] - slope * |base - c * step| for c < N (log2 units). `base` is the
-// distance at c = 0. Where the warp's distances all have one sign the bias is
-// linear in c: two packed FMAs per pair.
+// Distance bias of a row: s[c] <- s[c] - slope |base - c| - r, where `base` is the
+// distance at c = 0 and the returned r is the same for the whole row. Where the
+// warp's distances all have one sign the bias is linear in c, and r = -slope base
+// leaves one FMA with an immediate per score.
 template <int N>
-__device__ __forceinline__ void add_bias(float* s, float mul, float slope, float base, float step) {
-  const float end = base - step * (N - 1);
-  const bool pos = __all_sync(0xffffffffu, base >= 0.f && end >= 0.f);
-  const bool neg = __all_sync(0xffffffffu, base <= 0.f && end <= 0.f);
+__device__ __forceinline__ float add_bias(float* s, float slope, float base) {
+  const bool pos = __all_sync(0xffffffffu, base >= static_cast<float>(N - 1));
+  const bool neg = __all_sync(0xffffffffu, base <= 0.f);
   if (pos || neg) {
     const float sl = pos ? slope : -slope;
-    const uint64_t m2 = f2_pack(mul, mul), t0 = f2_pack(-sl * base, -sl * base), s2 = f2_pack(sl * step, sl * step);
 #pragma unroll
-    for (int c = 0; c < N; c += 2) {
-      const uint64_t b = f2_fma(s2, f2_pack(static_cast<float>(c), static_cast<float>(c + 1)), t0);
-      f2_unpack(f2_fma(m2, f2_pack(s[c], s[c + 1]), b), s[c], s[c + 1]);
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < N; ++c) s[c] = fmaf(mul, s[c], -slope * fabsf(fmaf(-step, static_cast<float>(c), base)));
+    for (int c = 0; c < N; ++c) s[c] = fmaf(sl, static_cast<float>(c), s[c]);
+    return -sl * base;
   }
+#pragma unroll
+  for (int c = 0; c < N; ++c) s[c] = fmaf(-slope, fabsf(base - static_cast<float>(c)), s[c]);
+  return 0.f;
 }
 
 // Zeroes the rows of a swizzled tile (KB column blocks of 128 rows x 128 bytes)

@@ -132,7 +132,8 @@ __device__ __forceinline__ void teardown(volatile int* abort_flag, uint64_t* don
   }
 }
 
-// Per packed row: -lse in log2 units and D = d_o . o, as [B Hkv, Tq][2][128]; an empty row, like a row whose lse is
+// Per packed row: -lse in log2 units (less slope times the row's token in the tile, which the dK/dV kernel's bias
+// counts on) and D = d_o . o, as [B Hkv, Tq][2][128]; an empty row, like a row whose lse is
 // -inf, gets (-inf, 0), which makes its P zero. One warp per row.
 template <int D>
 __global__ void __launch_bounds__(256) ex_row_stats(const ExTile p, const uint16_t* o, const uint16_t* d_o,
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(256) ex_row_stats(const ExTile p, const uint16
     const size_t at = ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D + lane * E;
     if (L > -CUDART_INF_F) {
       nl = -L * kLog2e;
+      if (p.slopes) nl = fmaf(-p.slopes[head] * kLog2e, static_cast<float>(row / p.g), nl);
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
         const uint32_t x = *reinterpret_cast<const uint32_t*>(o + at + e);
@@ -426,10 +428,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_doc = docs ? p.k_ids[(static_cast<size_t>(b) * p.Tk + kt) * 128 + row] : 0;  // padding: -1
     const bool all_rows = !p.causal || key < prefix;
     const bool all_keys = !p.causal || kt * 128 + 127 < prefix;
-    const bool cap = MOD && p.cap_k != 0.f;
+    const bool cap = MOD && p.cap.on;
     const bool bias = MOD && p.slopes != nullptr;
-    const float mul = bias ? 1.f : p.mul;
+    const float mul = p.mul;
     const uint64_t mul2 = f2_pack(mul, mul);
+    const float im = 1.f / mul;
     const float4* tok4 = reinterpret_cast<const float4*>(row_tok) + quarter * 8;
     const float4* sl4 = reinterpret_cast<const float4*>(row_slope) + quarter * 8;
     TileIter it = first;
@@ -463,37 +466,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(tS, pv);
       tmem_wait_ld();
       if (cap) {
-        tanh_scaled<32>(pv, p.cap_k);
+        cap_scores<32>(pv, p.cap);
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const uint64_t t2 = f2_pack(pv[c], pv[c + 1]);
-          f2_unpack(f2_fma(f2_mul(t2, f2_pack(-1.f, -1.f)), t2, f2_pack(1.f, 1.f)), w[c], w[c + 1]);
-        }
+        for (int c = 0; c < 32; c += 2) f2_unpack(cap_slope2(f2_pack(pv[c], pv[c + 1]), p.cap), w[c], w[c + 1]);
       }
       if (bias) {
-        const bool after = __all_sync(0xffffffffu, at_i <= 0);           // every token at or after the key
-        const bool before = __all_sync(0xffffffffu, at_i >= p.tpt - 1);  // every token at or before it
-        const float sign = before ? -1.f : 1.f;
-        const uint64_t pm2 = f2_pack(p.mul, p.mul);
-        if (after || before) {
-          const uint64_t sg2 = f2_pack(sign, sign), off2 = f2_pack(-sign * at, -sign * at);
+        // The statistics hold nl - slope token. With token >= key the bias is -slope (token - at), of which
+        // slope at is left; else slope (token - at), and otherwise the two cases element by element.
+        const bool after = __all_sync(0xffffffffu, at_i <= 0);
+        const bool before = __all_sync(0xffffffffu, at_i >= p.tpt - 1);
+        const float at_m = at * im;
+        if (after) {
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
-            const float4 tk = tok4[c >> 2], sl = sl4[c >> 2];
-            // slope times sign (token - key), the distance
-            const uint64_t d01 = f2_mul(f2_pack(-sl.x, -sl.y), f2_fma(f2_pack(tk.x, tk.y), sg2, off2));
-            const uint64_t d23 = f2_mul(f2_pack(-sl.z, -sl.w), f2_fma(f2_pack(tk.z, tk.w), sg2, off2));
-            f2_unpack(f2_fma(f2_pack(pv[c], pv[c + 1]), pm2, d01), pv[c], pv[c + 1]);
-            f2_unpack(f2_fma(f2_pack(pv[c + 2], pv[c + 3]), pm2, d23), pv[c + 2], pv[c + 3]);
+            const float4 sl = sl4[c >> 2];
+            const uint64_t at2 = f2_pack(at_m, at_m);
+            f2_unpack(f2_fma(f2_pack(sl.x, sl.y), at2, f2_pack(pv[c], pv[c + 1])), pv[c], pv[c + 1]);
+            f2_unpack(f2_fma(f2_pack(sl.z, sl.w), at2, f2_pack(pv[c + 2], pv[c + 3])), pv[c + 2], pv[c + 3]);
           }
         } else {
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
             const float4 tk = tok4[c >> 2], sl = sl4[c >> 2];
-            pv[c] = fmaf(pv[c], p.mul, -sl.x * fabsf(tk.x - at));
-            pv[c + 1] = fmaf(pv[c + 1], p.mul, -sl.y * fabsf(tk.y - at));
-            pv[c + 2] = fmaf(pv[c + 2], p.mul, -sl.z * fabsf(tk.z - at));
-            pv[c + 3] = fmaf(pv[c + 3], p.mul, -sl.w * fabsf(tk.w - at));
+            const float d0 = tk.x - at, d1 = tk.y - at, d2 = tk.z - at, d3 = tk.w - at;
+            pv[c] = fmaf(sl.x * im, tk.x - (before ? -d0 : fabsf(d0)), pv[c]);
+            pv[c + 1] = fmaf(sl.y * im, tk.y - (before ? -d1 : fabsf(d1)), pv[c + 1]);
+            pv[c + 2] = fmaf(sl.z * im, tk.z - (before ? -d2 : fabsf(d2)), pv[c + 2]);
+            pv[c + 3] = fmaf(sl.w * im, tk.w - (before ? -d3 : fabsf(d3)), pv[c + 3]);
           }
         }
       }
@@ -787,16 +786,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int head = hk * p.g + row % p.g;
     const bool row_valid = row < rt && tok < p.Nq;
     const float* st = p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
-    const float negl = st[row], delta = st[128 + row];
+    const float lse = row_valid ? p.lse_in[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok] : -CUDART_INF_F;
+    const float negl = lse > -CUDART_INF_F ? -lse * kLog2e : -CUDART_INF_F, delta = st[128 + row];
     const uint64_t negl2 = f2_pack(negl, negl), delta2 = f2_pack(delta, delta);
     const int pos = off + tok;
     const int lim = limit(pos) - quarter * 32;
     const int lim_all = limit(off + qt * p.tpt);
     const int my_doc = docs ? p.q_ids[(static_cast<size_t>(b) * p.Tq + qt) * 128 + row] : 0;  // padding: -2
-    const bool cap = MOD && p.cap_k != 0.f;
+    const bool cap = MOD && p.cap.on;
     const bool bias = MOD && p.slopes != nullptr;
-    const float slope = bias && row_valid ? p.slopes[head] * kLog2e : 0.f;
-    const float mul = bias ? 1.f : p.mul;
+    const float mul = p.mul;
+    const float slope = bias && row_valid ? p.slopes[head] * kLog2e / mul : 0.f;
     const uint64_t mul2 = f2_pack(mul, mul);
     TileIter it = first;
     bool ok = true;
@@ -823,18 +823,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(s_read);
       if (cap) {
-        tanh_scaled<32>(pv, p.cap_k);
+        cap_scores<32>(pv, p.cap);
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const uint64_t t2 = f2_pack(pv[c], pv[c + 1]);
-          f2_unpack(f2_fma(f2_mul(t2, f2_pack(-1.f, -1.f)), t2, f2_pack(1.f, 1.f)), w[c], w[c + 1]);
-        }
+        for (int c = 0; c < 32; c += 2) f2_unpack(cap_slope2(f2_pack(pv[c], pv[c + 1]), p.cap), w[c], w[c + 1]);
       }
-      if (bias) add_bias<32>(pv, p.mul, slope, static_cast<float>(pos - kt * 128 - quarter * 32), 1.f);
+      uint64_t e2 = negl2;
+      if (bias) {
+        const float e = fmaf(add_bias<32>(pv, slope, static_cast<float>(pos - kt * 128 - quarter * 32)), mul, negl);
+        e2 = f2_pack(e, e);
+      }
 #pragma unroll
       for (int c = 0; c < 32; c += 2) {
         float x0, x1;
-        f2_unpack(f2_fma(f2_pack(pv[c], pv[c + 1]), mul2, negl2), x0, x1);
+        f2_unpack(f2_fma(f2_pack(pv[c], pv[c + 1]), mul2, e2), x0, x1);
         pv[c] = fast_exp2(x0);
         pv[c + 1] = fast_exp2(x1);
       }
@@ -927,7 +928,7 @@ cudaError_t launch_ex_row_stats(int d, const ExTile& p, const uint16_t* o, const
 
 cudaError_t launch_ex_bwd(int d, const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk,
                           const CUtensorMap* tv, const ExTile& p, cudaStream_t s) {
-  const bool mod = p.cap_k != 0.f || p.slopes;
+  const bool mod = p.cap.on || p.slopes;
   if (d == 64) return mod ? launch_bwd<64, true>(tq, tg, tk, tv, p, s) : launch_bwd<64, false>(tq, tg, tk, tv, p, s);
   return mod ? launch_bwd<128, true>(tq, tg, tk, tv, p, s) : launch_bwd<128, false>(tq, tg, tk, tv, p, s);
 }

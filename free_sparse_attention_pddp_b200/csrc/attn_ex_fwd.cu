@@ -306,9 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int4 mine = t == 0 || single ? r0 : r1;
     int my_doc = docs && row_valid ? p.doc_q[static_cast<size_t>(b) * p.Nq + tok] : -2;
     if (my_doc < 0) my_doc = -2;  // a padded query matches no key
-    const float slope = MOD && p.slopes && row_valid ? p.slopes[head] * kLog2e : 0.f;
     const bool bias = MOD && p.slopes != nullptr;
-    const float mul = bias ? 1.f : p.mul;  // what turns a transformed score into log2 units
+    const float mul = p.mul;  // what turns a score into log2 units
+    const float slope = bias && row_valid ? p.slopes[head] * kLog2e / mul : 0.f;
     const uint64_t mul2 = f2_pack(mul, mul);
     float2* my_max = row_max + (t * 2 + half) * 128 + row;
     const float2* other_max = row_max + (t * 2 + (half ^ 1)) * 128 + row;
@@ -327,9 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(tS, sv);
       tmem_ld32(tS + 32, sv + 32);
       tmem_wait_ld();
+      float shift = 0.f;  // log2 units that the whole row of this tile lacks
       if (MOD) {
-        if (p.cap_k != 0.f) tanh_all<64>(sv, p.cap_k);
-        if (bias) add_bias<64>(sv, p.mul, slope, static_cast<float>(pos - kt * 128 - half * 64), 1.f);
+        if (p.cap.on) cap_scores<64>(sv, p.cap);
+        if (bias) shift = add_bias<64>(sv, slope, static_cast<float>(pos - kt * 128 - half * 64)) * mul;
       }
       const int4* ids = nullptr;
       bool partial = (kt + 1) * 128 > lim_all;
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 1; e < 15; e += 2) a = fmax3(a, sv[k * 16 + e], sv[k * 16 + e + 1]);
         mc[k] = fmaxf(a, sv[k * 16 + 15]);
       }
-      const float half_max = fmaxf(fmax3(mc[0], mc[1], mc[2]), mc[3]);
+      const float half_max = fmaf(fmaxf(fmax3(mc[0], mc[1], mc[2]), mc[3]), mul, shift);
       // Both warps meet here in every step, with the step's own word on whether their waits held, and leave the loop
       // in the same step if one did not.
       my_max[(i & 1) * 512] = make_float2(half_max, ok ? 0.f : 1.f);
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 other = other_max[(i & 1) * 512];
       ok = ok && other.y == 0.f;
       if (!ok) break;
-      const float mx = fmaxf(half_max, other.x) * mul;
+      const float mx = fmaxf(half_max, other.x);
       // a row that has seen no valid key keeps m = -inf, l = 0 and P = 0
       const bool need = i == 0 ? mx > m : mx > m + kRescale;
       const bool rescale = i > 0 && __any_sync(0xffffffffu, need);
@@ -381,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         alpha = fast_exp2(m - mx);
         m = mx;
       }
-      const float ms = m == -CUDART_INF_F ? 0.f : m;
-      const uint64_t negm = f2_pack(-ms, -ms);
+      const float ms = m == -CUDART_INF_F ? 0.f : shift - m;
+      const uint64_t negm = f2_pack(ms, ms);
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
         uint32_t pk[16];
@@ -595,7 +596,7 @@ cudaError_t launch_fwd(const CUtensorMap* tq, const CUtensorMap* tk, const CUten
 
 cudaError_t launch_ex_fwd(int d, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const ExTile& p,
                           cudaStream_t s) {
-  const bool mod = p.cap_k != 0.f || p.slopes;
+  const bool mod = p.cap.on || p.slopes;
   if (d == 64) return mod ? launch_fwd<64, true>(tq, tk, tv, p, s) : launch_fwd<64, false>(tq, tk, tv, p, s);
   return mod ? launch_fwd<128, true>(tq, tk, tv, p, s) : launch_fwd<128, false>(tq, tk, tv, p, s);
 }

@@ -129,14 +129,25 @@ struct ExParams {
   int* status;
 };
 
+// The score cap: y(s) = cap log2(e) tanh(k s), k = scale / cap, for products s = q . k (cap_scores in attn_ex.cuh).
+struct CapFn {
+  int on;
+  float k, cl;       // cl = cap log2 e
+  float z2, z3;      // s^2 up to which the coefficients b, and a, hold (-1: never)
+  float a[5], b[4];  // y = s Q(s^2)
+  float neg_icl2;    // -1 / cl^2
+};
+constexpr float kTanhP0 = -0.333323412f, kTanhP1 = 0.133081745f, kTanhP2 = -0.0519478787f, kTanhP3 = 0.0151953385f;
+constexpr float kTanhR0 = -0.333318822f, kTanhR1 = 0.132776282f, kTanhR2 = -0.0477941821f;  // degree 2, |x| <= 0.4
+
 // The tile kernels' view of a call (attn_ex_fwd.cu, attn_ex_bwd.cu).
 struct ExTile {
   int B, Hq, Hkv, g, tpt, Nq, Nk;  // tpt: tokens of a packed query tile
   int qbox;                        // backward: tokens of a query map's box, tpt or (64 rows) tpt / 2
   int Tq, Tk;                      // query and key tiles
   int nsplit, single, chunk;       // forward: key splits, one-tile CTAs, heads per chunk of the work order
-  float mul;                       // log2 units per transformed score: scale log2 e, or cap log2 e
-  float cap_k;                     // scale / cap; 0: no cap
+  float mul;                       // log2 units per score: scale log2 e, or 1 where the cap yields them
+  CapFn cap;
   float scale;
   int causal;
   const float* slopes;
@@ -149,6 +160,7 @@ struct ExTile {
   uint16_t* o;                     // outputs, or the partials of the splits
   float* lse;
   const float* stats;              // backward: [B,Hkv,Tq][2][128], -lse in log2 units and d_o . o
+  const float* lse_in;             // backward: the forward's lse
   uint16_t *dq, *dk, *dv;
   float *part_o, *part_lse;        // [parts][B,Hkv,Tq,128](,d), lse in log2 units
   int* status;
@@ -171,7 +183,8 @@ struct DecodeParams {
   int B, Hq, Hkv, g, C;
   int nsplit, chunk;               // chunks of the keys, keys of a chunk
   int gsplit;                      // parts of a head group (32 heads each)
-  float mul, cap_k;                // as in ExTile
+  float mul;                       // as in ExTile
+  CapFn cap;
   const uint16_t *q, *k, *v;
   const int32_t* lens;
   const float* slopes;
