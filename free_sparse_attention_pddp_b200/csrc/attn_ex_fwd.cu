@@ -376,14 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mx = fmaxf(half_max, other.x);
       // a row that has seen no valid key keeps m = -inf, l = 0 and P = 0
       const bool need = i == 0 ? mx > m : mx > m + kRescale;
-      const bool rescale = i > 0 && __any_sync(0xffffffffu, need);
-      float alpha = 1.f;
-      if (need) {
-        alpha = fast_exp2(m - mx);
-        m = mx;
-      }
-      const float ms = m == -CUDART_INF_F ? 0.f : shift - m;
-      const uint64_t negm = f2_pack(ms, ms);
+      const float m_old = m;
+      m = need ? mx : m;
+      const float e0 = m == -CUDART_INF_F ? 0.f : shift - m;
+      const uint64_t e2 = f2_pack(e0, e0);
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
         uint32_t pk[16];
@@ -391,13 +387,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           float x0, x1;
-          f2_unpack(f2_fma(f2_pack(v[2 * q], v[2 * q + 1]), mul2, negm), x0, x1);
+          f2_unpack(f2_fma(f2_pack(v[2 * q], v[2 * q + 1]), mul2, e2), x0, x1);
           v[2 * q] = fast_exp2(x0);
           v[2 * q + 1] = fast_exp2(x1);
           pk[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
         }
         tmem_st16u(tS + h2 * 16, pk);
       }
+      if (i > 0 && __any_sync(0xffffffffu, need)) {
+        // O += P(i-1) V ran before S(i), so O may be scaled here; O += P(i) V waits for p_full
+        const float alpha = need ? fast_exp2(m_old - m) : 1.f;
+        l *= alpha;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float ov[16];
+          tmem_ld16(tO + c * 16, ov);
+          tmem_wait_ld();
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(ov[e] * alpha);
+          tmem_st16u(tO + c * 16, w);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[t]);
+      // the sum of this half's P, beside the products that wait for it
       {
         uint64_t a[16];
 #pragma unroll
@@ -410,27 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float s0, s1;
         f2_unpack(a[0], s0, s1);
-        l = l * alpha + (s0 + s1);
+        l += s0 + s1;
       }
-      tmem_wait_st();
-      if (rescale) {
-        // scale O once O += P(i-1) V is done; O += P(i) V waits for p_full
-        ok = mbar_wait_warp(&p_empty[t], (i - 1) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX);
-        if (!ok) continue;  // the other half learns of it in the next step
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          float ov[32];
-          tmem_ld32(tO + c * 32, ov);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-          tmem_st32(tO + c * 32, ov);
-        }
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      mbar_arrive(&p_full[t]);
     }
     // ---------------------------------------------------------------- epilogue of slot t
     const bool fin = ok && (nt == 0 || mbar_wait_warp(&p_empty[t], (nt - 1) & 1, wctx, MCS_WHERE_ATTN_EPILOGUE));
