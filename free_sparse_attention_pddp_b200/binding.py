@@ -250,74 +250,104 @@ def decode_workspace(shape: DecodeShape, device="cuda"):
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _fits(what, **tensors):
-    """Refuse a tensor that is not what the kernels read: name=(tensor, dtype name, shape); None passes.
+def _refuse(what, name, t, dtype, shape):
+    raise MCSError(1, f"{what}: {name} must be contiguous {dtype} {tuple(shape)} on the current CUDA device (like the "
+                      f"others), got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
-    All tensors are contiguous and on the current CUDA device (where the stream is)."""
+
+def _fits(what, ws, *tensors):
+    """Refuses tensors that are not what the kernels read: each (name, tensor, dtype, shape); None passes. All lie
+    on the current CUDA device, whose index is returned."""
     import torch
 
-    device = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype is not getattr(torch, dtype) or not t.is_contiguous() or (shape is not None and t.shape != shape):
-            raise MCSError(1, f"{what}: {name} must be contiguous {dtype} {shape if shape is not None else ''}, got "
-                              f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
-        if not t.is_cuda or t.get_device() != device:
-            raise MCSError(1, f"{what}: {name} is on {t.device}, not on the current CUDA device")
+    dev = ws.get_device()
+    if dev < 0 or dev != torch.cuda.current_device() or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        _refuse(what, "ws", ws, torch.uint8, ws.shape)
+    for name, t, dtype, shape in tensors:
+        if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or
+                              t.get_device() != dev):
+            _refuse(what, name, t, dtype, shape)
+    return dev
 
 
-def _attn_fits(what, s, q_like, k_like, lse, ws, slopes, prefix, doc_q, doc_k):
-    qs, ks = (s.B, s.Nq, s.Hq, s.d), (s.B, s.Nk, s.Hkv, s.d)
-    _fits(what, **{n: (t, "bfloat16", qs) for n, t in q_like.items()},
-          **{n: (t, "bfloat16", ks) for n, t in k_like.items()},
-          lse=(lse, "float32", (s.B, s.Hq, s.Nq)), ws=(ws, "uint8", None), slopes=(slopes, "float32", (s.Hq,)),
-          prefix=(prefix, "int32", (s.B,)), doc_q=(doc_q, "int32", (s.B, s.Nq)), doc_k=(doc_k, "int32", (s.B, s.Nk)))
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
-def _opts(slopes, prefix, doc_q, doc_k):
+def _on(stream, dev):
+    if stream is None:
+        import torch
+
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _opts(what, s, ws, slopes, prefix, doc_q, doc_k):
+    """The options' pointers (None without any), once they fit."""
     if slopes is None and prefix is None and doc_q is None and doc_k is None:
         return None
-    return ctypes.byref(AttnOpts(*(None if t is None else t.data_ptr() for t in (slopes, prefix, doc_q, doc_k))))
+    import torch
+
+    i32 = torch.int32
+    _fits(what, ws, ("slopes", slopes, torch.float32, (s.Hq,)), ("prefix", prefix, i32, (s.B,)),
+          ("doc_q", doc_q, i32, (s.B, s.Nq)), ("doc_k", doc_k, i32, (s.B, s.Nk)))
+    return ctypes.byref(AttnOpts(_at(slopes), _at(prefix), _at(doc_q), _at(doc_k)))
 
 
 def mcs_dense_ex(shape, q, k, v, o, lse, ws, slopes=None, prefix=None, doc_q=None, doc_k=None, stream=None):
     """Attention with capped or biased scores, causal, prefix and document masks, shared KV heads."""
-    _attn_fits("mcs_dense_ex", shape, dict(q=q, o=o), dict(k=k, v=v), lse, ws, slopes, prefix, doc_q, doc_k)
-    _check(load().mcs_dense_ex(ctypes.byref(shape), _opts(slopes, prefix, doc_q, doc_k), _ptr(q), _ptr(k), _ptr(v),
-                               _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "mcs_dense_ex")
+    import torch
+
+    bf16, s = torch.bfloat16, shape
+    qs, ks = (s.B, s.Nq, s.Hq, s.d), (s.B, s.Nk, s.Hkv, s.d)
+    dev = _fits("mcs_dense_ex", ws, ("q", q, bf16, qs), ("k", k, bf16, ks), ("v", v, bf16, ks), ("o", o, bf16, qs),
+                ("lse", lse, torch.float32, (s.B, s.Hq, s.Nq)))
+    opts = _opts("mcs_dense_ex", s, ws, slopes, prefix, doc_q, doc_k)
+    _check(load().mcs_dense_ex(ctypes.byref(s), opts, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                               _at(lse), ws.data_ptr(), ws.numel(), _on(stream, dev)), "mcs_dense_ex")
 
 
 def mcs_dense_bwd(shape, q, k, v, o, lse, d_o, dq, dk, dv, ws, slopes=None, prefix=None, doc_q=None, doc_k=None,
                   stream=None):
     """Gradients of mcs_dense_ex with respect to q, k and v, from its o and lse and the gradient d_o of o."""
-    _attn_fits("mcs_dense_bwd", shape, dict(q=q, o=o, d_o=d_o, dq=dq), dict(k=k, v=v, dk=dk, dv=dv), lse, ws, slopes,
-               prefix, doc_q, doc_k)
-    _check(load().mcs_dense_bwd(ctypes.byref(shape), _opts(slopes, prefix, doc_q, doc_k), _ptr(q), _ptr(k), _ptr(v),
-                                _ptr(o), _ptr(lse), _ptr(d_o), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws), ws.numel(),
-                                _stream(stream)), "mcs_dense_bwd")
+    import torch
 
-
-def _decode_fits(what, s, q, kp, vp, k, v, lens, o, lse, ws, slopes):
-    qs, cs, ps = (s.B, s.Hq, s.d), (s.B, s.C, s.Hkv, s.d), (s.P, s.Hkv, s.d)
-    _fits(what, q=(q, "bfloat16", qs), o=(o, "bfloat16", qs), kp=(kp, "bfloat16", ps), vp=(vp, "bfloat16", ps),
-          k=(k, "bfloat16", cs), v=(v, "bfloat16", cs), lens=(lens, "int32", (s.B,)),
-          lse=(lse, "float32", (s.B, s.Hq)), ws=(ws, "uint8", None), slopes=(slopes, "float32", (s.Hq,)))
+    bf16, s = torch.bfloat16, shape
+    qs, ks = (s.B, s.Nq, s.Hq, s.d), (s.B, s.Nk, s.Hkv, s.d)
+    dev = _fits("mcs_dense_bwd", ws, ("q", q, bf16, qs), ("k", k, bf16, ks), ("v", v, bf16, ks), ("o", o, bf16, qs),
+                ("lse", lse, torch.float32, (s.B, s.Hq, s.Nq)), ("d_o", d_o, bf16, qs), ("dq", dq, bf16, qs),
+                ("dk", dk, bf16, ks), ("dv", dv, bf16, ks))
+    opts = _opts("mcs_dense_bwd", s, ws, slopes, prefix, doc_q, doc_k)
+    _check(load().mcs_dense_bwd(ctypes.byref(s), opts, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                _at(lse), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
+                                ws.numel(), _on(stream, dev)), "mcs_dense_bwd")
 
 
 def mcs_decode(shape, q, k, v, lens, o, lse, ws, slopes=None, stream=None):
     """One token per request over a cache of capacity C (request b holds lens[b] keys)."""
-    _decode_fits("mcs_decode", shape, q, None, None, k, v, lens, o, lse, ws, slopes)
-    _check(load().mcs_decode(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(lens), _ptr(slopes), _ptr(o),
-                             _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "mcs_decode")
+    import torch
+
+    bf16, f32, s = torch.bfloat16, torch.float32, shape
+    qs, cs = (s.B, s.Hq, s.d), (s.B, s.C, s.Hkv, s.d)
+    dev = _fits("mcs_decode", ws, ("q", q, bf16, qs), ("k", k, bf16, cs), ("v", v, bf16, cs),
+                ("lens", lens, torch.int32, (s.B,)), ("o", o, bf16, qs), ("lse", lse, f32, (s.B, s.Hq)),
+                ("slopes", slopes, f32, (s.Hq,)))
+    _check(load().mcs_decode(ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(), _at(slopes),
+                             o.data_ptr(), _at(lse), ws.data_ptr(), ws.numel(), _on(stream, dev)), "mcs_decode")
 
 
 def mcs_decode_shared(shape, q, kp, vp, k, v, lens, o, lse, ws, slopes=None, stream=None):
     """mcs_decode behind a prefix of P keys that all requests share, read once for the batch."""
-    _decode_fits("mcs_decode_shared", shape, q, kp, vp, k, v, lens, o, lse, ws, slopes)
-    _check(load().mcs_decode_shared(ctypes.byref(shape), _ptr(q), _ptr(kp), _ptr(vp), _ptr(k), _ptr(v), _ptr(lens),
-                                    _ptr(slopes), _ptr(o), _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)),
-           "mcs_decode_shared")
+    import torch
+
+    bf16, f32, s = torch.bfloat16, torch.float32, shape
+    qs, cs, ps = (s.B, s.Hq, s.d), (s.B, s.C, s.Hkv, s.d), (s.P, s.Hkv, s.d)
+    dev = _fits("mcs_decode_shared", ws, ("q", q, bf16, qs), ("kp", kp, bf16, ps), ("vp", vp, bf16, ps),
+                ("k", k, bf16, cs), ("v", v, bf16, cs), ("lens", lens, torch.int32, (s.B,)), ("o", o, bf16, qs),
+                ("lse", lse, f32, (s.B, s.Hq)), ("slopes", slopes, f32, (s.Hq,)))
+    _check(load().mcs_decode_shared(ctypes.byref(s), q.data_ptr(), kp.data_ptr(), vp.data_ptr(), k.data_ptr(),
+                                    v.data_ptr(), lens.data_ptr(), _at(slopes), o.data_ptr(), _at(lse), ws.data_ptr(),
+                                    ws.numel(), _on(stream, dev)), "mcs_decode_shared")
 
 
 def _event(ev, must_exist: bool):

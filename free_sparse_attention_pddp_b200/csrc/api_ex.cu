@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kMaxGroup = 128;            // query heads of one KV head: one 128-row tile holds a token's
 constexpr int kMaxDocQueryTiles = 1 << 16;  // tiles of a document mask's bitmaps: over query tiles
-constexpr int kMaxDocKeyTiles = 1 << 13;    // and over key tiles (the dQ kernel has 1 KB left for it)
+constexpr int kMaxDocKeyTiles = 1 << 12;    // and over key tiles (the dQ kernel has 1 KB left for it)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -60,7 +60,7 @@ CapFn cap_fn(float scale, float cap) {
   if (!(cap > 0.f)) return f;
   f.on = 1;
   const double k = static_cast<double>(scale) / cap, cl = cap * 1.4426950408889634074;
-  f.k = static_cast<float>(k);
+  f.k2 = static_cast<float>(2.0 * k * 1.4426950408889634074);
   f.cl = static_cast<float>(cl);
   const double p3[5] = {1.0, kTanhP0, kTanhP1, kTanhP2, kTanhP3}, p2[4] = {1.0, kTanhR0, kTanhR1, kTanhR2};
   bool fits = true;

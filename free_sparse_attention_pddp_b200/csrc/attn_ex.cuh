@@ -11,9 +11,36 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "mcs_ptx.cuh"
 
 namespace mcs {
+
+// Calls f with the head size and the call's options as compile-time constants.
+// One kernel per combination: the options' code in one body overflows the
+// instruction cache (with all of it the capped dK/dV and dQ passes ran 1.29
+// times as long, 5.44 against 4.23 ms on 37 heads of 8192 tokens).
+template <typename F>
+cudaError_t with_options(int d, const ExTile& p, F f) {
+  using T = std::true_type;
+  using N = std::false_type;
+  auto pick = [&](auto D) {
+    const int which = (p.cap.on ? 4 : 0) + (p.slopes ? 2 : 0) + (p.k_ranges ? 1 : 0);
+    switch (which) {
+      case 0: return f(D, N{}, N{}, N{});
+      case 1: return f(D, N{}, N{}, T{});
+      case 2: return f(D, N{}, T{}, N{});
+      case 3: return f(D, N{}, T{}, T{});
+      case 4: return f(D, T{}, N{}, N{});
+      case 5: return f(D, T{}, N{}, T{});
+      case 6: return f(D, T{}, T{}, N{});
+      default: return f(D, T{}, T{}, T{});
+    }
+  };
+  if (d == 64) return pick(std::integral_constant<int, 64>{});
+  return pick(std::integral_constant<int, 128>{});
+}
 
 // CTA of the tile kernels: warp 0 issues the UMMAs, warp 1 the TMA loads, warp
 // 2 clears padded rows, warp 3 only completes their warpgroup; 16 softmax warps,
@@ -67,28 +94,36 @@ __device__ __forceinline__ bool docs_same(int4 a, int4 b) {  // every pair of ro
   return a.x == a.y && b.x == b.y && a.x == b.x && !a.z && !b.z;
 }
 
-// Sets, for tiles lo .. hi - 1, the bits of those whose documents meet `mine`
-// (or `mine2`), and returns their number to every thread. All threads of the
-// CTA call it. `count` is a shared word that is zero before.
-__device__ __forceinline__ int build_tile_bits(uint32_t* bits, int* count, const int4* ranges, int lo, int hi,
-                                               int4 mine, int4 mine2) {
+// For tiles lo .. hi - 1: sets the bits of those whose documents meet `mine` (or
+// `mine2`), in `whole` of those whose every pair with `mine` is valid (in
+// `whole2` with `mine2`, unless null), and returns the number of the first to
+// every thread. All threads of the CTA call it. `count` is a shared word that
+// is zero before.
+__device__ __forceinline__ int build_tile_bits(uint32_t* bits, uint32_t* whole, uint32_t* whole2, int* count,
+                                               const int4* ranges, int lo, int hi, int4 mine, int4 mine2) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   for (int w = warp; w * 32 < hi - lo; w += warps) {
     const int t = lo + w * 32 + lane;
-    bool on = false;
+    bool on = false, all = false, all2 = false;
     if (t < hi) {
       const int4 r = ranges[t];
       on = docs_meet(r, mine) || docs_meet(r, mine2);
+      all = docs_same(r, mine);
+      all2 = docs_same(r, mine2);
     }
     const uint32_t m = __ballot_sync(0xffffffffu, on);
+    const uint32_t a = __ballot_sync(0xffffffffu, all), a2 = __ballot_sync(0xffffffffu, all2);
     if (lane == 0) {
       bits[w] = m;
+      whole[w] = a;
+      if (whole2) whole2[w] = a2;
       if (m) atomicAdd(count, __popc(m));  // a whole-number sum: its order is free
     }
   }
   __syncthreads();
   return *count;
 }
+__device__ __forceinline__ bool tile_bit(const uint32_t* bits, int i) { return (bits[i >> 5] >> (i & 31)) & 1u; }
 
 // s[c] <- cap log2(e) tanh(k s[c]), the capped score in log2 units, in place.
 // |k s| <= 0.625: s Q(s^2) with Q from x + x z P(z), z = x^2, P of degree 3
@@ -100,6 +135,11 @@ __device__ __forceinline__ int build_tile_bits(uint32_t* bits, int* count, const
 // columns needs: scores of trained models mostly lie well inside the cap, and
 // the polynomials cost no MUFU slot (two for the last form, in kernels that
 // already use one per score).
+__device__ __forceinline__ float cap_far(float s, const CapFn& f) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(fabsf(s) * f.k2)));
+  return copysignf(fmaf(-2.f * f.cl, r, f.cl), s);
+}
 template <int N>
 __device__ __forceinline__ void cap_scores(float* s, const CapFn& f) {
   constexpr int W = N < 16 ? N : 16;
@@ -123,23 +163,21 @@ __device__ __forceinline__ void cap_scores(float* s, const CapFn& f) {
       for (int c = 0; c < W / 2; ++c)
         f2_unpack(f2_mul(f2_pack(v[2 * c], v[2 * c + 1]), f2_fma(f2_fma(f2_fma(b3, z[c], b2), z[c], b1), z[c], b0)),
                   v[2 * c], v[2 * c + 1]);
-    } else if (__all_sync(0xffffffffu, big <= f.z3)) {
+    } else {
       const uint64_t a0 = f2_pack(f.a[0], f.a[0]), a1 = f2_pack(f.a[1], f.a[1]), a2 = f2_pack(f.a[2], f.a[2]);
       const uint64_t a3 = f2_pack(f.a[3], f.a[3]), a4 = f2_pack(f.a[4], f.a[4]);
+      const bool far = !__all_sync(0xffffffffu, big <= f.z3);
 #pragma unroll
-      for (int c = 0; c < W / 2; ++c)
-        f2_unpack(f2_mul(f2_pack(v[2 * c], v[2 * c + 1]),
-                         f2_fma(f2_fma(f2_fma(f2_fma(a4, z[c], a3), z[c], a2), z[c], a1), z[c], a0)),
+      for (int c = 0; c < W / 2; ++c) {
+        const float s0 = v[2 * c], s1 = v[2 * c + 1];
+        f2_unpack(f2_mul(f2_pack(s0, s1), f2_fma(f2_fma(f2_fma(f2_fma(a4, z[c], a3), z[c], a2), z[c], a1), z[c], a0)),
                   v[2 * c], v[2 * c + 1]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < W; ++c) {
-        const float x = v[c] * f.k, y = x * x;
-        const float q = fmaf(fmaf(fmaf(kTanhP3, y, kTanhP2), y, kTanhP1), y, kTanhP0);
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + fast_exp2(fabsf(x) * (2.f * kLog2e))));
-        const float t = copysignf(fmaf(-2.f, r, 1.f), x);
-        v[c] = f.cl * (fabsf(x) <= 0.625f ? fmaf(x * y, q, x) : t);
+        if (far) {
+          float z0, z1;
+          f2_unpack(z[c], z0, z1);
+          v[2 * c] = z0 <= f.z3 ? v[2 * c] : cap_far(s0, f);
+          v[2 * c + 1] = z1 <= f.z3 ? v[2 * c + 1] : cap_far(s1, f);
+        }
       }
     }
   }

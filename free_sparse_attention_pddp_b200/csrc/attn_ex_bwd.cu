@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(256) ex_row_stats(const ExTile p, const uint16
 
 }  // namespace
 
-template <int D, bool MOD>
+template <int D, bool CAP, bool BIAS, bool DOC>
 __global__ void __launch_bounds__(kThreads, 1)
     ex_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
@@ -220,9 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // query tiles lo .. Tq - 1 reach these keys
   int lo = 0;
   if (p.causal && kt * 128 >= prefix) lo = min(p.Tq, max(0, kt * 128 - off) / p.tpt);
-  const bool docs = p.k_ranges != nullptr;
   const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
-  const int4 mine = docs ? p.k_ranges[static_cast<size_t>(b) * p.Tk + kt] : none;
+  const int4 mine = DOC ? p.k_ranges[static_cast<size_t>(b) * p.Tk + kt] : none;
   const int rt = p.tpt * p.g;
   const bool halves = p.qbox < p.tpt;  // a tile loads as two boxes of 64 rows
 
@@ -265,8 +264,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int n = p.Tq - lo;
-  if (docs) n = build_tile_bits(bits, count, p.q_ranges + static_cast<size_t>(b) * p.Tq, lo, p.Tq, mine, none);
-  const TileIter first{docs ? bits : nullptr, lo, lo};
+  const uint32_t* whole = bits + ((p.Tq + 31) >> 5);
+  if (DOC)
+    n = build_tile_bits(bits, bits + ((p.Tq + 31) >> 5), nullptr, count, p.q_ranges + static_cast<size_t>(b) * p.Tq, lo,
+                        p.Tq, mine, none);
+  const TileIter first{DOC ? bits : nullptr, lo, lo};
   const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
 
   if (warp < 4) {
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Q or d_o of list entry j, half h
         auto ready = [&](uint64_t* full, int j, int h) {
           const int s = j % C::NS;
-          const bool there = wait(docs ? &qg_ok[s] : &full[halves ? 2 * s + h : 2 * s], j / C::NS);
+          const bool there = wait(DOC ? &qg_ok[s] : &full[halves ? 2 * s + h : 2 * s], j / C::NS);
           tc_fence_after();
           return there;
         };
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 2 && docs) {
+    } else if (warp == 2 && DOC) {
       // ---------------------------------------------------------------- padded queries
       TileIter it = first;
       for (int j = 0; j < n; ++j) {
@@ -425,35 +427,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_addr + quarter * 32;
     const uint32_t tP = tS + 128;
     const bool key_valid = key < p.Nk;
-    const int my_doc = docs ? p.k_ids[(static_cast<size_t>(b) * p.Tk + kt) * 128 + row] : 0;  // padding: -1
+    const int my_doc = DOC ? p.k_ids[(static_cast<size_t>(b) * p.Tk + kt) * 128 + row] : 0;  // padding: -1
     const bool all_rows = !p.causal || key < prefix;
     const bool all_keys = !p.causal || kt * 128 + 127 < prefix;
-    const bool cap = MOD && p.cap.on;
-    const bool bias = MOD && p.slopes != nullptr;
     const float mul = p.mul;
     const uint64_t mul2 = f2_pack(mul, mul);
     const float im = 1.f / mul;
     const float4* tok4 = reinterpret_cast<const float4*>(row_tok) + quarter * 8;
     const float4* sl4 = reinterpret_cast<const float4*>(row_slope) + quarter * 8;
     TileIter it = first;
+    // the tile's index and, where its documents differ, the id of row `lane` of this quarter, fetched a step ahead
+    int qt_next = n > 0 ? it.next() : 0, id_next = 0;
+    auto fetch_id = [&]() {
+      if (DOC && !tile_bit(whole, qt_next - lo))
+        id_next = __ldg(p.q_ids + (static_cast<size_t>(b) * p.Tq + qt_next) * 128 + quarter * 32 + lane);
+    };
+    if (n > 0) fetch_id();
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const int s = i % C::NS;
-      const int qt = it.next();
+      const int qt = qt_next, id = id_next;
+      const bool mixed = DOC && !tile_bit(whole, qt - lo);
+      if (i + 1 < n) {
+        qt_next = it.next();
+        fetch_id();
+      }
       const float4* nl4 = reinterpret_cast<const float4*>(smem + C::OFF_STAT + s * 1024) + quarter * 8;
       const float4* dl4 = nl4 + 32;
       // this key's place among the tile's tokens: token c sees it when c >= at
       const int at_i = key - off - qt * p.tpt;
       const float at = static_cast<float>(at_i);
-      const int4* ids = nullptr;
-      bool partial = !all_keys && kt * 128 + 127 > off + qt * p.tpt;
-      if (docs) {
-        const size_t q_at = static_cast<size_t>(b) * p.Tq + qt;
-        if (!docs_same(mine, p.q_ranges[q_at])) {
-          partial = true;
-          ids = reinterpret_cast<const int4*>(p.q_ids + q_at * 128) + quarter * 8;
-        }
-      }
+      const bool partial = mixed || (!all_keys && kt * 128 + 127 > off + qt * p.tpt);
       // the statistics of this stage, then the scores
       if (!mbar_wait_warp(&q_full[halves ? 2 * s + half : 2 * s], (i / C::NS) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX) ||
           !mbar_wait_warp(&s_full[half], i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
@@ -465,12 +469,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       float w[32];   // 1 - t^2
       tmem_ld32(tS, pv);
       tmem_wait_ld();
-      if (cap) {
+      if (CAP) {
         cap_scores<32>(pv, p.cap);
 #pragma unroll
         for (int c = 0; c < 32; c += 2) f2_unpack(cap_slope2(f2_pack(pv[c], pv[c + 1]), p.cap), w[c], w[c + 1]);
       }
-      if (bias) {
+      if (BIAS) {
         // The statistics hold nl - slope token. With token >= key the bias is -slope (token - at), of which
         // slope at is left; else slope (token - at), and otherwise the two cases element by element.
         const bool after = __all_sync(0xffffffffu, at_i <= 0);
@@ -511,15 +515,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
           const float4 tk = tok4[c >> 2];
-          int4 id = make_int4(my_doc, my_doc, my_doc, my_doc);
-          if (ids) id = __ldg(ids + (c >> 2));  // padded queries hold -2, which no key's id equals
-          const bool v0 = (all_rows || tk.x >= at) && id.x == my_doc, v1 = (all_rows || tk.y >= at) && id.y == my_doc;
-          const bool v2 = (all_rows || tk.z >= at) && id.z == my_doc, v3 = (all_rows || tk.w >= at) && id.w == my_doc;
+          bool v0 = all_rows || tk.x >= at, v1 = all_rows || tk.y >= at;
+          bool v2 = all_rows || tk.z >= at, v3 = all_rows || tk.w >= at;
+          if (mixed) {  // padded queries hold -2, which no key's id equals
+            // every lane takes part in the shuffles: none stands behind a condition that differs between lanes
+            const int i0 = __shfl_sync(0xffffffffu, id, c), i1 = __shfl_sync(0xffffffffu, id, c + 1);
+            const int i2 = __shfl_sync(0xffffffffu, id, c + 2), i3 = __shfl_sync(0xffffffffu, id, c + 3);
+            v0 = v0 && i0 == my_doc;
+            v1 = v1 && i1 == my_doc;
+            v2 = v2 && i2 == my_doc;
+            v3 = v3 && i3 == my_doc;
+          }
           pv[c] = v0 ? pv[c] : 0.f;
           pv[c + 1] = v1 ? pv[c + 1] : 0.f;
           pv[c + 2] = v2 ? pv[c + 2] : 0.f;
           pv[c + 3] = v3 ? pv[c + 3] : 0.f;
-          if (cap) {  // a padded key's scores may be NaN
+          if (CAP) {  // a padded key's scores may be NaN
             w[c] = v0 ? w[c] : 0.f;
             w[c + 1] = v1 ? w[c + 1] : 0.f;
             w[c + 2] = v2 ? w[c + 2] : 0.f;
@@ -533,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(pv[2 * c], pv[2 * c + 1]);
         tmem_st16u(tS, pk);  // over scores that this thread has read
       }
-      if (cap) {
+      if (CAP) {
 #pragma unroll
         for (int c = 0; c < 32; c += 2)
           f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_pack(w[c], w[c + 1])), pv[c], pv[c + 1]);
@@ -586,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   teardown(abort_flag, done, kv_full, n > 0 ? 1 + 4 * C::NS : 0, tmem);
 }
 
-template <int D, bool MOD>
+template <int D, bool CAP, bool BIAS, bool DOC>
 __global__ void __launch_bounds__(kThreads, 1)
     ex_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
@@ -632,9 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int prefix = p.prefix ? p.prefix[b] : 0;
   auto limit = [&](int pos) { return p.causal ? min(p.Nk, max(max(pos + 1, prefix), 0)) : p.Nk; };
   const int hi = (limit(off + min(p.Nq, (qt + 1) * p.tpt) - 1) + 127) >> 7;
-  const bool docs = p.k_ranges != nullptr;
   const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
-  const int4 mine = docs ? p.q_ranges[static_cast<size_t>(b) * p.Tq + qt] : none;
+  const int4 mine = DOC ? p.q_ranges[static_cast<size_t>(b) * p.Tq + qt] : none;
   const int rt = p.tpt * p.g;
 
   if (threadIdx.x == 0) {
@@ -672,8 +682,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int n = hi;
-  if (docs) n = build_tile_bits(bits, count, p.k_ranges + static_cast<size_t>(b) * p.Tk, 0, hi, mine, none);
-  const TileIter first{docs ? bits : nullptr, 0, 0};
+  const uint32_t* whole = bits + ((p.Tk + 31) >> 5);
+  if (DOC)
+    n = build_tile_bits(bits, bits + ((p.Tk + 31) >> 5), nullptr, count, p.k_ranges + static_cast<size_t>(b) * p.Tk, 0,
+                        hi, mine, none);
+  const TileIter first{DOC ? bits : nullptr, 0, 0};
   const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
   // TMEM: S | dP 0 | dQ | dP 1
   auto dp_buf = [&](int i) { return tmem + ((i & 1) ? 384u : 128u); };
@@ -697,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(bar);
         };
         auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
-        uint64_t* ready = docs ? k_ok : k_full;
+        uint64_t* ready = DOC ? k_ok : k_full;
         // S(j) and dP(j): S is free once the softmax has read S(j - 1), dP's buffer once dQ(j - 2) was issued
         auto both = [&](int j) {
           if (j > 0 && !wait(s_read, j - 1)) return false;
@@ -757,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 2 && docs) {
+    } else if (warp == 2 && DOC) {
       // ---------------------------------------------------------------- padded keys
       TileIter it = first;
       for (int j = 0; j < n; ++j) {
@@ -792,25 +805,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pos = off + tok;
     const int lim = limit(pos) - quarter * 32;
     const int lim_all = limit(off + qt * p.tpt);
-    const int my_doc = docs ? p.q_ids[(static_cast<size_t>(b) * p.Tq + qt) * 128 + row] : 0;  // padding: -2
-    const bool cap = MOD && p.cap.on;
-    const bool bias = MOD && p.slopes != nullptr;
+    const int my_doc = DOC ? p.q_ids[(static_cast<size_t>(b) * p.Tq + qt) * 128 + row] : 0;  // padding: -2
     const float mul = p.mul;
-    const float slope = bias && row_valid ? p.slopes[head] * kLog2e / mul : 0.f;
+    const float slope = BIAS && row_valid ? p.slopes[head] * kLog2e / mul : 0.f;
     const uint64_t mul2 = f2_pack(mul, mul);
     TileIter it = first;
+    // the tile's index and, where its documents differ, the id of key `lane` of this quarter, fetched a step ahead
+    int kt_next = n > 0 ? it.next() : 0, id_next = 0;
+    auto fetch_id = [&]() {
+      if (DOC && !tile_bit(whole, kt_next))
+        id_next = __ldg(p.k_ids + (static_cast<size_t>(b) * p.Tk + kt_next) * 128 + quarter * 32 + lane);
+    };
+    if (n > 0) fetch_id();
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int kt = it.next();
-      const int4* ids = nullptr;
-      bool partial = (kt + 1) * 128 > lim_all;
-      if (docs) {
-        const size_t at = static_cast<size_t>(b) * p.Tk + kt;
-        if (!docs_same(mine, p.k_ranges[at])) {
-          partial = true;
-          ids = reinterpret_cast<const int4*>(p.k_ids + at * 128) + quarter * 8;
-        }
+      const int kt = kt_next, id = id_next;
+      const bool mixed = DOC && !tile_bit(whole, kt);
+      if (i + 1 < n) {
+        kt_next = it.next();
+        fetch_id();
       }
+      const bool partial = mixed || (kt + 1) * 128 > lim_all;
       if (!mbar_wait_warp(s_full, i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
         ok = false;
         break;
@@ -822,13 +837,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(s_read);
-      if (cap) {
+      if (CAP) {
         cap_scores<32>(pv, p.cap);
 #pragma unroll
         for (int c = 0; c < 32; c += 2) f2_unpack(cap_slope2(f2_pack(pv[c], pv[c + 1]), p.cap), w[c], w[c + 1]);
       }
       uint64_t e2 = negl2;
-      if (bias) {
+      if (BIAS) {
         const float e = fmaf(add_bias<32>(pv, slope, static_cast<float>(pos - kt * 128 - quarter * 32)), mul, negl);
         e2 = f2_pack(e, e);
       }
@@ -839,21 +854,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         pv[c] = fast_exp2(x0);
         pv[c + 1] = fast_exp2(x1);
       }
-      if (cap) {
+      if (CAP) {
 #pragma unroll
         for (int c = 0; c < 32; c += 2)
           f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_pack(w[c], w[c + 1])), pv[c], pv[c + 1]);
       }
       if (partial) {
         const int valid = lim - kt * 128;
-        if (ids) {
+        if (mixed) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const int4 id = __ldg(ids + (c >> 2));
-            pv[c] = (c < valid && id.x == my_doc) ? pv[c] : 0.f;
-            pv[c + 1] = (c + 1 < valid && id.y == my_doc) ? pv[c + 1] : 0.f;
-            pv[c + 2] = (c + 2 < valid && id.z == my_doc) ? pv[c + 2] : 0.f;
-            pv[c + 3] = (c + 3 < valid && id.w == my_doc) ? pv[c + 3] : 0.f;
+          for (int c = 0; c < 32; ++c) {
+            const int i_c = __shfl_sync(0xffffffffu, id, c);  // every lane takes part
+            pv[c] = (c < valid && i_c == my_doc) ? pv[c] : 0.f;
           }
         } else {
 #pragma unroll
@@ -900,16 +912,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-template <int D, bool MOD>
+template <int D, bool CAP, bool BIAS, bool DOC>
 cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk, const CUtensorMap* tv,
                        const ExTile& p, cudaStream_t s) {
   static KernelReady ready_kv, ready_q;
-  cudaError_t e = make_ready(ready_kv, ex_dkv_kernel<D, MOD>, DkvCfg<D>::SMEM + 8192, kLaunchRegs);
+  cudaError_t e = make_ready(ready_kv, ex_dkv_kernel<D, CAP, BIAS, DOC>, DkvCfg<D>::SMEM + 16384, kLaunchRegs);  // 2^16 query tiles
   if (e != cudaSuccess) return e;
-  if ((e = make_ready(ready_q, ex_dq_kernel<D, MOD>, DqCfg<D>::SMEM + 1024, kLaunchRegs)) != cudaSuccess) return e;
-  const unsigned bits_q = p.k_ranges ? (p.Tq + 31) / 32 * 4u : 0u, bits_k = p.k_ranges ? (p.Tk + 31) / 32 * 4u : 0u;
-  ex_dkv_kernel<D, MOD><<<p.B * p.Hkv * p.Tk, kThreads, DkvCfg<D>::SMEM + bits_q, s>>>(*tq, *tg, *tk, *tv, p);
-  ex_dq_kernel<D, MOD><<<p.B * p.Hkv * p.Tq, kThreads, DqCfg<D>::SMEM + bits_k, s>>>(*tq, *tg, *tk, *tv, p);
+  if ((e = make_ready(ready_q, ex_dq_kernel<D, CAP, BIAS, DOC>, DqCfg<D>::SMEM + 1024, kLaunchRegs)) != cudaSuccess) return e;  // 2^12 key tiles
+  const unsigned bits_q = DOC ? (p.Tq + 31) / 32 * 8u : 0u, bits_k = DOC ? (p.Tk + 31) / 32 * 8u : 0u;
+  ex_dkv_kernel<D, CAP, BIAS, DOC><<<p.B * p.Hkv * p.Tk, kThreads, DkvCfg<D>::SMEM + bits_q, s>>>(*tq, *tg, *tk, *tv, p);
+  ex_dq_kernel<D, CAP, BIAS, DOC><<<p.B * p.Hkv * p.Tq, kThreads, DqCfg<D>::SMEM + bits_k, s>>>(*tq, *tg, *tk, *tv, p);
   note_launches(2);
   return cudaGetLastError();
 }
@@ -928,9 +940,9 @@ cudaError_t launch_ex_row_stats(int d, const ExTile& p, const uint16_t* o, const
 
 cudaError_t launch_ex_bwd(int d, const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk,
                           const CUtensorMap* tv, const ExTile& p, cudaStream_t s) {
-  const bool mod = p.cap.on || p.slopes;
-  if (d == 64) return mod ? launch_bwd<64, true>(tq, tg, tk, tv, p, s) : launch_bwd<64, false>(tq, tg, tk, tv, p, s);
-  return mod ? launch_bwd<128, true>(tq, tg, tk, tv, p, s) : launch_bwd<128, false>(tq, tg, tk, tv, p, s);
+  return with_options(d, p, [&](auto D, auto CAP, auto BIAS, auto DOC) {
+    return launch_bwd<D.value, CAP.value, BIAS.value, DOC.value>(tq, tg, tk, tv, p, s);
+  });
 }
 
 }  // namespace mcs

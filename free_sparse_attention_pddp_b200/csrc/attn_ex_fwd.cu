@@ -53,12 +53,12 @@ struct FwdCfg {
   static constexpr uint32_t NBAR = 1 + 5 * NS + 2 + 2 + 2 + 1;
   static constexpr uint32_t OFF_MAX = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;  // [parity][slot][half][row]
   static constexpr uint32_t OFF_BITS = OFF_MAX + 2 * 2 * 2 * 128 * 8;
-  static constexpr uint32_t SMEM = OFF_BITS + 1024;  // and 4 bytes for each 32 key tiles under a document mask
+  static constexpr uint32_t SMEM = OFF_BITS + 1024;  // and three bits for each key tile under a document mask
 };
 
 }  // namespace
 
-template <int D, bool MOD>
+template <int D, bool CAP, bool BIAS, bool DOC>
 __global__ void __launch_bounds__(kThreads, 1)
     ex_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
@@ -118,10 +118,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int T = (limit(off + last_tok(has1 ? qt0 + 1 : qt0)) + 127) >> 7;
   const int lo = static_cast<int>(static_cast<long long>(split) * T / p.nsplit);
   const int hi = static_cast<int>(static_cast<long long>(split + 1) * T / p.nsplit);
-  const bool docs = p.k_ranges != nullptr;
   const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
   int4 r0 = none, r1 = none;
-  if (docs) {
+  if (DOC) {
     r0 = p.q_ranges[b * p.Tq + qt0];
     if (has1) r1 = p.q_ranges[b * p.Tq + qt0 + 1];
   }
@@ -163,8 +162,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int n = hi - lo;  // key tiles of this CTA
-  if (docs) n = build_tile_bits(bits, count, p.k_ranges + static_cast<size_t>(b) * p.Tk, lo, hi, r0, r1);
-  const TileIter first{docs ? bits : nullptr, lo, lo};
+  const int bit_words = (p.Tk + 31) >> 5;
+  if (DOC)
+    n = build_tile_bits(bits, bits + bit_words, bits + 2 * bit_words, count,
+                        p.k_ranges + static_cast<size_t>(b) * p.Tk, lo, hi, r0, r1);
+  const TileIter first{DOC ? bits : nullptr, lo, lo};
   // key tiles of the slots, in the order of the CTA's list
   const int n0 = single ? (n + 1) >> 1 : n;
   const int n1 = single ? n >> 1 : (has1 ? n : 0);
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
         const uint64_t dV = sdesc_sw128(smem_u32(sV), 16384, 1024);
-        uint64_t* v_bar = docs ? v_ok : v_full;
+        uint64_t* v_bar = DOC ? v_ok : v_full;
         // S_t = Q_t K^T with the CTA's list entry j
         auto issue_s = [&](int t, int j) {
           const uint64_t dQt = sdesc_advance(dQ, single ? 0 : t * C::TILE);
@@ -267,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp == 2 && docs) {
+    } else if (warp == 2 && DOC) {
       // ---------------------------------------------------------------- padded keys
       TileIter it = first;
       for (int j = 0; j < n; ++j) {
@@ -303,24 +305,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pos = p.lens ? p.P + min(max(row_valid ? p.lens[tok] : 0, 0), p.C) - 1 : off + tok;
     const int lim = limit(pos) - half * 64;
     const int lim_all = limit(off + qt * p.tpt);  // keys that every row of the tile sees
-    const int4 mine = t == 0 || single ? r0 : r1;
-    int my_doc = docs && row_valid ? p.doc_q[static_cast<size_t>(b) * p.Nq + tok] : -2;
+    const uint32_t* whole = bits + (t == 0 || single ? 1 : 2) * bit_words;
+    int my_doc = DOC && row_valid ? p.doc_q[static_cast<size_t>(b) * p.Nq + tok] : -2;
     if (my_doc < 0) my_doc = -2;  // a padded query matches no key
-    const bool bias = MOD && p.slopes != nullptr;
     const float mul = p.mul;  // what turns a score into log2 units
-    const float slope = bias && row_valid ? p.slopes[head] * kLog2e / mul : 0.f;
+    const float slope = BIAS && row_valid ? p.slopes[head] * kLog2e / mul : 0.f;
     const uint64_t mul2 = f2_pack(mul, mul);
     float2* my_max = row_max + (t * 2 + half) * 128 + row;
     const float2* other_max = row_max + (t * 2 + (half ^ 1)) * 128 + row;
     const int pair_bar = 2 + t * 4 + wq;  // the two warps that share these rows
     TileIter it = first;
     if (single && t == 1 && nt > 0) it.next();
+    // the tile's index and, where its documents differ, the ids of keys `lane` and 32 + `lane` of this half; both are
+    // fetched a step ahead
+    int kt_next = nt > 0 ? it.next() : 0, id0_next = 0, id1_next = 0;
+    auto fetch_ids = [&]() {
+      if (DOC && !tile_bit(whole, kt_next - lo)) {
+        const int* at = p.k_ids + (static_cast<size_t>(b) * p.Tk + kt_next) * 128 + half * 64 + lane;
+        id0_next = __ldg(at);
+        id1_next = __ldg(at + 32);
+      }
+    };
+    if (nt > 0) fetch_ids();
     float m = -CUDART_INF_F;  // running max, log2 units (the same in both halves)
     float l = 0.f;            // this half's sum
     bool ok = true;
     for (int i = 0; i < nt; ++i) {
-      const int kt = it.next();
-      if (single && i + 1 < nt) it.next();
+      const int kt = kt_next, id0 = id0_next, id1 = id1_next;
+      const bool mixed = DOC && !tile_bit(whole, kt - lo);
+      if (i + 1 < nt) {
+        if (single) it.next();
+        kt_next = it.next();
+        fetch_ids();
+      }
       ok = ok && mbar_wait_warp(&s_full[t], i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX);
       tc_fence_after();
       float sv[64];  // after a failed wait: whatever the columns hold
@@ -328,29 +345,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(tS + 32, sv + 32);
       tmem_wait_ld();
       float shift = 0.f;  // log2 units that the whole row of this tile lacks
-      if (MOD) {
-        if (p.cap.on) cap_scores<64>(sv, p.cap);
-        if (bias) shift = add_bias<64>(sv, slope, static_cast<float>(pos - kt * 128 - half * 64)) * mul;
+      if (CAP) cap_scores<64>(sv, p.cap);
+      if (BIAS) {
+        shift = add_bias<64>(sv, slope, static_cast<float>(pos - kt * 128 - half * 64)) * mul;
       }
-      const int4* ids = nullptr;
-      bool partial = (kt + 1) * 128 > lim_all;
-      if (docs) {
-        const size_t at = static_cast<size_t>(b) * p.Tk + kt;
-        if (!docs_same(mine, p.k_ranges[at])) {
-          partial = true;
-          ids = reinterpret_cast<const int4*>(p.k_ids + at * 128) + half * 16;
-        }
-      }
-      if (partial) {
+      if (mixed || (kt + 1) * 128 > lim_all) {
         const int valid = lim - kt * 128;
-        if (ids) {
+        if (mixed) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            const int4 k4 = __ldg(ids + (c >> 2));  // padded keys hold -1, which no query's id equals
-            sv[c] = (c < valid && k4.x == my_doc) ? sv[c] : -CUDART_INF_F;
-            sv[c + 1] = (c + 1 < valid && k4.y == my_doc) ? sv[c + 1] : -CUDART_INF_F;
-            sv[c + 2] = (c + 2 < valid && k4.z == my_doc) ? sv[c + 2] : -CUDART_INF_F;
-            sv[c + 3] = (c + 3 < valid && k4.w == my_doc) ? sv[c + 3] : -CUDART_INF_F;
+          for (int c = 0; c < 64; ++c) {
+            const int id = __shfl_sync(0xffffffffu, c < 32 ? id0 : id1, c & 31);  // padding: -1, which no query has
+            sv[c] = (c < valid && id == my_doc) ? sv[c] : -CUDART_INF_F;
           }
         } else {
 #pragma unroll
@@ -572,14 +577,14 @@ __global__ void __launch_bounds__(128) ex_doc_tiles(const ExTile p, int* k_ids, 
   if (i == 0) (key ? k_ranges : q_ranges)[at] = make_int4(s_min, s_max, s_pad, 0);
 }
 
-template <int D, bool MOD>
+template <int D, bool CAP, bool BIAS, bool DOC>
 cudaError_t launch_fwd(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const ExTile& p,
                        cudaStream_t s) {
-  auto kern = ex_fwd_kernel<D, MOD>;
-  const unsigned bits = p.k_ranges ? (p.Tk + 31) / 32 * 4u : 0u;
+  auto kern = ex_fwd_kernel<D, CAP, BIAS, DOC>;
+  const unsigned bits = DOC ? (p.Tk + 31) / 32 * 12u : 0u;
   const unsigned smem = FwdCfg<D>::SMEM + bits;
   static KernelReady ready;
-  const cudaError_t e = make_ready(ready, kern, FwdCfg<D>::SMEM + 8192, kLaunchRegs);  // 8192: 2^16 tiles
+  const cudaError_t e = make_ready(ready, kern, FwdCfg<D>::SMEM + 1536, kLaunchRegs);  // 2^12 tiles
   if (e != cudaSuccess) return e;
   const int per = p.single ? 1 : 2;
   const long long grid = static_cast<long long>(p.B) * p.Hkv * ((p.Tq + per - 1) / per) * p.nsplit;
@@ -592,9 +597,9 @@ cudaError_t launch_fwd(const CUtensorMap* tq, const CUtensorMap* tk, const CUten
 
 cudaError_t launch_ex_fwd(int d, const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const ExTile& p,
                           cudaStream_t s) {
-  const bool mod = p.cap.on || p.slopes;
-  if (d == 64) return mod ? launch_fwd<64, true>(tq, tk, tv, p, s) : launch_fwd<64, false>(tq, tk, tv, p, s);
-  return mod ? launch_fwd<128, true>(tq, tk, tv, p, s) : launch_fwd<128, false>(tq, tk, tv, p, s);
+  return with_options(d, p, [&](auto D, auto CAP, auto BIAS, auto DOC) {
+    return launch_fwd<D.value, CAP.value, BIAS.value, DOC.value>(tq, tk, tv, p, s);
+  });
 }
 
 cudaError_t launch_ex_combine(int d, const ExTile& p, int parts, cudaStream_t s) {

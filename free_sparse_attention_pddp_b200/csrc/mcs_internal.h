@@ -132,11 +132,12 @@ struct ExParams {
 // The score cap: y(s) = cap log2(e) tanh(k s), k = scale / cap, for products s = q . k (cap_scores in attn_ex.cuh).
 struct CapFn {
   int on;
-  float k, cl;       // cl = cap log2 e
+  float k2, cl;      // 2 k log2 e, cap log2 e
   float z2, z3;      // s^2 up to which the coefficients b, and a, hold (-1: never)
   float a[5], b[4];  // y = s Q(s^2)
   float neg_icl2;    // -1 / cl^2
 };
+// tanh(x) = x + x z P(z), z = x^2: the coefficients of P, degree 3
 constexpr float kTanhP0 = -0.333323412f, kTanhP1 = 0.133081745f, kTanhP2 = -0.0519478787f, kTanhP3 = 0.0151953385f;
 constexpr float kTanhR0 = -0.333318822f, kTanhR1 = 0.132776282f, kTanhR2 = -0.0477941821f;  // degree 2, |x| <= 0.4
 

@@ -268,7 +268,7 @@ typedef struct mcs_attn_opts {
                             values outside [0, Nk] act as the nearest bound */
   const int32_t* doc_q;  /* int32 [B, Nq] and */
   const int32_t* doc_k;  /* int32 [B, Nk]: document ids in any order, both given or both null (the same
-                            array may serve as both); at most 2^20 keys, and 2^16 tiles of
+                            array may serve as both); at most 2^19 keys, and 2^16 tiles of
                             floor(128 / (Hq / Hkv)) queries, else MCS_ERR_UNSUPPORTED */
 } mcs_attn_opts;
 

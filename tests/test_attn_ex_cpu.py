@@ -126,9 +126,9 @@ def test_attn_arguments_are_refused(mcs):
     for o in (mcs.AttnOpts(None, None, doc, None), mcs.AttnOpts(None, None, None, doc), mcs.AttnOpts(None, doc, None, None),
               mcs.AttnOpts(doc + 2, None, None, None)):
         assert fwd(ct.byref(o)) == 1 and bwd(ct.byref(o)) == 1
-    # more document tiles than the bitmaps hold: 2^13 of 128 keys, 2^16 of one token (128 heads to a KV head)
+    # more document tiles than the bitmaps hold: 2^12 of 128 keys, 2^16 of one token (128 heads to a KV head)
     docs = mcs.AttnOpts(None, None, doc, doc)
-    assert fwd(ct.byref(docs), s=mcs.AttnShape(1, 1, 1, 1, (1 << 20) + 1, 64)) == 2
+    assert fwd(ct.byref(docs), s=mcs.AttnShape(1, 1, 1, 1, (1 << 19) + 1, 64)) == 2
     assert fwd(ct.byref(docs), s=mcs.AttnShape(1, 128, 1, (1 << 16) + 1, 10, 64)) == 2
 
 
