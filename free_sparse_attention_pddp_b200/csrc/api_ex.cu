@@ -123,7 +123,7 @@ FwdPlan fwd_plan(int B, int Hkv, int g, int Nq, int Nk, int d) {
 
 // workspace: status | document tiles | partials of the key splits
 struct FwdWs {
-  size_t k_ids, k_ranges, q_ranges, part_lse, part_o, total;
+  size_t k_ids, k_ranges, q_ranges, order, part_lse, part_o, total;
 };
 
 FwdWs fwd_layout(const FwdPlan& f, int B, int Hkv, int d) {
@@ -137,6 +137,7 @@ FwdWs fwd_layout(const FwdPlan& f, int B, int Hkv, int d) {
   w.k_ids = take(static_cast<size_t>(B) * f.Tk * 512);
   w.k_ranges = take(static_cast<size_t>(B) * f.Tk * 16);
   w.q_ranges = take(static_cast<size_t>(B) * f.Tq * 16);
+  w.order = take(static_cast<size_t>(B) * f.Tq * 4);
   const size_t rows = f.parts > 1 ? static_cast<size_t>(f.parts) * B * Hkv * f.Tq * 128 : 0;
   w.part_lse = take(rows * 4);
   w.part_o = take(rows * d * 4);
@@ -146,7 +147,7 @@ FwdWs fwd_layout(const FwdPlan& f, int B, int Hkv, int d) {
 
 // workspace: status | document tiles | statistics of the packed rows
 struct BwdWs {
-  size_t k_ids, k_ranges, q_ids, q_ranges, stats, total;
+  size_t k_ids, k_ranges, q_ids, q_ranges, order, k_order, stats, total;
 };
 
 BwdWs bwd_layout(const FwdPlan& f, int B, int Hkv) {
@@ -161,6 +162,8 @@ BwdWs bwd_layout(const FwdPlan& f, int B, int Hkv) {
   w.k_ranges = take(static_cast<size_t>(B) * f.Tk * 16);
   w.q_ids = take(static_cast<size_t>(B) * f.Tq * 512);
   w.q_ranges = take(static_cast<size_t>(B) * f.Tq * 16);
+  w.order = take(static_cast<size_t>(B) * f.Tq * 4);
+  w.k_order = take(static_cast<size_t>(B) * f.Tk * 4);
   w.stats = take(static_cast<size_t>(B) * Hkv * f.Tq * 1024);
   w.total = off;
   return w;
@@ -352,6 +355,12 @@ mcs_status mcs_dense_ex(const mcs_attn_shape* s, const mcs_attn_opts* opts, cons
     t.k_ids = ids;
     t.k_ranges = kr;
     t.q_ranges = qr;
+    // with more jobs than SMs their order matters
+    if (!f.single && static_cast<long long>(p.B) * p.Hkv * ((f.Tq + 1) / 2) > kSms) {
+      int* order = reinterpret_cast<int*>(base + w.order);
+      if (launch_ex_doc_order(t, 2, order, nullptr, stream) != cudaSuccess) return MCS_ERR_CUDA;
+      t.order = order;
+    }
   }
   if (f.parts > 1) {
     t.part_lse = reinterpret_cast<float*>(base + w.part_lse);
@@ -403,6 +412,13 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
     t.k_ranges = kr;
     t.q_ids = qid;
     t.q_ranges = qr;
+    if (static_cast<long long>(p.B) * p.Hkv * std::max(f.Tq, f.Tk) > kSms) {
+      int* order = reinterpret_cast<int*>(base + w.order);
+      int* k_order = reinterpret_cast<int*>(base + w.k_order);
+      if (launch_ex_doc_order(t, 1, order, k_order, stream) != cudaSuccess) return MCS_ERR_CUDA;
+      t.order = order;
+      t.k_order = k_order;
+    }
   }
   if (launch_ex_row_stats(s->d, t, static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(d_o), lse, stats,
                           stream) != cudaSuccess)

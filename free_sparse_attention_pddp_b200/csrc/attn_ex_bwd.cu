@@ -204,7 +204,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // causal: the first key tiles meet the most queries and go first, the heads of a chunk side by side
   const int BH = p.B * p.Hkv;
   int kt, bh;
-  if (p.causal) {
+  if (DOC && p.k_order) {  // the tiles with the most work first
+    const int at = p.k_order[blockIdx.x / p.Hkv];
+    bh = at / p.Tk * p.Hkv + blockIdx.x % p.Hkv;
+    kt = at % p.Tk;
+  } else if (p.causal) {
     const int per_chunk = p.chunk * p.Tk;
     const int ch = blockIdx.x / per_chunk, in = blockIdx.x % per_chunk;
     const int heads = min(p.chunk, BH - ch * p.chunk);
@@ -436,22 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float4* tok4 = reinterpret_cast<const float4*>(row_tok) + quarter * 8;
     const float4* sl4 = reinterpret_cast<const float4*>(row_slope) + quarter * 8;
     TileIter it = first;
-    // the tile's index and, where its documents differ, the id of row `lane` of this quarter, fetched a step ahead
-    int qt_next = n > 0 ? it.next() : 0, id_next = 0;
-    auto fetch_id = [&]() {
-      if (DOC && !tile_bit(whole, qt_next - lo))
-        id_next = __ldg(p.q_ids + (static_cast<size_t>(b) * p.Tq + qt_next) * 128 + quarter * 32 + lane);
-    };
-    if (n > 0) fetch_id();
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const int s = i % C::NS;
-      const int qt = qt_next, id = id_next;
+      const int qt = it.next();
+      // where the tile's documents differ: the id of row `lane` of this quarter, under way while S is
       const bool mixed = DOC && !tile_bit(whole, qt - lo);
-      if (i + 1 < n) {
-        qt_next = it.next();
-        fetch_id();
-      }
+      int id = 0;
+      if (mixed) id = __ldg(p.q_ids + (static_cast<size_t>(b) * p.Tq + qt) * 128 + quarter * 32 + lane);
       const float4* nl4 = reinterpret_cast<const float4*>(smem + C::OFF_STAT + s * 1024) + quarter * 8;
       const float4* dl4 = nl4 + 32;
       // this key's place among the tile's tokens: token c sees it when c >= at
@@ -628,7 +624,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   const int BH = p.B * p.Hkv;
   int qt, bh;
-  if (p.causal) {  // the last query tiles see the most keys and go first
+  if (DOC && p.order) {
+    const int at = p.order[blockIdx.x / p.Hkv];
+    bh = at / p.Tq * p.Hkv + blockIdx.x % p.Hkv;
+    qt = at % p.Tq;
+  } else if (p.causal) {  // the last query tiles see the most keys and go first
     const int per_chunk = p.chunk * p.Tq;
     const int ch = blockIdx.x / per_chunk, in = blockIdx.x % per_chunk;
     const int heads = min(p.chunk, BH - ch * p.chunk);
@@ -810,21 +810,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float slope = BIAS && row_valid ? p.slopes[head] * kLog2e / mul : 0.f;
     const uint64_t mul2 = f2_pack(mul, mul);
     TileIter it = first;
-    // the tile's index and, where its documents differ, the id of key `lane` of this quarter, fetched a step ahead
-    int kt_next = n > 0 ? it.next() : 0, id_next = 0;
-    auto fetch_id = [&]() {
-      if (DOC && !tile_bit(whole, kt_next))
-        id_next = __ldg(p.k_ids + (static_cast<size_t>(b) * p.Tk + kt_next) * 128 + quarter * 32 + lane);
-    };
-    if (n > 0) fetch_id();
     bool ok = true;
     for (int i = 0; i < n; ++i) {
-      const int kt = kt_next, id = id_next;
+      const int kt = it.next();
+      // where the tile's documents differ: the id of key `lane` of this quarter, under way while S is
       const bool mixed = DOC && !tile_bit(whole, kt);
-      if (i + 1 < n) {
-        kt_next = it.next();
-        fetch_id();
-      }
+      int id = 0;
+      if (mixed) id = __ldg(p.k_ids + (static_cast<size_t>(b) * p.Tk + kt) * 128 + quarter * 32 + lane);
       const bool partial = mixed || (kt + 1) * 128 > lim_all;
       if (!mbar_wait_warp(s_full, i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX)) {
         ok = false;

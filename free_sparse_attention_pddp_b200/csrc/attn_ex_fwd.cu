@@ -97,7 +97,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   u /= p.nsplit;
   int job, bh;
   const int BH = p.B * p.Hkv;
-  if (p.causal) {
+  if (DOC && p.order) {  // the jobs with the most key tiles first
+    const int at = p.order[u / p.Hkv];
+    bh = at / groups * p.Hkv + u % p.Hkv;
+    job = at % groups;
+  } else if (p.causal) {
     const int per_chunk = p.chunk * groups;
     const int ch = u / per_chunk, in = u % per_chunk;
     const int heads = min(p.chunk, BH - ch * p.chunk);
@@ -316,27 +320,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pair_bar = 2 + t * 4 + wq;  // the two warps that share these rows
     TileIter it = first;
     if (single && t == 1 && nt > 0) it.next();
-    // the tile's index and, where its documents differ, the ids of keys `lane` and 32 + `lane` of this half; both are
-    // fetched a step ahead
-    int kt_next = nt > 0 ? it.next() : 0, id0_next = 0, id1_next = 0;
-    auto fetch_ids = [&]() {
-      if (DOC && !tile_bit(whole, kt_next - lo)) {
-        const int* at = p.k_ids + (static_cast<size_t>(b) * p.Tk + kt_next) * 128 + half * 64 + lane;
-        id0_next = __ldg(at);
-        id1_next = __ldg(at + 32);
-      }
-    };
-    if (nt > 0) fetch_ids();
     float m = -CUDART_INF_F;  // running max, log2 units (the same in both halves)
     float l = 0.f;            // this half's sum
     bool ok = true;
     for (int i = 0; i < nt; ++i) {
-      const int kt = kt_next, id0 = id0_next, id1 = id1_next;
+      const int kt = it.next();
+      if (single && i + 1 < nt) it.next();
+      // where the tile's documents differ: the ids of keys `lane` and 32 + `lane` of this half, under way while S is
       const bool mixed = DOC && !tile_bit(whole, kt - lo);
-      if (i + 1 < nt) {
-        if (single) it.next();
-        kt_next = it.next();
-        fetch_ids();
+      int id0 = 0, id1 = 0;
+      if (mixed) {
+        const int* at = p.k_ids + (static_cast<size_t>(b) * p.Tk + kt) * 128 + half * 64 + lane;
+        id0 = __ldg(at);
+        id1 = __ldg(at + 32);
       }
       ok = ok && mbar_wait_warp(&s_full[t], i & 1, wctx, MCS_WHERE_ATTN_SOFTMAX);
       tc_fence_after();
@@ -577,6 +573,80 @@ __global__ void __launch_bounds__(128) ex_doc_tiles(const ExTile p, int* k_ids, 
   if (i == 0) (key ? k_ranges : q_ranges)[at] = make_int4(s_min, s_max, s_pad, 0);
 }
 
+// Order of the jobs of a document mask, those with the most tiles first: the
+// documents' lengths differ, and a long job that starts last runs alone. Job i
+// of request b is `per` query tiles (their key tiles) or, in the second CTA, one
+// key tile (its query tiles). A counting sort by one CTA: order[rank] = b jobs + i.
+__global__ void __launch_bounds__(1024) ex_doc_order(const ExTile p, int per, int* q_order, int* k_order) {
+  __shared__ int bins[4096 + 1];
+  __shared__ int sums[32];
+  const bool key = blockIdx.x == 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int jobs = key ? p.Tk : (p.Tq + per - 1) / per, all = jobs * p.B;
+  const int tiles = key ? p.Tq : p.Tk;
+  const int4* ranges = key ? p.q_ranges : p.k_ranges;
+  int* order = key ? k_order : q_order;
+  const int step = (tiles + 4095) / 4096;  // tiles per bin
+  for (int i = threadIdx.x; i <= 4096; i += 1024) bins[i] = 0;
+  __syncthreads();
+  const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
+  auto bin = [&](int at) {  // a whole warp: 4096 less the job's tiles
+    const int b = at / jobs, i = at % jobs, off = p.Nk - p.Nq;
+    const int prefix = p.prefix ? p.prefix[b] : 0;
+    int lo = 0, hi = tiles;
+    int4 r0, r1 = none;
+    if (key) {
+      r0 = p.k_ranges[static_cast<size_t>(b) * p.Tk + i];
+      if (p.causal && i * 128 >= prefix) lo = min(p.Tq, max(0, i * 128 - off) / p.tpt);
+    } else {
+      r0 = p.q_ranges[static_cast<size_t>(b) * p.Tq + i * per];
+      if (per == 2 && i * per + 1 < p.Tq) r1 = p.q_ranges[static_cast<size_t>(b) * p.Tq + i * per + 1];
+      const int last = off + min(p.Nq, (i + 1) * per * p.tpt) - 1;
+      if (p.causal) hi = (min(p.Nk, max(max(last + 1, prefix), 0)) + 127) >> 7;
+    }
+    int n = 0;
+    for (int t = lo + lane; t < hi; t += 32) {
+      const int4 r = ranges[static_cast<size_t>(b) * tiles + t];
+      n += docs_meet(r, r0) || docs_meet(r, r1);
+    }
+    return 4096 - __reduce_add_sync(0xffffffffu, n) / step;
+  };
+  for (int at = warp; at < all; at += 32) {
+    const int n = bin(at);
+    if (lane == 0) atomicAdd(&bins[n], 1);
+  }
+  __syncthreads();
+  // exclusive sums of the bins, four to a thread (the last bin, empty jobs, comes after them)
+  int mine[4], total = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    mine[e] = bins[threadIdx.x * 4 + e];
+    total += mine[e];
+  }
+  int incl = total;
+#pragma unroll
+  for (int w = 1; w < 32; w <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, w);
+    if (lane >= w) incl += y;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int before = incl - total;
+  for (int w = 0; w < warp; ++w) before += sums[w];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    bins[threadIdx.x * 4 + e] = before;
+    before += mine[e];
+  }
+  if (threadIdx.x == 1023) bins[4096] = before;
+  __syncthreads();
+  // equal jobs land in any order: it decides when they run, not what they compute
+  for (int at = warp; at < all; at += 32) {
+    const int n = bin(at);
+    if (lane == 0) order[atomicAdd(&bins[n], 1)] = at;
+  }
+}
+
 template <int D, bool CAP, bool BIAS, bool DOC>
 cudaError_t launch_fwd(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const ExTile& p,
                        cudaStream_t s) {
@@ -606,6 +676,12 @@ cudaError_t launch_ex_combine(int d, const ExTile& p, int parts, cudaStream_t s)
   const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.B) * p.Nq * p.Hq + 3) / 4);
   if (d == 64) ex_combine<64><<<grid, 128, 0, s>>>(p, parts);
   else ex_combine<128><<<grid, 128, 0, s>>>(p, parts);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ex_doc_order(const ExTile& p, int per, int* q_order, int* k_order, cudaStream_t s) {
+  ex_doc_order<<<k_order ? 2 : 1, 1024, 0, s>>>(p, per, q_order, k_order);
   note_launches(1);
   return cudaGetLastError();
 }
