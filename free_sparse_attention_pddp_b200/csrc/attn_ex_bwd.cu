@@ -276,7 +276,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
     if (warp == 0) {
       // ---------------------------------------------------------------- UMMA issuer
       if (n > 0 && elect_one()) {
@@ -417,11 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-    named_barrier_sync<1, kThreads>();
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
   } else {
     // ---------------------------------------------------------------- P and dS, then the epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int quarter = (warp - 4) >> 2;  // query rows 32 quarter .. 32 quarter + 31 of each tile
     const int half = quarter >> 1;
     const int wq = warp & 3;
@@ -587,8 +583,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       else store_row<D / 2>(tmem + lane_addr + 384 + c0, n > 0, key_valid, p.scale, p.dk + at + c0);
     }
     __syncwarp();
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
-    named_barrier_sync<1, kThreads>();
   }
   teardown(abort_flag, done, kv_full, n > 0 ? 1 + 4 * C::NS : 0, tmem);
 }
