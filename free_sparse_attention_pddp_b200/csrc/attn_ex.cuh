@@ -68,18 +68,19 @@ __device__ __forceinline__ void named_barrier_sync() {
   asm volatile("barrier.sync %0, %1;" ::"n"(ID), "n"(NTHREADS) : "memory");
 }
 
-// Tiles lo .. hi - 1 in order; with a bitmap (bit 0 of word 0: tile lo's
-// 32-aligned start), only those whose bit is set.
+// Tiles from `cur` on in order; with bitmaps, those that are in one of them
+// (bit 0 of word 0 is tile `base`).
 struct TileIter {
-  const uint32_t* bits;  // null: every tile
-  int cur, base;         // next candidate; tile of bit 0
+  const uint32_t *bits, *bits2;  // null: every tile, no second bitmap
+  int cur, base;
+  __device__ __forceinline__ uint32_t word(int w) const { return bits2 ? bits[w] | bits2[w] : bits[w]; }
   __device__ __forceinline__ int next() {
     if (!bits) return cur++;
     int i = cur - base;
-    uint32_t w = bits[i >> 5] >> (i & 31);
+    uint32_t w = word(i >> 5) >> (i & 31);
     while (!w) {  // the caller asks for no more tiles than there are
       i = (i | 31) + 1;
-      w = bits[i >> 5];
+      w = word(i >> 5);
     }
     i += __ffs(w) - 1;
     cur = base + i + 1;
@@ -94,35 +95,52 @@ __device__ __forceinline__ bool docs_same(int4 a, int4 b) {  // every pair of ro
   return a.x == a.y && b.x == b.y && a.x == b.x && !a.z && !b.z;
 }
 
-// For tiles lo .. hi - 1: sets the bits of those whose documents meet `mine` (or
-// `mine2`), in `whole` of those whose every pair with `mine` is valid (in
-// `whole2` with `mine2`, unless null), and returns the number of the first to
-// every thread. All threads of the CTA call it. `count` is a shared word that
-// is zero before.
-__device__ __forceinline__ int build_tile_bits(uint32_t* bits, uint32_t* whole, uint32_t* whole2, int* count,
-                                               const int4* ranges, int lo, int hi, int4 mine, int4 mine2) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  for (int w = warp; w * 32 < hi - lo; w += warps) {
-    const int t = lo + w * 32 + lane;
-    bool on = false, all = false, all2 = false;
-    if (t < hi) {
-      const int4 r = ranges[t];
-      on = docs_meet(r, mine) || docs_meet(r, mine2);
-      all = docs_same(r, mine);
-      all2 = docs_same(r, mine2);
-    }
-    const uint32_t m = __ballot_sync(0xffffffffu, on);
-    const uint32_t a = __ballot_sync(0xffffffffu, all), a2 = __ballot_sync(0xffffffffu, all2);
-    if (lane == 0) {
-      bits[w] = m;
-      whole[w] = a;
-      if (whole2) whole2[w] = a2;
-      if (m) atomicAdd(count, __popc(m));  // a whole-number sum: its order is free
-    }
+// What a document mask makes of tiles lo .. hi - 1, as bitmaps in shared memory:
+// those whose documents meet the CTA's tile, those of whose pairs with it every
+// one is valid, and those with padding. `two`: for two tiles at once, the second
+// one's bitmaps behind the first one's.
+struct TileBits {
+  uint32_t *meet, *whole, *pads, *meet2, *whole2;
+  __device__ __forceinline__ TileBits(uint32_t* at, int tiles) {
+    const int w = (tiles + 31) >> 5;
+    meet = at;
+    whole = at + w;
+    pads = at + 2 * w;
+    meet2 = at + 3 * w;
+    whole2 = at + 4 * w;
   }
-  __syncthreads();
-  return *count;
-}
+  // All threads of the CTA call it. counts: three shared words, zero before: tiles that meet either, `mine`, `mine2`.
+  template <bool TWO>
+  __device__ __forceinline__ void build(int* counts, const int4* ranges, int lo, int hi, int4 mine, int4 mine2) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    for (int w = warp; w * 32 < hi - lo; w += warps) {
+      const int t = lo + w * 32 + lane;
+      int4 r = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
+      if (t < hi) r = ranges[t];
+      const uint32_t m = __ballot_sync(0xffffffffu, docs_meet(r, mine));
+      const uint32_t a = __ballot_sync(0xffffffffu, docs_same(r, mine));
+      const uint32_t z = __ballot_sync(0xffffffffu, r.z != 0);
+      uint32_t m2 = 0, a2 = 0;
+      if (TWO) {
+        m2 = __ballot_sync(0xffffffffu, docs_meet(r, mine2));
+        a2 = __ballot_sync(0xffffffffu, docs_same(r, mine2));
+      }
+      if (lane == 0) {
+        meet[w] = m;
+        whole[w] = a;
+        pads[w] = z;
+        if (TWO) {
+          meet2[w] = m2;
+          whole2[w] = a2;
+        }
+        atomicAdd(&counts[0], __popc(m | m2));  // whole-number sums: their order is free
+        atomicAdd(&counts[1], __popc(m));
+        atomicAdd(&counts[2], __popc(m2));
+      }
+    }
+    __syncthreads();
+  }
+};
 __device__ __forceinline__ bool tile_bit(const uint32_t* bits, int i) { return (bits[i >> 5] >> (i & 31)) & 1u; }
 
 // s[c] <- cap log2(e) tanh(k s[c]), the capped score in log2 units, in place.
@@ -205,6 +223,18 @@ __device__ __forceinline__ float add_bias(float* s, float slope, float base) {
 #pragma unroll
   for (int c = 0; c < N; ++c) s[c] = fmaf(-slope, fabsf(base - static_cast<float>(c)), s[c]);
   return 0.f;
+}
+
+// CTA u of an ordered launch: chunk by chunk of heads (whose K and V fit L2
+// together), the B x jobs jobs in their order, the chunk's heads side by side.
+// Returns b Hkv + head and the job.
+__device__ __forceinline__ int ordered_job(const ExTile& p, const int* order, int jobs, int u, int* job) {
+  const int most = min(p.Hkv, max(1, p.chunk / p.B)), all = p.B * jobs;
+  const int ch = u / (most * all), in = u % (most * all);
+  const int heads = min(most, p.Hkv - ch * most);
+  const int at = order[in / heads];
+  *job = at % jobs;
+  return at / jobs * p.Hkv + ch * most + in % heads;
 }
 
 // Zeroes the rows of a swizzled tile (KB column blocks of 128 rows x 128 bytes)

@@ -51,7 +51,7 @@ struct DkvCfg {
   // kv_full, q_full[NS][2], g_full[NS][2], q_empty[NS][2], g_empty[NS][2], qg_ok[NS], s_full[2], dp_full[2],
   // p_full[2], ds_full[2], done
   static constexpr uint32_t NBAR = 1 + 9 * NS + 9;
-  static constexpr uint32_t OFF_BITS = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;
+  static constexpr uint32_t OFF_BITS = OFF_BAR + (NBAR * 8 + 32 + 15) / 16 * 16;
   static constexpr uint32_t SMEM = OFF_BITS + 1024;
 };
 
@@ -68,7 +68,7 @@ struct DqCfg {
   static constexpr uint32_t OFF_BAR = OFF_V + NV * TILE;
   // qg_full, k_full[NK], k_ok[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full, s_read, dp_full[2], ds_full[2], done
   static constexpr uint32_t NBAR = 1 + 3 * NK + 2 * NV + 2 + 2 + 2 + 1;
-  static constexpr uint32_t OFF_BITS = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;
+  static constexpr uint32_t OFF_BITS = OFF_BAR + (NBAR * 8 + 32 + 15) / 16 * 16;
   static constexpr uint32_t SMEM = OFF_BITS + 1024;
 };
 
@@ -205,9 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int BH = p.B * p.Hkv;
   int kt, bh;
   if (DOC && p.k_order) {  // the tiles with the most work first
-    const int at = p.k_order[blockIdx.x / p.Hkv];
-    bh = at / p.Tk * p.Hkv + blockIdx.x % p.Hkv;
-    kt = at % p.Tk;
+    bh = ordered_job(p, p.k_order, p.Tk, blockIdx.x, &kt);
   } else if (p.causal) {
     const int per_chunk = p.chunk * p.Tk;
     const int ch = blockIdx.x / per_chunk, in = blockIdx.x % per_chunk;
@@ -248,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(done, 1);
     *abort_flag = 0;
-    *count = 0;
+    count[0] = count[1] = count[2] = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -268,11 +266,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int n = p.Tq - lo;
-  const uint32_t* whole = bits + ((p.Tq + 31) >> 5);
-  if (DOC)
-    n = build_tile_bits(bits, bits + ((p.Tq + 31) >> 5), nullptr, count, p.q_ranges + static_cast<size_t>(b) * p.Tq, lo,
-                        p.Tq, mine, none);
-  const TileIter first{DOC ? bits : nullptr, lo, lo};
+  TileBits tiles(bits, p.Tq);
+  if (DOC) {
+    tiles.build<false>(count, p.q_ranges + static_cast<size_t>(b) * p.Tq, lo, p.Tq, mine, none);
+    n = count[0];
+  }
+  const TileIter first{DOC ? tiles.meet : nullptr, nullptr, lo, lo};
   const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
 
   if (warp < 4) {
@@ -301,23 +300,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                          (!start || kk > 0) ? 1u : 0u);
         };
         auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
-        // Q or d_o of list entry j, half h
-        auto ready = [&](uint64_t* full, int j, int h) {
+        // Q or d_o of list entry j, half h; `pad`: once the padded rows are clear
+        auto ready = [&](uint64_t* full, int j, int h, bool pad) {
           const int s = j % C::NS;
-          const bool there = wait(DOC ? &qg_ok[s] : &full[halves ? 2 * s + h : 2 * s], j / C::NS);
+          const bool there = wait(&full[halves ? 2 * s + h : 2 * s], j / C::NS) && (!pad || wait(&qg_ok[s], j / C::NS));
           tc_fence_after();
           return there;
         };
+        TileIter it = first;
+        bool pad = DOC && tile_bit(tiles.pads, it.next() - lo);
         bool ok = wait(kv_full, 0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!ok || !(ok = ready(q_full, 0, h))) break;
+          if (!ok || !(ok = ready(q_full, 0, h, pad))) break;
           scores(tmem + h * 64, dK, sdesc_advance(dQ, h * 8192), &s_full[h]);
-          if (!(ok = ready(g_full, 0, h))) break;
+          if (!(ok = ready(g_full, 0, h, pad))) break;
           scores(tmem + 128 + h * 64, dV, sdesc_advance(dG, h * 8192), &dp_full[h]);
         }
         for (int i = 0; ok && i < n; ++i) {
           const uint32_t at = (i % C::NS) * C::TILE, nx = ((i + 1) % C::NS) * C::TILE;
+          if (DOC && i + 1 < n) pad = tile_bit(tiles.pads, it.next() - lo);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (!(ok = wait(&p_full[h], i))) break;
@@ -325,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             accumulate(tmem + 256, tmem + h * 64, sdesc_advance(dGm, at + h * 8192), i == 0 && h == 0);
             umma_commit(&g_empty[2 * (i % C::NS) + h]);
             if (i + 1 < n) {
-              if (!(ok = ready(q_full, i + 1, h))) break;
+              if (!(ok = ready(q_full, i + 1, h, pad))) break;
               scores(tmem + h * 64, dK, sdesc_advance(dQ, nx + h * 8192), &s_full[h]);
             }
             if (!(ok = wait(&ds_full[h], i))) break;
@@ -333,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             accumulate(tmem + 384, tmem + 128 + h * 64, sdesc_advance(dQm, at + h * 8192), i == 0 && h == 0);
             umma_commit(&q_empty[2 * (i % C::NS) + h]);
             if (i + 1 < n) {
-              if (!(ok = ready(g_full, i + 1, h))) break;
+              if (!(ok = ready(g_full, i + 1, h, pad))) break;
               scores(tmem + 128 + h * 64, dV, sdesc_advance(dG, nx + h * 8192), &dp_full[h]);
             } else if (h == 1) {
               umma_commit(done);
@@ -405,8 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           there = mbar_wait_warp(&q_full[2 * s + h], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER) &&
                   mbar_wait_warp(&g_full[2 * s + h], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER);
         if (!there) break;
-        const size_t at = static_cast<size_t>(b) * p.Tq + it.next();
-        if (p.q_ranges[at].z) {
+        const int qt = it.next();
+        if (tile_bit(tiles.pads, qt - lo)) {
+          const size_t at = static_cast<size_t>(b) * p.Tq + qt;
           zero_padded_rows<C::KB>(sQ + s * C::TILE, p.q_ids + at * 128);
           zero_padded_rows<C::KB>(sG + s * C::TILE, p.q_ids + at * 128);
           fence_proxy_async_smem();
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = i % C::NS;
       const int qt = it.next();
       // where the tile's documents differ: the id of row `lane` of this quarter, under way while S is
-      const bool mixed = DOC && !tile_bit(whole, qt - lo);
+      const bool mixed = DOC && !tile_bit(tiles.whole, qt - lo);
       int id = 0;
       if (mixed) id = __ldg(p.q_ids + (static_cast<size_t>(b) * p.Tq + qt) * 128 + quarter * 32 + lane);
       const float4* nl4 = reinterpret_cast<const float4*>(smem + C::OFF_STAT + s * 1024) + quarter * 8;
@@ -619,9 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int BH = p.B * p.Hkv;
   int qt, bh;
   if (DOC && p.order) {
-    const int at = p.order[blockIdx.x / p.Hkv];
-    bh = at / p.Tq * p.Hkv + blockIdx.x % p.Hkv;
-    qt = at % p.Tq;
+    bh = ordered_job(p, p.order, p.Tq, blockIdx.x, &qt);
   } else if (p.causal) {  // the last query tiles see the most keys and go first
     const int per_chunk = p.chunk * p.Tq;
     const int ch = blockIdx.x / per_chunk, in = blockIdx.x % per_chunk;
@@ -660,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(done, 1);
     *abort_flag = 0;
-    *count = 0;
+    count[0] = count[1] = count[2] = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -676,11 +677,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int n = hi;
-  const uint32_t* whole = bits + ((p.Tk + 31) >> 5);
-  if (DOC)
-    n = build_tile_bits(bits, bits + ((p.Tk + 31) >> 5), nullptr, count, p.k_ranges + static_cast<size_t>(b) * p.Tk, 0,
-                        hi, mine, none);
-  const TileIter first{DOC ? bits : nullptr, 0, 0};
+  TileBits tiles(bits, p.Tk);
+  if (DOC) {
+    tiles.build<false>(count, p.k_ranges + static_cast<size_t>(b) * p.Tk, 0, hi, mine, none);
+    n = count[0];
+  }
+  const TileIter first{DOC ? tiles.meet : nullptr, nullptr, 0, 0};
   const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
   // TMEM: S | dP 0 | dQ | dP 1
   auto dp_buf = [&](int i) { return tmem + ((i & 1) ? 384u : 128u); };
@@ -704,11 +706,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(bar);
         };
         auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
-        uint64_t* ready = DOC ? k_ok : k_full;
+        TileIter it = first;
         // S(j) and dP(j): S is free once the softmax has read S(j - 1), dP's buffer once dQ(j - 2) was issued
         auto both = [&](int j) {
           if (j > 0 && !wait(s_read, j - 1)) return false;
-          if (!wait(&ready[j % C::NK], j / C::NK)) return false;
+          if (!wait(&k_full[j % C::NK], j / C::NK)) return false;
+          if (DOC && tile_bit(tiles.pads, it.next()) && !wait(&k_ok[j % C::NK], j / C::NK)) return false;
           tc_fence_after();
           scores(tmem, dQ, sdesc_advance(dK, (j % C::NK) * C::TILE), s_full);
           if (!wait(&v_full[j % C::NV], j / C::NV)) return false;
@@ -770,8 +773,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < n; ++j) {
         const int s = j % C::NK;
         if (!mbar_wait_warp(&k_full[s], (j / C::NK) & 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
-        const size_t at = static_cast<size_t>(b) * p.Tk + it.next();
-        if (p.k_ranges[at].z) {
+        const int kt = it.next();
+        if (tile_bit(tiles.pads, kt)) {
+          const size_t at = static_cast<size_t>(b) * p.Tk + kt;
           zero_padded_rows<C::KB>(sK + s * C::TILE, p.k_ids + at * 128);
           fence_proxy_async_smem();
         }
@@ -808,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < n; ++i) {
       const int kt = it.next();
       // where the tile's documents differ: the id of key `lane` of this quarter, under way while S is
-      const bool mixed = DOC && !tile_bit(whole, kt);
+      const bool mixed = DOC && !tile_bit(tiles.whole, kt);
       int id = 0;
       if (mixed) id = __ldg(p.k_ids + (static_cast<size_t>(b) * p.Tk + kt) * 128 + quarter * 32 + lane);
       const bool partial = mixed || (kt + 1) * 128 > lim_all;
@@ -902,10 +906,10 @@ template <int D, bool CAP, bool BIAS, bool DOC>
 cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk, const CUtensorMap* tv,
                        const ExTile& p, cudaStream_t s) {
   static KernelReady ready_kv, ready_q;
-  cudaError_t e = make_ready(ready_kv, ex_dkv_kernel<D, CAP, BIAS, DOC>, DkvCfg<D>::SMEM + 16384, kLaunchRegs);  // 2^16 query tiles
+  cudaError_t e = make_ready(ready_kv, ex_dkv_kernel<D, CAP, BIAS, DOC>, DkvCfg<D>::SMEM + 24576, kLaunchRegs);  // 2^16 query tiles
   if (e != cudaSuccess) return e;
-  if ((e = make_ready(ready_q, ex_dq_kernel<D, CAP, BIAS, DOC>, DqCfg<D>::SMEM + 1024, kLaunchRegs)) != cudaSuccess) return e;  // 2^12 key tiles
-  const unsigned bits_q = DOC ? (p.Tq + 31) / 32 * 8u : 0u, bits_k = DOC ? (p.Tk + 31) / 32 * 8u : 0u;
+  if ((e = make_ready(ready_q, ex_dq_kernel<D, CAP, BIAS, DOC>, DqCfg<D>::SMEM + 1536, kLaunchRegs)) != cudaSuccess) return e;  // 2^12 key tiles
+  const unsigned bits_q = DOC ? (p.Tq + 31) / 32 * 12u : 0u, bits_k = DOC ? (p.Tk + 31) / 32 * 12u : 0u;
   ex_dkv_kernel<D, CAP, BIAS, DOC><<<p.B * p.Hkv * p.Tk, kThreads, DkvCfg<D>::SMEM + bits_q, s>>>(*tq, *tg, *tk, *tv, p);
   ex_dq_kernel<D, CAP, BIAS, DOC><<<p.B * p.Hkv * p.Tq, kThreads, DqCfg<D>::SMEM + bits_k, s>>>(*tq, *tg, *tk, *tv, p);
   note_launches(2);

@@ -51,9 +51,9 @@ struct FwdCfg {
   static constexpr uint32_t OFF_BAR = OFF_V + NS * TILE;
   // q_full, k_full[NS], v_full[NS], v_ok[NS], k_empty[NS], v_empty[NS], s_full[2], p_full[2], p_empty[2], drain
   static constexpr uint32_t NBAR = 1 + 5 * NS + 2 + 2 + 2 + 1;
-  static constexpr uint32_t OFF_MAX = OFF_BAR + (NBAR * 8 + 16 + 15) / 16 * 16;  // [parity][slot][half][row]
+  static constexpr uint32_t OFF_MAX = OFF_BAR + (NBAR * 8 + 32 + 15) / 16 * 16;  // [parity][slot][half][row]
   static constexpr uint32_t OFF_BITS = OFF_MAX + 2 * 2 * 2 * 128 * 8;
-  static constexpr uint32_t SMEM = OFF_BITS + 1024;  // and three bits for each key tile under a document mask
+  static constexpr uint32_t SMEM = OFF_BITS + 1024;  // and five bits for each key tile under a document mask
 };
 
 }  // namespace
@@ -98,9 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int job, bh;
   const int BH = p.B * p.Hkv;
   if (DOC && p.order) {  // the jobs with the most key tiles first
-    const int at = p.order[u / p.Hkv];
-    bh = at / groups * p.Hkv + u % p.Hkv;
-    job = at % groups;
+    bh = ordered_job(p, p.order, groups, u, &job);
   } else if (p.causal) {
     const int per_chunk = p.chunk * groups;
     const int ch = u / per_chunk, in = u % per_chunk;
@@ -119,7 +117,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto limit = [&](int pos) { return p.causal ? min(p.Nk, max(max(pos + 1, prefix), 0)) : p.Nk; };
   auto last_tok = [&](int qt) { return min(p.Nq, (qt + 1) * p.tpt) - 1; };
   const int off = p.Nk - p.Nq;  // position of token 0
-  const int T = (limit(off + last_tok(has1 ? qt0 + 1 : qt0)) + 127) >> 7;
+  const int T0 = (limit(off + last_tok(qt0)) + 127) >> 7;
+  const int T = has1 ? (limit(off + last_tok(qt0 + 1)) + 127) >> 7 : T0;
   const int lo = static_cast<int>(static_cast<long long>(split) * T / p.nsplit);
   const int hi = static_cast<int>(static_cast<long long>(split + 1) * T / p.nsplit);
   const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
@@ -145,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
-    *count = 0;
+    count[0] = count[1] = count[2] = 0;
     fence_mbar_init();
   }
   if (warp == 0) {
@@ -165,15 +164,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int n = hi - lo;  // key tiles of this CTA
-  const int bit_words = (p.Tk + 31) >> 5;
-  if (DOC)
-    n = build_tile_bits(bits, bits + bit_words, bits + 2 * bit_words, count,
-                        p.k_ranges + static_cast<size_t>(b) * p.Tk, lo, hi, r0, r1);
-  const TileIter first{DOC ? bits : nullptr, lo, lo};
-  // key tiles of the slots, in the order of the CTA's list
-  const int n0 = single ? (n + 1) >> 1 : n;
-  const int n1 = single ? n >> 1 : (has1 ? n : 0);
+  // key tiles of this CTA and of its slots; the CTA's list holds what either slot needs
+  TileBits tiles(bits, p.Tk);
+  int n = hi - lo, n0 = min(hi, T0) - lo, n1 = has1 ? n : 0;
+  if (DOC) {
+    tiles.build<true>(count, p.k_ranges + static_cast<size_t>(b) * p.Tk, lo, hi, r0, r1);
+    n = count[0];
+    n0 = count[1];
+    n1 = count[2];
+  }
+  if (n0 < 0) n0 = 0;
+  if (single) n1 = n >> 1, n0 = n - n1;
+  const TileIter first{DOC ? tiles.meet : nullptr, DOC ? tiles.meet2 : nullptr, lo, lo};
   const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
 
   if (warp < 4) {
@@ -186,7 +188,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dQ = sdesc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t dK = sdesc_sw128(smem_u32(sK), 16, 1024);
         const uint64_t dV = sdesc_sw128(smem_u32(sV), 16384, 1024);
-        uint64_t* v_bar = DOC ? v_ok : v_full;
         // S_t = Q_t K^T with the CTA's list entry j
         auto issue_s = [&](int t, int j) {
           const uint64_t dQt = sdesc_advance(dQ, single ? 0 : t * C::TILE);
@@ -208,37 +209,71 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(&p_empty[t]);
         };
         auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
+        // V of list entry j; `pad`: once its padded rows are clear
+        auto v_there = [&](int j, bool pad) {
+          const int s = j % C::NS;
+          return wait(&v_full[s], j / C::NS) && (!pad || wait(&v_ok[s], j / C::NS));
+        };
+        TileIter it = first;
+        const int steps = single ? (n + 1) >> 1 : n;
+        int i0 = 0, i1 = 0;     // the slots' steps
+        int behind = -1;        // slot 1's list entry whose O += P V is to come
+        bool behind_pad = false;
         bool ok = wait(q_full, 0);
+        // step's slots (1, 2) and whether their V tiles hold padding (4, 8)
+        auto look = [&](int step) {
+          const int j0 = single ? 2 * step : step, j1 = single ? j0 + 1 : j0;
+          int f = 0;
+          if (DOC) {
+            if (j0 >= n) return 0;
+            int kt = it.next() - lo;
+            if (tile_bit(tiles.pads, kt)) f |= single ? 4 : 12;
+            if (single) {
+              f |= 1;
+              if (j1 < n) f |= tile_bit(tiles.pads, it.next() - lo) ? 10 : 2;
+            } else {
+              f |= (tile_bit(tiles.meet, kt) ? 1 : 0) | (tile_bit(tiles.meet2, kt) ? 2 : 0);
+            }
+          } else {
+            f = (j0 < (single ? n : n0) ? 1 : 0) | (j1 < (single || has1 ? n : 0) ? 2 : 0);
+          }
+          return f;
+        };
+        int flags = look(0);
         // UMMAs run in order, so S_t(i + 1) overwrites P_t(i) only after the product that reads it
-        for (int i = 0; ok && i <= n0; ++i) {
-          const int j0 = single ? 2 * i : i;            // list entry of slot 0's step i
-          const int jp = single ? 2 * i - 1 : i - 1;    // of slot 1's step i - 1
-          const int j1 = single ? 2 * i + 1 : i;        // of slot 1's step i
-          if (i < n0) {
-            if (!wait(&k_full[j0 % C::NS], j0 / C::NS)) break;
+        for (int step = 0; ok && step <= steps; ++step) {
+          const int j0 = single ? 2 * step : step, j1 = single ? j0 + 1 : j0;
+          const int now = flags;
+          const bool a0 = now & 1, a1 = now & 2, pad0 = now & 4, pad1 = now & 8;
+          if (a0) {
+            if (!(ok = wait(&k_full[j0 % C::NS], j0 / C::NS))) break;
             tc_fence_after();
             issue_s(0, j0);
-            if (!has1) umma_commit(&k_empty[j0 % C::NS]);
+            if (single || !a1) umma_commit(&k_empty[j0 % C::NS]);
           }
-          if (i >= 1 && i - 1 < n1) {
-            if (single && !wait(&v_bar[jp % C::NS], jp / C::NS)) break;
-            if (!wait(&p_full[1], i - 1)) break;
+          if (behind >= 0) {
+            if (!(ok = v_there(behind, behind_pad) && wait(&p_full[1], i1 - 1))) break;
             tc_fence_after();
-            issue_o(1, i - 1, jp);
-            umma_commit(&v_empty[jp % C::NS]);
+            issue_o(1, i1 - 1, behind);
+            umma_commit(&v_empty[behind % C::NS]);
+            behind = -1;
           }
-          if (i < n1) {
-            if (single && !wait(&k_full[j1 % C::NS], j1 / C::NS)) break;
+          if (a1) {
+            if (!(ok = wait(&k_full[j1 % C::NS], j1 / C::NS))) break;
             tc_fence_after();
             issue_s(1, j1);
             umma_commit(&k_empty[j1 % C::NS]);
+            behind = j1;
+            behind_pad = pad1;
+            ++i1;
           }
-          if (i < n0) {
-            if (!wait(&v_bar[j0 % C::NS], j0 / C::NS)) break;
-            if (!wait(&p_full[0], i)) break;
+          flags = look(step + 1);  // beside the softmax that the next product waits for
+          if (a0) {
+            if (!(ok = v_there(j0, pad0) && wait(&p_full[0], i0))) break;
             tc_fence_after();
-            issue_o(0, i, j0);
-            if (!has1) umma_commit(&v_empty[j0 % C::NS]);
+            issue_o(0, i0, j0);
+            if (single || !a1) umma_commit(&v_empty[j0 % C::NS]);
+            ++i0;
           }
         }
       }
@@ -280,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = j % C::NS;
         if (!mbar_wait_warp(&v_full[s], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
         const int kt = it.next();
-        if (p.k_ranges[static_cast<size_t>(b) * p.Tk + kt].z) {
+        if (tile_bit(tiles.pads, kt - lo)) {
           zero_padded_rows<C::KB>(sV + s * C::TILE, p.k_ids + (static_cast<size_t>(b) * p.Tk + kt) * 128);
           fence_proxy_async_smem();
         }
@@ -309,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pos = p.lens ? p.P + min(max(row_valid ? p.lens[tok] : 0, 0), p.C) - 1 : off + tok;
     const int lim = limit(pos) - half * 64;
     const int lim_all = limit(off + qt * p.tpt);  // keys that every row of the tile sees
-    const uint32_t* whole = bits + (t == 0 || single ? 1 : 2) * bit_words;
+    const uint32_t* whole = t == 0 || single ? tiles.whole : tiles.whole2;
     int my_doc = DOC && row_valid ? p.doc_q[static_cast<size_t>(b) * p.Nq + tok] : -2;
     if (my_doc < 0) my_doc = -2;  // a padded query matches no key
     const float mul = p.mul;  // what turns a score into log2 units
@@ -319,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float2* other_max = row_max + (t * 2 + (half ^ 1)) * 128 + row;
     const int pair_bar = 2 + t * 4 + wq;  // the two warps that share these rows
     TileIter it = first;
+    if (DOC && !single) it = TileIter{t == 0 ? tiles.meet : tiles.meet2, nullptr, lo, lo};
     if (single && t == 1 && nt > 0) it.next();
     float m = -CUDART_INF_F;  // running max, log2 units (the same in both halves)
     float l = 0.f;            // this half's sum
@@ -640,10 +676,14 @@ __global__ void __launch_bounds__(1024) ex_doc_order(const ExTile p, int per, in
   }
   if (threadIdx.x == 1023) bins[4096] = before;
   __syncthreads();
-  // equal jobs land in any order: it decides when they run, not what they compute
-  for (int at = warp; at < all; at += 32) {
-    const int n = bin(at);
-    if (lane == 0) order[atomicAdd(&bins[n], 1)] = at;
+  // Equal jobs land about in order (neighbours share their tiles in L2); the order decides when they run, not what
+  // they compute.
+  for (int at = warp; at - warp < all; at += 32) {
+    if (at < all) {
+      const int n = bin(at);
+      if (lane == 0) order[atomicAdd(&bins[n], 1)] = at;
+    }
+    __syncthreads();
   }
 }
 
@@ -651,10 +691,10 @@ template <int D, bool CAP, bool BIAS, bool DOC>
 cudaError_t launch_fwd(const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv, const ExTile& p,
                        cudaStream_t s) {
   auto kern = ex_fwd_kernel<D, CAP, BIAS, DOC>;
-  const unsigned bits = DOC ? (p.Tk + 31) / 32 * 12u : 0u;
+  const unsigned bits = DOC ? (p.Tk + 31) / 32 * 20u : 0u;
   const unsigned smem = FwdCfg<D>::SMEM + bits;
   static KernelReady ready;
-  const cudaError_t e = make_ready(ready, kern, FwdCfg<D>::SMEM + 1536, kLaunchRegs);  // 2^12 tiles
+  const cudaError_t e = make_ready(ready, kern, FwdCfg<D>::SMEM + 2560, kLaunchRegs);  // 2^12 tiles
   if (e != cudaSuccess) return e;
   const int per = p.single ? 1 : 2;
   const long long grid = static_cast<long long>(p.B) * p.Hkv * ((p.Tq + per - 1) / per) * p.nsplit;
