@@ -3,12 +3,12 @@
 //   dP = d_o V^T,  dS = P (dP - D) (1 - t^2),
 //   dV = P^T d_o,  dK = scale dS^T Q,  dQ = scale dS K.
 //
-// Two kernels instead of one: dK and dV are sums over queries, dQ over keys,
-// so a single sweep would have to add one of them into global memory from many
+// Two kinds of CTAs in one launch: dK and dV are sums over queries, dQ over
+// keys, so a single sweep would have to add one of them into global memory from many
 // CTAs, in an order that changes from run to run. Here every sum is one CTA's,
 // in a fixed order, at the price of seven products per tile instead of five.
 //
-//   ex_dkv_kernel: a CTA owns 128 keys of a KV head, K and V resident, and
+//   dkv_tile: a CTA owns 128 keys of a KV head, K and V resident, and
 //     streams packed query tiles (so the heads that share the KV head are
 //     summed in the accumulators). Scores are computed transposed, keys on
 //     TMEM lanes: S^T = K Q^T, dP^T = V d_o^T. P^T and dS^T (bf16) overwrite
@@ -19,11 +19,13 @@
 //     the other half's products. With whole tiles in one chain the tensor pipe
 //     waited 1500 of every 3500 cycles; halves cost the N = 64 products 48
 //     cycles for 32 cycles of work.
-//   ex_dq_kernel: a CTA owns one packed query tile and streams key tiles:
+//   dq_tile: a CTA owns one packed query tile and streams key tiles:
 //     S = Q K^T, dP = d_o V^T, dS over dP, dQ += dS K. S(i+1) and dP(i+1) are
 //     computed while the softmax works on tile i (dP has two buffers).
 //
 // Four threads work on a row of a tile, 32 of its columns each.
+#include <algorithm>
+
 #include "attn_ex.cuh"
 
 namespace mcs {
@@ -31,9 +33,6 @@ namespace mcs {
 namespace {
 
 constexpr int kThreads = kExThreads;
-constexpr int kLaunchRegs = kExLaunchRegs;
-constexpr int kLowRegs = kExLowRegs;
-constexpr int kSoftRegs = kExSoftRegs;
 constexpr int kSoftThreads = 512;
 
 template <int D>
@@ -171,9 +170,8 @@ __global__ void __launch_bounds__(256) ex_row_stats(const ExTile p, const uint16
 }  // namespace
 
 template <int D, bool CAP, bool BIAS, bool DOC>
-__global__ void __launch_bounds__(kThreads, 1)
-    ex_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
-                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
+__device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_g, const CUtensorMap& tm_k,
+                                         const CUtensorMap& tm_v, const ExTile& p, int cta) {
   using C = DkvCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -205,16 +203,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int BH = p.B * p.Hkv;
   int kt, bh;
   if (DOC && p.k_order) {  // the tiles with the most work first
-    bh = ordered_job(p, p.k_order, p.Tk, blockIdx.x, &kt);
+    bh = ordered_job(p, p.k_order, p.Tk, cta, &kt);
   } else if (p.causal) {
     const int per_chunk = p.chunk * p.Tk;
-    const int ch = blockIdx.x / per_chunk, in = blockIdx.x % per_chunk;
+    const int ch = cta / per_chunk, in = cta % per_chunk;
     const int heads = min(p.chunk, BH - ch * p.chunk);
     bh = ch * p.chunk + in % heads;
     kt = in / heads;
   } else {
-    kt = blockIdx.x % p.Tk;
-    bh = blockIdx.x / p.Tk;
+    kt = cta % p.Tk;
+    bh = cta / p.Tk;
   }
   const int b = bh / p.Hkv, hk = bh % p.Hkv;
   const int off = p.Nk - p.Nq;
@@ -591,9 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int D, bool CAP, bool BIAS, bool DOC>
-__global__ void __launch_bounds__(kThreads, 1)
-    ex_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
-                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
+__device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_g, const CUtensorMap& tm_k,
+                                        const CUtensorMap& tm_v, const ExTile& p, int cta) {
   using C = DqCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -622,16 +619,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int BH = p.B * p.Hkv;
   int qt, bh;
   if (DOC && p.order) {
-    bh = ordered_job(p, p.order, p.Tq, blockIdx.x, &qt);
+    bh = ordered_job(p, p.order, p.Tq, cta, &qt);
   } else if (p.causal) {  // the last query tiles see the most keys and go first
     const int per_chunk = p.chunk * p.Tq;
-    const int ch = blockIdx.x / per_chunk, in = blockIdx.x % per_chunk;
+    const int ch = cta / per_chunk, in = cta % per_chunk;
     const int heads = min(p.chunk, BH - ch * p.chunk);
     bh = ch * p.chunk + in % heads;
     qt = p.Tq - 1 - in / heads;
   } else {
-    qt = blockIdx.x % p.Tq;
-    bh = blockIdx.x / p.Tq;
+    qt = cta % p.Tq;
+    bh = cta / p.Tq;
   }
   const int b = bh / p.Hkv, hk = bh % p.Hkv;
   const int off = p.Nk - p.Nq;
@@ -688,7 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto dp_buf = [&](int i) { return tmem + ((i & 1) ? 384u : 128u); };
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
     if (warp == 0) {
       // ---------------------------------------------------------------- UMMA issuer
       if (n > 0 && elect_one()) {
@@ -784,11 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-    named_barrier_sync<1, kThreads>();
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
   } else {
     // ---------------------------------------------------------------- dS, then the epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int quarter = (warp - 4) >> 2;  // keys 32 quarter .. 32 quarter + 31 of each tile
     const int wq = warp & 3;
     const int row = wq * 32 + lane;
@@ -894,10 +887,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       store_row<D / 4>(tmem + lane_addr + 256 + c0, n > 0, row_valid, p.scale, dst);
     }
     __syncwarp();
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLaunchRegs));
-    named_barrier_sync<1, kThreads>();
   }
   teardown(abort_flag, done, qg_full, n > 0 ? 1 + C::NK + C::NV : 0, tmem);
+}
+
+template <int D, bool CAP, bool BIAS, bool DOC>
+__global__ void __launch_bounds__(kThreads, 1)
+    ex_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
+                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
+  const int keys = p.B * p.Hkv * p.Tk;
+  if (static_cast<int>(blockIdx.x) < keys) dkv_tile<D, CAP, BIAS, DOC>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x);
+  else dq_tile<D, CAP, BIAS, DOC>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x - keys);
 }
 
 namespace {
@@ -905,14 +905,15 @@ namespace {
 template <int D, bool CAP, bool BIAS, bool DOC>
 cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk, const CUtensorMap* tv,
                        const ExTile& p, cudaStream_t s) {
-  static KernelReady ready_kv, ready_q;
-  cudaError_t e = make_ready(ready_kv, ex_dkv_kernel<D, CAP, BIAS, DOC>, DkvCfg<D>::SMEM + 24576, kLaunchRegs);  // 2^16 query tiles
+  static KernelReady ready;
+  auto kern = ex_bwd_kernel<D, CAP, BIAS, DOC>;
+  constexpr unsigned most_kv = DkvCfg<D>::SMEM + 24576, most_q = DqCfg<D>::SMEM + 1536;  // 2^16 and 2^12 tiles
+  const cudaError_t e = make_ready(ready, kern, std::max(most_kv, most_q), 0);
   if (e != cudaSuccess) return e;
-  if ((e = make_ready(ready_q, ex_dq_kernel<D, CAP, BIAS, DOC>, DqCfg<D>::SMEM + 1536, kLaunchRegs)) != cudaSuccess) return e;  // 2^12 key tiles
-  const unsigned bits_q = DOC ? (p.Tq + 31) / 32 * 12u : 0u, bits_k = DOC ? (p.Tk + 31) / 32 * 12u : 0u;
-  ex_dkv_kernel<D, CAP, BIAS, DOC><<<p.B * p.Hkv * p.Tk, kThreads, DkvCfg<D>::SMEM + bits_q, s>>>(*tq, *tg, *tk, *tv, p);
-  ex_dq_kernel<D, CAP, BIAS, DOC><<<p.B * p.Hkv * p.Tq, kThreads, DqCfg<D>::SMEM + bits_k, s>>>(*tq, *tg, *tk, *tv, p);
-  note_launches(2);
+  const unsigned smem = std::max(DkvCfg<D>::SMEM + (DOC ? (p.Tq + 31) / 32 * 12u : 0u),
+                                 DqCfg<D>::SMEM + (DOC ? (p.Tk + 31) / 32 * 12u : 0u));
+  kern<<<p.B * p.Hkv * (p.Tk + p.Tq), kThreads, smem, s>>>(*tq, *tg, *tk, *tv, p);
+  note_launches(1);
   return cudaGetLastError();
 }
 
