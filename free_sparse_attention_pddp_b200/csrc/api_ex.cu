@@ -98,19 +98,21 @@ struct FwdPlan {
 
 constexpr int kSms = 148;
 
-// One query tile and at least four key tiles: both slots of a CTA take that
-// tile. While a wave has room, the keys are split into parts of at least four
-// tiles per slot, joined by a second launch.
+// Few query tiles and an odd number of them (a pair would leave a slot without
+// work), at least four key tiles: both slots of a CTA take one query tile and
+// half of its keys. While a wave has room, the keys are split further, to one
+// tile per slot; a second launch joins the parts (about 4 us, two key tiles'
+// time).
 FwdPlan fwd_plan(int B, int Hkv, int g, int Nq, int Nk, int d) {
   FwdPlan f;
   f.tpt = 128 / g;
   f.Tq = (Nq + f.tpt - 1) / f.tpt;
   f.Tk = (Nk + 127) / 128;
-  f.single = f.Tq == 1 && f.Tk >= 4;
-  const long long ctas = static_cast<long long>(B) * Hkv * (f.single ? 1 : (f.Tq + 1) / 2);
+  f.single = f.Tq <= 5 && f.Tq % 2 == 1 && f.Tk >= 4;
+  const long long ctas = static_cast<long long>(B) * Hkv * (f.single ? f.Tq : (f.Tq + 1) / 2);
   f.nsplit = 1;
-  if (2 * ctas <= kSms) {
-    const long long most = f.Tk / (f.single ? 8 : 4);
+  if (2 * ctas <= kSms && f.Tk >= 4) {
+    const long long most = f.Tk / (f.single ? 2 : 1);
     f.nsplit = static_cast<int>(std::max(1ll, std::min(kSms / ctas, most)));
   }
   f.parts = f.nsplit * (f.single ? 2 : 1);
@@ -202,7 +204,7 @@ mcs_status check_decode(const mcs_decode_shape* s) {
 
 // How single tokens fill the GPU. Two CTAs to an SM; the keys are cut so that
 // about eight waves of them cover the batch (lengths differ, and a late long
-// request should not run alone), in chunks of at least 256 keys, less only
+// request should not run alone), in chunks of at least 512 keys, less only
 // where the batch would not fill one wave.
 struct DecodePlan {
   int gsplit, chunk, nsplit;
@@ -218,7 +220,7 @@ DecodePlan decode_plan(const mcs_decode_shape* s) {
     const long long per_job = std::max(1ll, ctas / jobs);
     return ((s->C + per_job - 1) / per_job + 63) / 64 * 64;
   };
-  f.chunk = static_cast<int>(std::max(64ll, std::max(cut(8 * slots), std::min(256ll, cut(slots)))));
+  f.chunk = static_cast<int>(std::max(64ll, std::max(cut(8 * slots), std::min(512ll, cut(slots)))));
   f.nsplit = (s->C + f.chunk - 1) / f.chunk;
   if (s->P > 0) f.pre = fwd_plan(1, s->Hkv, g, s->B, s->P, s->d);
   return f;

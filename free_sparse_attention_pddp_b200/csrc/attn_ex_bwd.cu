@@ -131,39 +131,44 @@ __device__ __forceinline__ void teardown(volatile int* abort_flag, uint64_t* don
   }
 }
 
-// Per packed row: -lse in log2 units (less slope times the row's token in the tile, which the dK/dV kernel's bias
-// counts on) and D = d_o . o, as [B Hkv, Tq][2][128]; an empty row, like a row whose lse is
-// -inf, gets (-inf, 0), which makes its P zero. One warp per row.
+// Per packed row: -lse in log2 units (less slope times the row's token in the tile, which the dK/dV tiles' bias counts
+// on) and D = d_o . o, as [B Hkv, Tq][2][128]; an empty row, like a row whose lse is -inf, gets (-inf, 0), which makes
+// its P zero. One CTA per tile, 16 bytes of a row per lane: reading o and d_o once from HBM is the bound.
 template <int D>
 __global__ void __launch_bounds__(256) ex_row_stats(const ExTile p, const uint16_t* o, const uint16_t* d_o,
                                                     const float* lse, float* stats) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long r = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (r >= static_cast<long long>(p.B) * p.Hkv * p.Tq * 128) return;
-  const int row = r & 127, qt = (r >> 7) % p.Tq, bh = (r >> 7) / p.Tq;
-  const int tok = qt * p.tpt + row / p.g, head = bh % p.Hkv * p.g + row % p.g, b = bh / p.Hkv;
-  float nl = -CUDART_INF_F, s = 0.f;
-  if (row < p.tpt * p.g && tok < p.Nq) {
-    const float L = lse[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok];
-    const size_t at = ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D + lane * E;
-    if (L > -CUDART_INF_F) {
-      nl = -L * kLog2e;
-      if (p.slopes) nl = fmaf(-p.slopes[head] * kLog2e, static_cast<float>(row / p.g), nl);
+  constexpr int LANES = D / 8;             // of a row
+  constexpr int PASS = 256 / LANES;        // rows at a time
+  const int qt = blockIdx.x % p.Tq, bh = blockIdx.x / p.Tq;
+  const int b = bh / p.Hkv, hk = bh % p.Hkv;
+  const int c = threadIdx.x % LANES;
+  float* out = stats + static_cast<size_t>(blockIdx.x) * 256;
+#pragma unroll 4
+  for (int r0 = 0; r0 < 128; r0 += PASS) {
+    const int row = r0 + threadIdx.x / LANES;
+    const int t = row / p.g, tok = qt * p.tpt + t, head = hk * p.g + row - t * p.g;
+    float nl = -CUDART_INF_F, s = 0.f;
+    if (t < p.tpt && tok < p.Nq) {
+      const float L = lse[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok];
+      const size_t at = ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D + c * 8;
+      const uint4 x = *reinterpret_cast<const uint4*>(o + at), y = *reinterpret_cast<const uint4*>(d_o + at);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+      if (L > -CUDART_INF_F) {
+        nl = -L * kLog2e;
+        if (p.slopes) nl = fmaf(-p.slopes[head] * kLog2e, static_cast<float>(t), nl);
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(o + at + e);
-        const uint32_t y = *reinterpret_cast<const uint32_t*>(d_o + at + e);
-        s = fmaf(__uint_as_float(x << 16), __uint_as_float(y << 16), s);
-        s = fmaf(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u), s);
+        for (int e = 0; e < 4; ++e) {
+          s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+          s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+        }
       }
     }
-  }
 #pragma unroll
-  for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-  if (lane == 0) {
-    stats[(r >> 7) * 256 + row] = nl;
-    stats[(r >> 7) * 256 + 128 + row] = s;
+    for (int w = LANES / 2; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+    if (c == 0) {
+      out[row] = nl;
+      out[128 + row] = s;
+    }
   }
 }
 
@@ -921,8 +926,7 @@ cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUten
 
 cudaError_t launch_ex_row_stats(int d, const ExTile& p, const uint16_t* o, const uint16_t* d_o, const float* lse,
                                 float* stats, cudaStream_t s) {
-  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.Tq * 128;
-  const unsigned grid = static_cast<unsigned>(rows / 8);
+  const unsigned grid = static_cast<unsigned>(p.B) * p.Hkv * p.Tq;
   if (d == 64) ex_row_stats<64><<<grid, 256, 0, s>>>(p, o, d_o, lse, stats);
   else ex_row_stats<128><<<grid, 256, 0, s>>>(p, o, d_o, lse, stats);
   note_launches(1);
