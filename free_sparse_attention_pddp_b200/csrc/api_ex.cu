@@ -111,7 +111,7 @@ FwdPlan fwd_plan(int B, int Hkv, int g, int Nq, int Nk, int d) {
   f.single = f.Tq <= 5 && f.Tq % 2 == 1 && f.Tk >= 4;
   const long long ctas = static_cast<long long>(B) * Hkv * (f.single ? f.Tq : (f.Tq + 1) / 2);
   f.nsplit = 1;
-  if (2 * ctas <= kSms && f.Tk >= 4) {
+  if (2 * ctas <= kSms && f.Tk >= (f.single ? 4 : 6)) {
     const long long most = f.Tk / (f.single ? 2 : 1);
     f.nsplit = static_cast<int>(std::max(1ll, std::min(kSms / ctas, most)));
   }
@@ -149,10 +149,26 @@ FwdWs fwd_layout(const FwdPlan& f, int B, int Hkv, int d) {
 
 // workspace: status | document tiles | statistics of the packed rows
 struct BwdWs {
-  size_t k_ids, k_ranges, q_ids, q_ranges, order, k_order, stats, total;
+  size_t k_ids, k_ranges, q_ids, q_ranges, order, k_order, stats, part_kv, total;
+  int kv_splits;
 };
 
-BwdWs bwd_layout(const FwdPlan& f, int B, int Hkv) {
+// A key tile's CTA sweeps all Tq query tiles (1.6 us each, 1.5 times as long as
+// a query CTA's key tile). Its sweep is split among several CTAs where they fit
+// the first wave and save at least five tiles' time (joining the parts costs
+// about 5 us), or where it would last twice an SM's share of the whole (many
+// query heads to a KV head).
+int kv_splits(const FwdPlan& f, int B, int Hkv) {
+  const long long heads = static_cast<long long>(B) * Hkv, keys = heads * f.Tk, queries = heads * f.Tq;
+  if (keys + queries < kSms) {
+    const int most = static_cast<int>(std::min<long long>({(kSms - queries) / keys, f.Tq / 2, 16}));
+    return most > 1 && f.Tq - f.Tq / most >= 5 ? most : 1;
+  }
+  const double sweep = 1.5 * f.Tq, share = static_cast<double>(keys) * (1.5 + 1.0) * f.Tq / kSms;
+  return sweep > 2 * share ? std::min({static_cast<int>(ceil(sweep / share)), f.Tq / 2, 16}) : 1;
+}
+
+BwdWs bwd_layout(const FwdPlan& f, int B, int Hkv, int Nk, int d) {
   BwdWs w;
   size_t off = MCS_STATUS_BYTES;
   auto take = [&](size_t bytes) {
@@ -167,6 +183,8 @@ BwdWs bwd_layout(const FwdPlan& f, int B, int Hkv) {
   w.order = take(static_cast<size_t>(B) * f.Tq * 4);
   w.k_order = take(static_cast<size_t>(B) * f.Tk * 4);
   w.stats = take(static_cast<size_t>(B) * Hkv * f.Tq * 1024);
+  w.kv_splits = kv_splits(f, B, Hkv);
+  w.part_kv = take(w.kv_splits > 1 ? static_cast<size_t>(w.kv_splits) * 2 * B * Nk * Hkv * d * 4 : 0);
   w.total = off;
   return w;
 }
@@ -321,7 +339,7 @@ size_t mcs_attn_workspace_bytes(const mcs_attn_shape* s, mcs_op op) {
   if (op == MCS_OP_DENSE_EX)
     return fwd_layout(fwd_plan(s->B, s->Hkv, s->Hq / s->Hkv, s->Nq, s->Nk, s->d), s->B, s->Hkv, s->d).total;
   if (op == MCS_OP_DENSE_BWD)
-    return bwd_layout(fwd_plan(s->B, s->Hkv, s->Hq / s->Hkv, s->Nq, s->Nk, s->d), s->B, s->Hkv).total;
+    return bwd_layout(fwd_plan(s->B, s->Hkv, s->Hq / s->Hkv, s->Nq, s->Nk, s->d), s->B, s->Hkv, s->Nk, s->d).total;
   return 0;
 }
 
@@ -387,7 +405,7 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
   ExParams p = ex_params(s, opts);
   p.status = static_cast<int*>(ws);
   const FwdPlan f = fwd_plan(p.B, p.Hkv, p.g, p.Nq, p.Nk, s->d);
-  const BwdWs w = bwd_layout(f, p.B, p.Hkv);
+  const BwdWs w = bwd_layout(f, p.B, p.Hkv, p.Nk, s->d);
   uint8_t* base = static_cast<uint8_t*>(ws);
   CUtensorMap tq, tg, tk, tv;
   const int qbox = 64 % p.g == 0 ? f.tpt / 2 : f.tpt;
@@ -398,6 +416,9 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
     return MCS_ERR_CUDA;
   ExTile t = tile_params(p, f, s->d);
   t.qbox = qbox;
+  t.kv_splits = w.kv_splits;
+  t.kv_size = static_cast<size_t>(p.B) * p.Nk * p.Hkv * s->d;
+  if (w.kv_splits > 1) t.part_kv = reinterpret_cast<float*>(base + w.part_kv);
   t.dq = static_cast<uint16_t*>(dq);
   t.dk = static_cast<uint16_t*>(dk);
   t.dv = static_cast<uint16_t*>(dv);

@@ -19,6 +19,8 @@
 //     the other half's products. With whole tiles in one chain the tensor pipe
 //     waited 1500 of every 3500 cycles; halves cost the N = 64 products 48
 //     cycles for 32 cycles of work.
+//     Where these CTAs are few, the query tiles are split among several, whose
+//     fp32 parts ex_sum_parts adds.
 //   dq_tile: a CTA owns one packed query tile and streams key tiles:
 //     S = Q K^T, dP = d_o V^T, dS over dP, dQ += dS K. S(i+1) and dP(i+1) are
 //     computed while the softmax works on tile i (dP has two buffers).
@@ -100,6 +102,24 @@ __device__ __forceinline__ void store_row(uint32_t taddr, bool have, bool valid,
     for (int e = 0; e < W / 8; ++e)
       d4[e] = make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
                          pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
+  }
+}
+
+// The same as fp32.
+template <int N>
+__device__ __forceinline__ void store_part(uint32_t taddr, bool have, bool valid, float* dst) {
+#pragma unroll
+  for (int cc = 0; cc < N / 32; ++cc) {
+    float v[32];
+    if (have) {
+      tmem_ld32(taddr + cc * 32, v);
+      tmem_wait_ld();
+    }
+    if (!valid) continue;
+    float4* d4 = reinterpret_cast<float4*>(dst + cc * 32);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      d4[e] = have ? make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
 }
 
@@ -206,6 +226,8 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
   const int lane = threadIdx.x & 31;
   // causal: the first key tiles meet the most queries and go first, the heads of a chunk side by side
   const int BH = p.B * p.Hkv;
+  const int split = cta % p.kv_splits;  // the query tiles' part
+  cta /= p.kv_splits;
   int kt, bh;
   if (DOC && p.k_order) {  // the tiles with the most work first
     bh = ordered_job(p, p.k_order, p.Tk, cta, &kt);
@@ -225,6 +247,9 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
   // query tiles lo .. Tq - 1 reach these keys
   int lo = 0;
   if (p.causal && kt * 128 >= prefix) lo = min(p.Tq, max(0, kt * 128 - off) / p.tpt);
+  const int rest = p.Tq - lo;
+  const int hi = lo + static_cast<int>(static_cast<long long>(rest) * (split + 1) / p.kv_splits);
+  lo += static_cast<int>(static_cast<long long>(rest) * split / p.kv_splits);
   const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
   const int4 mine = DOC ? p.k_ranges[static_cast<size_t>(b) * p.Tk + kt] : none;
   const int rt = p.tpt * p.g;
@@ -268,10 +293,10 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int n = p.Tq - lo;
+  int n = hi - lo;
   TileBits tiles(bits, p.Tq);
   if (DOC) {
-    tiles.build<false>(count, p.q_ranges + static_cast<size_t>(b) * p.Tq, lo, p.Tq, mine, none);
+    tiles.build<false>(count, p.q_ranges + static_cast<size_t>(b) * p.Tq, lo, hi, mine, none);
     n = count[0];
   }
   const TileIter first{DOC ? tiles.meet : nullptr, nullptr, lo, lo};
@@ -585,7 +610,10 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
       const size_t at = ((static_cast<size_t>(b) * p.Nk + key) * p.Hkv + hk) * D;
       // quarters 0 and 1 store the two halves of dV's columns, 2 and 3 those of dK's
       const int c0 = (quarter & 1) * (D / 2);
-      if (quarter < 2) store_row<D / 2>(tmem + lane_addr + 256 + c0, n > 0, key_valid, 1.f, p.dv + at + c0);
+      if (p.part_kv)
+        store_part<D / 2>(tmem + lane_addr + (quarter < 2 ? 256 : 384) + c0, n > 0, key_valid,
+                          p.part_kv + (quarter < 2 ? 0 : p.kv_splits * p.kv_size) + split * p.kv_size + at + c0);
+      else if (quarter < 2) store_row<D / 2>(tmem + lane_addr + 256 + c0, n > 0, key_valid, 1.f, p.dv + at + c0);
       else store_row<D / 2>(tmem + lane_addr + 384 + c0, n > 0, key_valid, p.scale, p.dk + at + c0);
     }
     __syncwarp();
@@ -900,12 +928,32 @@ template <int D, bool CAP, bool BIAS, bool DOC>
 __global__ void __launch_bounds__(kThreads, 1)
     ex_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
-  const int keys = p.B * p.Hkv * p.Tk;
+  const int keys = p.B * p.Hkv * p.Tk * p.kv_splits;
   if (static_cast<int>(blockIdx.x) < keys) dkv_tile<D, CAP, BIAS, DOC>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x);
   else dq_tile<D, CAP, BIAS, DOC>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x - keys);
 }
 
 namespace {
+
+// dV and dK as the sums of their parts over the query tiles, in the parts' order; four values per thread.
+__global__ void __launch_bounds__(256) ex_sum_parts(const ExTile p) {
+  const size_t quads = p.kv_size / 4;
+  const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= 2 * quads) return;
+  const bool key = i >= quads;
+  const size_t at = key ? i - quads : i;
+  const float4* src = reinterpret_cast<const float4*>(p.part_kv) + (key ? p.kv_splits * quads : 0) + at;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < p.kv_splits; ++s) {
+    const float4 x = src[s * quads];
+    a.x += x.x;
+    a.y += x.y;
+    a.z += x.z;
+    a.w += x.w;
+  }
+  const float f = key ? p.scale : 1.f;
+  reinterpret_cast<uint2*>(key ? p.dk : p.dv)[at] = make_uint2(pack_bf16(a.x * f, a.y * f), pack_bf16(a.z * f, a.w * f));
+}
 
 template <int D, bool CAP, bool BIAS, bool DOC>
 cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk, const CUtensorMap* tv,
@@ -917,8 +965,9 @@ cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUten
   if (e != cudaSuccess) return e;
   const unsigned smem = std::max(DkvCfg<D>::SMEM + (DOC ? (p.Tq + 31) / 32 * 12u : 0u),
                                  DqCfg<D>::SMEM + (DOC ? (p.Tk + 31) / 32 * 12u : 0u));
-  kern<<<p.B * p.Hkv * (p.Tk + p.Tq), kThreads, smem, s>>>(*tq, *tg, *tk, *tv, p);
-  note_launches(1);
+  kern<<<p.B * p.Hkv * (p.Tk * p.kv_splits + p.Tq), kThreads, smem, s>>>(*tq, *tg, *tk, *tv, p);
+  if (p.part_kv) ex_sum_parts<<<static_cast<unsigned>((p.kv_size / 2 + 255) / 256), 256, 0, s>>>(p);
+  note_launches(p.part_kv ? 2 : 1);
   return cudaGetLastError();
 }
 

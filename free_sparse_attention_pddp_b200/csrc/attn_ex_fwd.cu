@@ -556,21 +556,36 @@ __global__ void __launch_bounds__(128) ex_combine(const ExTile p, int parts) {
   const size_t at = ((static_cast<size_t>(b) * p.Hkv + head / p.g) * p.Tq + tok / p.tpt) * 128 + tok % p.tpt * p.g +
                     head % p.g;
   const size_t slice = static_cast<size_t>(p.B) * p.Hkv * p.Tq * 128;
-  float m = -CUDART_INF_F;
-  for (int s = lane; s < parts; s += 32) m = fmaxf(m, p.part_lse[s * slice + at]);
+  float m = -CUDART_INF_F, l = 0.f, o[E] = {};
+  // four parts at a time, so that their loads overlap
+  for (int s0 = 0; s0 < parts; s0 += 4) {
+    float ls[4], v[4][E];
 #pragma unroll
-  for (int w = 16; w; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-  float l = 0.f, o[E] = {};
-  if (m > -CUDART_INF_F)
-    for (int s = 0; s < parts; ++s) {
-      const float w = fast_exp2(p.part_lse[s * slice + at] - m);
-      const float* src = p.part_o + (s * slice + at) * D + lane * E;
-      l += w;
-      if (w > 0.f) {
+    for (int k = 0; k < 4; ++k) {
+      ls[k] = -CUDART_INF_F;
+      if (s0 + k < parts) {
+        ls[k] = p.part_lse[(s0 + k) * slice + at];
+        const float* src = p.part_o + ((s0 + k) * slice + at) * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
+        for (int e = 0; e < E; ++e) v[k][e] = src[e];
       }
     }
+    const float mn = fmaxf(m, fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3])));
+    if (mn == -CUDART_INF_F) continue;
+    const float a = fast_exp2(m - mn);
+    m = mn;
+    l *= a;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= a;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (ls[k] == -CUDART_INF_F) continue;
+      const float w = fast_exp2(ls[k] - m);
+      l += w;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[k][e], o[e]);
+    }
+  }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + static_cast<size_t>(r) * D + lane * E);
 #pragma unroll

@@ -163,6 +163,9 @@ struct ExTile {
   float* lse;
   const float* stats;              // backward: [B,Hkv,Tq][2][128], -lse in log2 units and d_o . o
   const float* lse_in;             // backward: the forward's lse
+  int kv_splits;                   // backward: CTAs that share a key tile's queries
+  size_t kv_size;                  // elements of dk
+  float* part_kv;                  // [2 (dv, dk)][kv_splits][B,Nk,Hkv,d], null unless kv_splits > 1
   uint16_t *dq, *dk, *dv;
   float *part_o, *part_lse;        // [parts][B,Hkv,Tq,128](,d), lse in log2 units
   int* status;

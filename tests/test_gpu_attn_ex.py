@@ -257,3 +257,18 @@ def test_one_pass_equals_mcs_dense(mcs):
     for n, t in (("o", o), ("lse", lse)):  # both lie within the same bound of the exact value
         attn_ref.check(got[n], want[n], n)
         attn_ref.check(t, want[n], n)
+
+
+def test_queries_split_among_key_tiles(mcs):
+    """Many query heads to one KV head, and few key tiles: dK and dV come as parts that are added."""
+    both(mcs, 1, 8, 1, 2100, 300, 128, causal=True, cap=30.0, seed=24)
+    both(mcs, 1, 24, 1, 1500, 1500, 64, causal=True, slopes=[.01 * h for h in range(24)], seed=25)
+    ids = packed_ids(2, 900, 300, 7, 100)
+    both(mcs, 2, 6, 1, 900, 900, 64, doc_q=ids, doc_k=ids, seed=26)
+
+
+def test_documents_in_many_jobs(mcs):
+    """More jobs than SMs, so that they run in the order of their tiles."""
+    ids = packed_ids(3, 1300, 500, 8, 250)
+    both(mcs, 3, 8, 8, 1300, 1300, 64, doc_q=ids, doc_k=ids, causal=True, prefix=[0, 700, 1300], seed=27)
+    both(mcs, 3, 9, 3, 1300, 1300, 128, doc_q=ids, doc_k=ids, cap=20.0, seed=28)
