@@ -15,8 +15,9 @@
 //           ex_combine like any other split of the keys.
 //
 // TMEM (512 columns): S_0 | S_1 (128 each) | O_0 | O_1 (D each). P_t (bf16
-// pairs) overwrites the first 64 columns of S_t and is the TS-form A operand of
-// O_t += P_t V.
+// pairs, the TS-form A operand of O_t += P_t V) overwrites S_t where d = 128. With
+// d = 64 it has columns of its own, and S(i + 1) is computed while the softmax
+// works on S(i).
 //
 // Masks: a key tile is skipped, whole, or partial. Causal and prefix masks
 // bound the tile range and give each row a key limit; a document mask skips
@@ -42,6 +43,8 @@ constexpr float kRescale = 4.0f;
 
 template <int D>
 struct FwdCfg {
+  // With d = 64 the accumulators leave 128 TMEM columns for P, so S(i + 1) need not wait for O += P(i) V.
+  static constexpr bool AHEAD = D == 64;
   static constexpr int KB = D / 64;
   static constexpr uint32_t TILE = 128u * D * 2u;
   static constexpr int NS = D == 128 ? 2 : 4;  // K/V stages
@@ -49,8 +52,8 @@ struct FwdCfg {
   static constexpr uint32_t OFF_K = 2 * TILE;
   static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
   static constexpr uint32_t OFF_BAR = OFF_V + NS * TILE;
-  // q_full, k_full[NS], v_full[NS], v_ok[NS], k_empty[NS], v_empty[NS], s_full[2], p_full[2], p_empty[2], drain
-  static constexpr uint32_t NBAR = 1 + 5 * NS + 2 + 2 + 2 + 1;
+  // q_full, k_full[NS], v_full[NS], v_ok[NS], k_empty[NS], v_empty[NS], s_full[2], s_read[2], p_full[2], p_empty[2], drain
+  static constexpr uint32_t NBAR = 1 + 5 * NS + 8 + 1;
   static constexpr uint32_t OFF_MAX = OFF_BAR + (NBAR * 8 + 32 + 15) / 16 * 16;  // [parity][slot][half][row]
   static constexpr uint32_t OFF_BITS = OFF_MAX + 2 * 2 * 2 * 128 * 8;
   static constexpr uint32_t SMEM = OFF_BITS + 1024;  // and five bits for each key tile under a document mask
@@ -75,7 +78,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_empty = v_ok + C::NS;        // [stage]: every S from it is computed
   uint64_t* v_empty = k_empty + C::NS;     // [stage]: every O += P V from it is done
   uint64_t* s_full = v_empty + C::NS;      // [slot]: S(i) computed
-  uint64_t* p_full = s_full + 2;           // [slot]: P(i) written (and O rescaled)
+  uint64_t* s_read = s_full + 2;           // [slot]: S(i) is in registers (AHEAD)
+  uint64_t* p_full = s_read + 2;           // [slot]: P(i) written (and O rescaled)
   uint64_t* p_empty = p_full + 2;          // [slot]: O += P(i) V done
   uint64_t* drain_bar = p_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
@@ -139,6 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s_full[t], 1);
+      mbar_init(&s_read[t], 256);
       mbar_init(&p_full[t], 256);
       mbar_init(&p_empty[t], 1);
     }
@@ -203,8 +208,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t dVs = sdesc_advance(dV, (j % C::NS) * C::TILE);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(tmem + 256 + t * D, tmem + t * 128 + (kk >> 2) * 64 + (kk & 3) * 8, sdesc_advance(dVs, kk * 2048),
-                         IDESC_O,
+            umma_bf16_ts(tmem + 256 + t * D,
+                         C::AHEAD ? tmem + 384 + t * 64 + kk * 8 : tmem + t * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                         sdesc_advance(dVs, kk * 2048), IDESC_O,
                          (i > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&p_empty[t]);
         };
@@ -240,6 +246,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           return f;
         };
         int flags = look(0);
+        if constexpr (C::AHEAD) {
+          // S of a step, then the products of the step before
+          int prev = 0, o0 = 0, o1 = 0;
+          for (int step = 0; ok && step <= steps; ++step) {
+            const int j0 = single ? 2 * step : step, j1 = single ? j0 + 1 : j0;
+            const int p0 = single ? j0 - 2 : j0 - 1, p1 = single ? j1 - 2 : j1 - 1;
+            const int now = flags;
+            if (now & 1) {
+              if (!(ok = wait(&k_full[j0 % C::NS], j0 / C::NS) && (i0 == 0 || wait(&s_read[0], i0 - 1)))) break;
+              tc_fence_after();
+              issue_s(0, j0);
+              if (single || !(now & 2)) umma_commit(&k_empty[j0 % C::NS]);
+              ++i0;
+            }
+            if (now & 2) {
+              if (!(ok = wait(&k_full[j1 % C::NS], j1 / C::NS) && (i1 == 0 || wait(&s_read[1], i1 - 1)))) break;
+              tc_fence_after();
+              issue_s(1, j1);
+              umma_commit(&k_empty[j1 % C::NS]);
+              ++i1;
+            }
+            flags = look(step + 1);
+            if (prev & 1) {
+              if (!(ok = v_there(p0, prev & 4) && wait(&p_full[0], o0))) break;
+              tc_fence_after();
+              issue_o(0, o0, p0);
+              if (single || !(prev & 2)) umma_commit(&v_empty[p0 % C::NS]);
+              ++o0;
+            }
+            if (prev & 2) {
+              if (!(ok = v_there(p1, prev & 8) && wait(&p_full[1], o1))) break;
+              tc_fence_after();
+              issue_o(1, o1, p1);
+              umma_commit(&v_empty[p1 % C::NS]);
+              ++o1;
+            }
+            prev = now;
+          }
+        } else
         // UMMAs run in order, so S_t(i + 1) overwrites P_t(i) only after the product that reads it
         for (int step = 0; ok && step <= steps; ++step) {
           const int j0 = single ? 2 * step : step, j1 = single ? j0 + 1 : j0;
@@ -335,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = wq * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + lane_addr + t * 128 + half * 64;
+    const uint32_t tP = C::AHEAD ? tmem + lane_addr + 384 + t * 64 + half * 32 : tS;
     const uint32_t tO = tmem + lane_addr + 256 + t * D + half * (D / 2);  // this half's output columns
     const int nt = t == 0 ? n0 : n1;
     const int qt = single ? qt0 : qt0 + t;
@@ -376,6 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(tS, sv);
       tmem_ld32(tS + 32, sv + 32);
       tmem_wait_ld();
+      if (C::AHEAD) {
+        tc_fence_before();
+        mbar_arrive(&s_read[t]);
+      }
       float shift = 0.f;  // log2 units that the whole row of this tile lacks
       if (CAP) cap_scores<64>(sv, p.cap);
       if (BIAS) {
@@ -429,10 +479,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           v[2 * q + 1] = fast_exp2(x1);
           pk[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
         }
-        tmem_st16u(tS + h2 * 16, pk);
+        if (C::AHEAD && h2 == 0 && i > 0) {  // O += P(i-1) V has read P(i-1), and O may be scaled
+          ok = mbar_wait_warp(&p_empty[t], (i - 1) & 1, wctx, MCS_WHERE_ATTN_SOFTMAX);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        tmem_st16u(tP + h2 * 16, pk);
       }
+      if (!ok) continue;  // the other half learns of it in the next step
       if (i > 0 && __any_sync(0xffffffffu, need)) {
-        // O += P(i-1) V ran before S(i), so O may be scaled here; O += P(i) V waits for p_full
+        // O += P(i-1) V ran before S(i) (AHEAD: before this step's P), so O may be scaled here; O += P(i) V waits for p_full
         const float alpha = need ? fast_exp2(m_old - m) : 1.f;
         l *= alpha;
 #pragma unroll 1
