@@ -11,6 +11,7 @@ using namespace mcs;
 namespace {
 
 constexpr int kMaxGroup = 128;            // query heads of one KV head: one 128-row tile holds a token's
+constexpr int kExactDeltaKeys = 256;      // up to so many keys D is summed from P dP (ex_row_stats)
 constexpr int kMaxDocQueryTiles = 1 << 16;  // tiles of a document mask's bitmaps: over query tiles
 constexpr int kMaxDocKeyTiles = 1 << 12;    // and over key tiles (the dQ kernel has 1 KB left for it)
 
@@ -443,7 +444,8 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
       t.k_order = k_order;
     }
   }
-  if (launch_ex_row_stats(s->d, t, static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(d_o), lse, stats,
+  if (p.Nk <= kExactDeltaKeys) t.stats_out = stats;
+  else if (launch_ex_row_stats(s->d, t, static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(d_o), lse, stats,
                           stream) != cudaSuccess)
     return MCS_ERR_CUDA;
   return ok_or_cuda(launch_ex_bwd(s->d, &tq, &tg, &tk, &tv, t, stream));

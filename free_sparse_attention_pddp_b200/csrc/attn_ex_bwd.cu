@@ -153,7 +153,9 @@ __device__ __forceinline__ void teardown(volatile int* abort_flag, uint64_t* don
 
 // Per packed row: -lse in log2 units (less slope times the row's token in the tile, which the dK/dV tiles' bias counts
 // on) and D = d_o . o, as [B Hkv, Tq][2][128]; an empty row, like a row whose lse is -inf, gets (-inf, 0), which makes
-// its P zero. One CTA per tile, 16 bytes of a row per lane: reading o and d_o once from HBM is the bound.
+// its P zero. o is rounded to bf16, so D is off by up to 2^-8 |d_o| |o|: little beside dP where a row's P is spread over
+// many keys, but with few keys dP - D cancels (up to 0.5 % of dK and dQ, 1 % with sharp scores); there
+// ex_delta_kernel sums D from P dP instead, a sweep of two products. One CTA per tile, 16 bytes of a row per lane: reading o and d_o once from HBM is the bound.
 template <int D>
 __global__ void __launch_bounds__(256) ex_row_stats(const ExTile p, const uint16_t* o, const uint16_t* d_o,
                                                     const float* lse, float* stats) {
@@ -621,7 +623,7 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
   teardown(abort_flag, done, kv_full, n > 0 ? 1 + 4 * C::NS : 0, tmem);
 }
 
-template <int D, bool CAP, bool BIAS, bool DOC>
+template <int D, bool CAP, bool BIAS, bool DOC, bool DELTA>
 __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_g, const CUtensorMap& tm_k,
                                         const CUtensorMap& tm_v, const ExTile& p, int cta) {
   using C = DqCfg<D>;
@@ -756,7 +758,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
           tc_fence_after();
           const uint64_t bb = sdesc_advance(dKm, (i % C::NK) * C::TILE);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 0; kk < (DELTA ? 0 : 8); ++kk)
             umma_bf16_ts(tmem + 256, dp_buf(i) + (kk >> 1) * 32 + (kk & 1) * 8, sdesc_advance(bb, kk * 2048),
                          IDESC_A, (i > 0 || kk > 0) ? 1u : 0u);
           umma_commit(&k_empty[i % C::NK]);
@@ -824,7 +826,8 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
     const bool row_valid = row < rt && tok < p.Nq;
     const float* st = p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
     const float lse = row_valid ? p.lse_in[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok] : -CUDART_INF_F;
-    const float negl = lse > -CUDART_INF_F ? -lse * kLog2e : -CUDART_INF_F, delta = st[128 + row];
+    const float negl = lse > -CUDART_INF_F ? -lse * kLog2e : -CUDART_INF_F, delta = DELTA ? 0.f : st[128 + row];
+    uint64_t d2 = 0;  // DELTA: the sum of P dP, over even and odd columns
     const uint64_t negl2 = f2_pack(negl, negl), delta2 = f2_pack(delta, delta);
     const int pos = off + tok;
     const int lim = limit(pos) - quarter * 32;
@@ -856,7 +859,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
       if (CAP) {
         cap_scores<32>(pv, p.cap);
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) f2_unpack(cap_slope2(f2_pack(pv[c], pv[c + 1]), p.cap), w[c], w[c + 1]);
+        for (int c = 0; c < (DELTA ? 0 : 32); c += 2) f2_unpack(cap_slope2(f2_pack(pv[c], pv[c + 1]), p.cap), w[c], w[c + 1]);
       }
       uint64_t e2 = negl2;
       if (BIAS) {
@@ -870,7 +873,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
         pv[c] = fast_exp2(x0);
         pv[c + 1] = fast_exp2(x1);
       }
-      if (CAP) {
+      if (CAP && !DELTA) {
 #pragma unroll
         for (int c = 0; c < 32; c += 2)
           f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_pack(w[c], w[c + 1])), pv[c], pv[c + 1]);
@@ -896,23 +899,42 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
       tc_fence_after();
       tmem_ld32(tP, w);
       tmem_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 32; c += 2)
-        f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_sub(f2_pack(w[c], w[c + 1]), delta2)), w[c], w[c + 1]);
       if (partial) {  // a padded key's V, a padded query's d_o may be NaN
 #pragma unroll
         for (int c = 0; c < 32; ++c) w[c] = pv[c] == 0.f ? 0.f : w[c];
       }
-      uint32_t pk[16];
+      if (DELTA) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(w[2 * c], w[2 * c + 1]);
-      tmem_st16u(tP, pk);  // over dP columns that this thread has read
-      tmem_wait_st();
+        for (int c = 0; c < 32; c += 2) d2 = f2_fma(f2_pack(pv[c], pv[c + 1]), f2_pack(w[c], w[c + 1]), d2);
+      } else {
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          float a, b2;
+          f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_sub(f2_pack(w[c], w[c + 1]), delta2)), a, b2);
+          pk[c / 2] = pack_bf16(a, b2);
+        }
+        tmem_st16u(tP, pk);  // over dP columns that this thread has read
+        tmem_wait_st();
+      }
       tc_fence_before();
       mbar_arrive(&ds_full[i & 1]);
     }
     const bool fin = ok && (n == 0 || mbar_wait_warp(done, 0, wctx, MCS_WHERE_ATTN_EPILOGUE));
-    if (fin) {
+    if (DELTA) {
+      // the four quarters' sums, added in order; the ring has no reader or writer left
+      float* sums = reinterpret_cast<float*>(sK);
+      float even, odd;
+      f2_unpack(d2, even, odd);
+      sums[quarter * 128 + row] = even + odd;
+      named_barrier_sync<2, 512>();
+      if (fin && quarter == 0) {
+        const bool live = negl > -CUDART_INF_F;
+        float* out = p.stats_out + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
+        out[row] = BIAS && live ? fmaf(-p.slopes[head] * kLog2e, static_cast<float>(row / p.g), negl) : negl;
+        out[128 + row] = live ? (sums[row] + sums[128 + row]) + (sums[256 + row] + sums[384 + row]) : 0.f;
+      }
+    } else if (fin) {
       tc_fence_after();
       // each quarter of the warps stores its quarter of the columns
       const int c0 = quarter * (D / 4);
@@ -930,7 +952,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
   const int keys = p.B * p.Hkv * p.Tk * p.kv_splits;
   if (static_cast<int>(blockIdx.x) < keys) dkv_tile<D, CAP, BIAS, DOC>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x);
-  else dq_tile<D, CAP, BIAS, DOC>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x - keys);
+  else dq_tile<D, CAP, BIAS, DOC, false>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x - keys);
+}
+
+// The rows' statistics with D summed from P dP in fp32, for few keys (see ex_row_stats).
+template <int D, bool CAP, bool BIAS, bool DOC>
+__global__ void __launch_bounds__(kThreads, 1)
+    ex_delta_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
+                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const ExTile p) {
+  dq_tile<D, CAP, BIAS, DOC, true>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x);
 }
 
 namespace {
@@ -965,6 +996,15 @@ cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUten
   if (e != cudaSuccess) return e;
   const unsigned smem = std::max(DkvCfg<D>::SMEM + (DOC ? (p.Tq + 31) / 32 * 12u : 0u),
                                  DqCfg<D>::SMEM + (DOC ? (p.Tk + 31) / 32 * 12u : 0u));
+  if (p.stats_out) {
+    static KernelReady ready_delta;
+    auto delta = ex_delta_kernel<D, CAP, BIAS, DOC>;
+    const cudaError_t e2 = make_ready(ready_delta, delta, most_q, 0);
+    if (e2 != cudaSuccess) return e2;
+    delta<<<p.B * p.Hkv * p.Tq, kThreads, DqCfg<D>::SMEM + (DOC ? (p.Tk + 31) / 32 * 12u : 0u), s>>>(*tq, *tg, *tk,
+                                                                                                  *tv, p);
+    note_launches(1);
+  }
   kern<<<p.B * p.Hkv * (p.Tk * p.kv_splits + p.Tq), kThreads, smem, s>>>(*tq, *tg, *tk, *tv, p);
   if (p.part_kv) ex_sum_parts<<<static_cast<unsigned>((p.kv_size / 2 + 255) / 256), 256, 0, s>>>(p);
   note_launches(p.part_kv ? 2 : 1);

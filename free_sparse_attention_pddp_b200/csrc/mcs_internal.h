@@ -166,6 +166,7 @@ struct ExTile {
   int kv_splits;                   // backward: CTAs that share a key tile's queries
   size_t kv_size;                  // elements of dk
   float* part_kv;                  // [2 (dv, dk)][kv_splits][B,Nk,Hkv,d], null unless kv_splits > 1
+  float* stats_out;                // not null: the statistics come from the sweep over the keys
   uint16_t *dq, *dk, *dv;
   float *part_o, *part_lse;        // [parts][B,Hkv,Tq,128](,d), lse in log2 units
   int* status;

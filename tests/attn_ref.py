@@ -9,7 +9,8 @@ relative to the value, e = 2^-24 half an fp32 step.
   P: relative error <= 2 Es_i (its own score and the row's sum), then u where it
   is rounded to bf16; every sum over n terms adds n e of the terms' sizes.
   o: u |o| + (u + 2 Es_i + n e) sum P |v|.
-  dS = P (dP - D) (1 - t^2): dP like x; D = d_o.o with the o that was rounded.
+  dS = P (dP - D) (1 - t^2): dP like x; D = d_o.o with the o that was rounded, or
+  summed from P dP in fp32.
   dq, dk, dv: u of the value, plus the terms' errors times |k|, |q|, |d_o|.
   Underflow: a probability below 2^-126, fp32's and bf16's smallest normal
   number, may become 0, and so may a result. With at most 2^17 terms of size
@@ -39,11 +40,11 @@ def valid_mask(B, Nq, Nk, causal=False, prefix=None, doc_q=None, doc_k=None, dev
     return ok
 
 
-def attn(q, k, v, d_o=None, scale=None, cap=0.0, slopes=None, pos=None, valid=None):
+def attn(q, k, v, d_o=None, scale=None, cap=0.0, slopes=None, pos=None, valid=None, exact_d=False):
     """q [B,Nq,Hq,d], k, v [B,Nk,Hkv,d] of any type; pos [B or 1, Nq] query positions; valid bool [B,Nq,Nk].
 
     Returns a dict of (value, bound) pairs, fp64: o [B,Nq,Hq,d], lse [B,Hq,Nq] and,
-    with d_o, dq, dk, dv. Rows that no pair needs may hold NaN."""
+    with d_o, dq, dk, dv. Rows that no pair needs may hold NaN. exact_d: D is summed from P dP in fp32."""
     B, Nq, Hq, d = q.shape
     Nk, Hkv = k.shape[1:3]
     g = Hq // Hkv
@@ -85,6 +86,8 @@ def attn(q, k, v, d_o=None, scale=None, cap=0.0, slopes=None, pos=None, valid=No
         dS = P * (dP - D) * w
         edp = (d + 8) * E * (G.abs() @ V.abs().transpose(-1, -2))
         ed = (G.abs() * (tol_o + (d + 8) * E * o.abs())).sum(-1, keepdim=True)
+        if exact_d:  # dP's and P's errors, and the sum's
+            ed = (P * (edp + Ep * dP.abs())).sum(-1, keepdim=True)
         et = 2.0 ** -20 + (es / cap if cap else 0.0)  # of t
         tol_dS = U * dS.abs() + P * w * (edp + ed + Ep * (dP - D).abs()) + P * (dP - D).abs() * 2 * t.abs() * et
         if not cap:

@@ -60,7 +60,7 @@ def both(mcs, B, Hq, Hkv, Nq, Nk, d, cap=0.0, scale=0.0, slopes=None, causal=Fal
     shape = mcs.AttnShape(B, Hq, Hkv, Nq, Nk, d, scale=scale, cap=cap, causal=causal)
     got = run(mcs, shape, q, k, v, d_o, slopes=slopes, prefix=prefix, doc_q=doc_q, doc_k=doc_k)
     valid = attn_ref.valid_mask(B, Nq, Nk, causal, prefix, doc_q, doc_k, "cuda")
-    want = attn_ref.attn(q, k, v, d_o, scale=scale or None, cap=cap, slopes=slopes, valid=valid)
+    want = attn_ref.attn(q, k, v, d_o, scale=scale or None, cap=cap, slopes=slopes, valid=valid, exact_d=Nk <= 256)
     for name in ("lse", "o", "dv", "dk", "dq"):
         attn_ref.check(got[name], want[name], name)
     return got
@@ -272,3 +272,11 @@ def test_documents_in_many_jobs(mcs):
     ids = packed_ids(3, 1300, 500, 8, 250)
     both(mcs, 3, 8, 8, 1300, 1300, 64, doc_q=ids, doc_k=ids, causal=True, prefix=[0, 700, 1300], seed=27)
     both(mcs, 3, 9, 3, 1300, 1300, 128, doc_q=ids, doc_k=ids, cap=20.0, seed=28)
+
+
+@pytest.mark.parametrize("gain", [2.0, 6.0])
+@pytest.mark.parametrize("N", [2, 3, 5, 17, 60, 256])
+def test_few_keys_and_sharp_scores(mcs, N, gain):
+    """dP - D cancels where a row has few keys: D must not carry o's rounding."""
+    both(mcs, 2, 6, 3, N, N, 64, causal=True, gain=gain, seed=N)
+    both(mcs, 1, 4, 4, N, N, 128, gain=gain, cap=30.0, slopes=[.1, .2, .3, .4], seed=N + 1)
