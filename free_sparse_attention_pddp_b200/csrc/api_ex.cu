@@ -226,7 +226,7 @@ mcs_status check_decode(const mcs_decode_shape* s) {
 // request should not run alone), in chunks of at least 512 keys, less only
 // where the batch would not fill one wave.
 struct DecodePlan {
-  int gsplit, chunk, nsplit;
+  int gsplit, chunk, nsplit, cluster;
   FwdPlan pre;
 };
 
@@ -241,6 +241,7 @@ DecodePlan decode_plan(const mcs_decode_shape* s) {
   };
   f.chunk = static_cast<int>(std::max(64ll, std::max(cut(8 * slots), std::min(512ll, cut(slots)))));
   f.nsplit = (s->C + f.chunk - 1) / f.chunk;
+  f.cluster = s->P == 0 && f.nsplit > 1 && f.nsplit <= 8 && jobs * f.nsplit <= slots;
   if (s->P > 0) f.pre = fwd_plan(1, s->Hkv, g, s->B, s->P, s->d);
   return f;
 }
@@ -258,7 +259,7 @@ DecodeWs decode_layout(const DecodePlan& f, const mcs_decode_shape* s) {
     off = align256(off + bytes);
     return at;
   };
-  const bool parts = f.nsplit > 1 || s->P > 0;
+  const bool parts = (f.nsplit > 1 && !f.cluster) || s->P > 0;
   const size_t rows = parts ? static_cast<size_t>(s->B) * s->Hq * f.nsplit : 0;
   const size_t pre = s->P > 0 ? static_cast<size_t>(f.pre.parts) * s->Hkv * f.pre.Tq * 128 : 0;
   w.part_lse = take(rows * 4);
@@ -296,7 +297,8 @@ mcs_status decode_call(const mcs_decode_shape* s, const void* q, const void* kp,
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
   p.status = static_cast<int*>(ws);
-  const bool parts = f.nsplit > 1 || s->P > 0;
+  const bool parts = (f.nsplit > 1 && !f.cluster) || s->P > 0;
+  p.cluster = f.cluster;
   if (parts) {
     p.part_lse = reinterpret_cast<float*>(base + w.part_lse);
     p.part_o = reinterpret_cast<float*>(base + w.part_o);

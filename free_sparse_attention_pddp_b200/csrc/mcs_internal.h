@@ -191,6 +191,7 @@ struct DecodeParams {
   int B, Hq, Hkv, g, C;
   int nsplit, chunk;               // chunks of the keys, keys of a chunk
   int gsplit;                      // parts of a head group (32 heads each)
+  int cluster;                     // the chunks of a request are one cluster, which joins them
   float mul;                       // as in ExTile
   CapFn cap;
   const uint16_t *q, *k, *v;

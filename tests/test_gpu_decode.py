@@ -173,3 +173,11 @@ def test_prefill_then_tokens_then_gradients(mcs):
             attn_ref.check(x, tuple(y[:, t] for y in want["o"]), f"token {t}")
             attn_ref.check(l, tuple(y[..., t] for y in want["lse"]), f"lse of token {t}")
     assert mcs.mcs_poll_status(ws)[0] == 0 and mcs.mcs_poll_status(wl)[0] == 0
+
+
+@pytest.mark.parametrize("C", [65, 128, 300, 512, 4000])
+def test_few_requests_whose_keys_are_split(mcs, C):
+    """One to three requests, chunks joined within a cluster or by a second launch, some of them empty."""
+    for B, Hq, Hkv in ((1, 12, 12), (3, 20, 1), (2, 40, 1)):
+        run(mcs, B, Hq, Hkv, C, 64, [C, 1, 0][:B], cap=20.0, slopes=[.02] * Hq, seed=C + B)
+        run(mcs, B, Hq, Hkv, C, 128, [C - 1, min(70, C - 1), 33][:B], seed=C)
