@@ -22,7 +22,8 @@ bool finite(float x) { return x == x && !isinf(x); }
 
 mcs_status check_heads(int Hq, int Hkv, int d, float scale, float cap) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1) return MCS_ERR_INVALID_ARG;
-  if (!finite(scale) || !finite(cap) || cap < 0.f) return MCS_ERR_INVALID_ARG;
+  if (!finite(scale) || (scale > 0.f && (scale < 1e-12f || scale > 1e12f))) return MCS_ERR_INVALID_ARG;
+  if (!finite(cap) || cap < 0.f || (cap > 0.f && cap < 1e-6f)) return MCS_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return MCS_ERR_UNSUPPORTED;
   if (Hq / Hkv > kMaxGroup) return MCS_ERR_UNSUPPORTED;
   return MCS_OK;

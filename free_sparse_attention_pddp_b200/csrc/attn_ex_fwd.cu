@@ -657,9 +657,9 @@ __global__ void __launch_bounds__(128) ex_combine(const ExTile p, int parts) {
 __global__ void __launch_bounds__(128) ex_doc_tiles(const ExTile p, int* k_ids, int4* k_ranges, int* q_ids,
                                                     int4* q_ranges) {
   __shared__ int s_min, s_max, s_pad;
-  const int b = blockIdx.y;
-  const bool key = static_cast<int>(blockIdx.x) < p.Tk;
-  const int tile = key ? blockIdx.x : blockIdx.x - p.Tk;
+  const int b = blockIdx.x / (p.Tk + p.Tq), at_b = blockIdx.x % (p.Tk + p.Tq);
+  const bool key = at_b < p.Tk;
+  const int tile = key ? at_b : at_b - p.Tk;
   if (threadIdx.x == 0) s_min = 0x7fffffff, s_max = static_cast<int>(0x80000000), s_pad = 0;
   __syncthreads();
   const int i = threadIdx.x;
@@ -799,7 +799,7 @@ cudaError_t launch_ex_doc_order(const ExTile& p, int per, int* q_order, int* k_o
 
 cudaError_t launch_ex_doc_tiles(const ExTile& p, int* k_ids, int4* k_ranges, int* q_ids, int4* q_ranges,
                                 cudaStream_t s) {
-  ex_doc_tiles<<<dim3(p.Tk + p.Tq, p.B), 128, 0, s>>>(p, k_ids, k_ranges, q_ids, q_ranges);
+  ex_doc_tiles<<<p.B * (p.Tk + p.Tq), 128, 0, s>>>(p, k_ids, k_ranges, q_ids, q_ranges);
   note_launches(1);
   return cudaGetLastError();
 }

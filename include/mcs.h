@@ -256,8 +256,8 @@ mcs_status mcs_dense(const mcs_shape* shape, const void* q, const void* k, const
 
 typedef struct mcs_attn_shape {
   int B, Hq, Hkv, Nq, Nk, d; /* d in {64, 128}; B*Nq*Hq and B*Nk*Hkv < 2^31 */
-  float scale;               /* <= 0 selects 1/sqrt(d) */
-  float cap;                 /* score cap; 0: none; negative or not finite: MCS_ERR_INVALID_ARG */
+  float scale;               /* <= 0 selects 1/sqrt(d); else in [1e-12, 1e12] */
+  float cap;                 /* score cap, at least 1e-6; 0: none */
   int flags;                 /* MCS_ATTN_CAUSAL or 0 */
 } mcs_attn_shape;
 

@@ -72,7 +72,7 @@ GOOD = dict(B=2, Hq=8, Hkv=4, Nq=100, Nk=300, d=128)
 
 @pytest.mark.parametrize("bad", [dict(B=0), dict(Hq=0), dict(Hkv=0), dict(Hkv=3), dict(Nq=0), dict(Nk=0), dict(Nk=-5),
                                  dict(d=96), dict(d=0), dict(cap=-1.0), dict(cap=math.nan), dict(cap=math.inf),
-                                 dict(scale=math.nan), dict(Hq=129, Hkv=1), dict(Nq=1 << 28),
+                                 dict(scale=math.nan), dict(scale=1e-20), dict(scale=1e20), dict(cap=1e-9), dict(Hq=129, Hkv=1), dict(Nq=1 << 28),
                                  dict(B=4, Nk=1 << 27)])
 def test_attn_shapes_are_refused(mcs, bad):
     s = mcs.AttnShape(**{**GOOD, **bad})

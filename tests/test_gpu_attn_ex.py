@@ -280,3 +280,44 @@ def test_few_keys_and_sharp_scores(mcs, N, gain):
     """dP - D cancels where a row has few keys: D must not carry o's rounding."""
     both(mcs, 2, 6, 3, N, N, 64, causal=True, gain=gain, seed=N)
     both(mcs, 1, 4, 4, N, N, 128, gain=gain, cap=30.0, slopes=[.1, .2, .3, .4], seed=N + 1)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_extreme_caps_and_scales(mcs, d):
+    both(mcs, 1, 2, 1, 70, 150, d, cap=1e-6, seed=29)
+    both(mcs, 1, 2, 1, 70, 150, d, cap=1e20, seed=30)
+    both(mcs, 1, 2, 1, 70, 150, d, scale=1e-12, slopes=[.5, .01], seed=31)
+
+
+def test_many_short_requests_with_documents(mcs):
+    """More requests than a grid's second dimension holds."""
+    B = 66000
+    ids = torch.tensor([[0, 0, 1]], dtype=torch.int32).repeat(B, 1)
+    both(mcs, B, 1, 1, 3, 3, 64, doc_q=ids, doc_k=ids, seed=32)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("docs", [False, True])
+def test_a_load_that_never_arrives_is_reported(mcs, docs, d):
+    """The producer withholds its first tile (debug flag bit 0): the bounded waits run out, the status says so, and
+    the next call computes."""
+    from free_sparse_attention_pddp_b200.binding import debug_set_flags
+
+    q, k, v, d_o = inputs(1, 2, 1, 140, 300, d, seed=33)
+    shape = mcs.AttnShape(1, 2, 1, 140, 300, d)
+    ids = dict(doc_q=torch.zeros(1, 140, dtype=torch.int32, device="cuda"),
+               doc_k=torch.zeros(1, 300, dtype=torch.int32, device="cuda")) if docs else {}
+    want = run(mcs, shape, q, k, v, d_o, **ids)
+    o, lse = torch.empty_like(q), torch.empty(1, 2, 140, device="cuda")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws, wb = (mcs.attn_workspace(shape, op) for op in (mcs.MCS_OP_DENSE_EX, mcs.MCS_OP_DENSE_BWD))
+    debug_set_flags(1)
+    try:
+        mcs.mcs_dense_ex(shape, q, k, v, o, lse, ws, **ids)
+        assert mcs.mcs_poll_status(ws)[0] == 4  # MCS_ERR_TIMEOUT
+        mcs.mcs_dense_bwd(shape, q, k, v, want["o"], want["lse"], d_o, dq, dk, dv, wb, **ids)
+        assert mcs.mcs_poll_status(wb)[0] == 4
+    finally:
+        debug_set_flags(0)
+    again = run(mcs, shape, q, k, v, d_o, **ids)
+    assert all(torch.equal(again[n], want[n]) for n in want)
