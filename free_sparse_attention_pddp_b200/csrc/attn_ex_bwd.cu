@@ -257,7 +257,63 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
   const int rt = p.tpt * p.g;
   const bool halves = p.qbox < p.tpt;  // a tile loads as two boxes of 64 rows
 
-  if (threadIdx.x == 0) {
+  const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
+  auto load_resident = [&]() {
+    mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
+#pragma unroll
+    for (int kb = 0; kb < C::KB; ++kb) {
+      tma_load_4d(&tm_k, kv_full, sK + kb * 16384, kb * 64, hk, kt * 128, b);
+      tma_load_4d(&tm_v, kv_full, sV + kb * 16384, kb * 64, hk, kt * 128, b);
+    }
+  };
+  // the loads of list entries j0 .. j1 - 1 (their tiles from `it`), for one thread
+  auto load_queries = [&](TileIter& it, int j0, int j1) {
+    bool ok = true;
+    for (int j = j0; j < j1 && ok; ++j) {
+      const int s = j % C::NS;
+      const int qt = it.next();
+      if ((p.debug_flags & 1) && j == 0) continue;  // test knob: never deliver tile 0
+      const uint32_t parity = ((j / C::NS) & 1) ^ 1;
+      const float* stats = p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
+      uint8_t* sS = smem + C::OFF_STAT + s * 1024;
+      auto free = [&](uint64_t* empty, int h) {
+        return j < C::NS || mbar_wait(&empty[2 * s + h], parity, wctx, MCS_WHERE_ATTN_PRODUCER);
+      };
+      auto box = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int h) {
+#pragma unroll
+        for (int kb = 0; kb < C::KB; ++kb)
+          tma_load_4d(map, bar, dst + s * C::TILE + kb * 16384 + h * 8192, kb * 64, hk * p.g,
+                      qt * p.tpt + h * p.qbox, b);
+      };
+      if (halves) {
+#pragma unroll
+        for (int h = 0; h < 2 && ok; ++h) {
+          if (!(ok = free(q_empty, h))) break;
+          mbar_arrive_expect_tx(&q_full[2 * s + h], C::KB * 8192 + 512);
+          box(&tm_q, &q_full[2 * s + h], sQ, h);
+          bulk_load(&q_full[2 * s + h], sS + h * 256, stats + h * 64, 256);
+          bulk_load(&q_full[2 * s + h], sS + 512 + h * 256, stats + 128 + h * 64, 256);
+          if (!(ok = free(g_empty, h))) break;
+          mbar_arrive_expect_tx(&g_full[2 * s + h], C::KB * 8192);
+          box(&tm_g, &g_full[2 * s + h], sG, h);
+        }
+      } else {  // a half's border cuts a token: the first half's barriers take the whole tile
+        if (!(ok = free(q_empty, 0) && free(q_empty, 1))) break;
+        mbar_arrive_expect_tx(&q_full[2 * s], C::KB * rt * 128 + 1024);
+        box(&tm_q, &q_full[2 * s], sQ, 0);
+        bulk_load(&q_full[2 * s], sS, stats, 1024);
+        if (!(ok = free(g_empty, 0) && free(g_empty, 1))) break;
+        mbar_arrive_expect_tx(&g_full[2 * s], C::KB * rt * 128);
+        box(&tm_g, &g_full[2 * s], sG, 0);
+      }
+    }
+  };
+  // without a document mask the list is known, and the first loads run beside the rest of the set-up
+  const int early = DOC ? 0 : max(0, min(hi - lo, C::NS));
+
+  if (warp == 1 && elect_one()) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_g);
     mbar_init(kv_full, 1);
     for (int s = 0; s < C::NS; ++s) {
       for (int h = 0; h < 2; ++h) {
@@ -278,6 +334,11 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
     *abort_flag = 0;
     count[0] = count[1] = count[2] = 0;
     fence_mbar_init();
+    if (early > 0) {
+      load_resident();
+      TileIter it{nullptr, nullptr, lo, lo};
+      load_queries(it, 0, early);
+    }
   }
   if (warp == 0) {
     tmem_alloc(tmem_slot, 512);
@@ -302,7 +363,6 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
     n = count[0];
   }
   const TileIter first{DOC ? tiles.meet : nullptr, nullptr, lo, lo};
-  const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
 
   if (warp < 4) {
     if (warp == 0) {
@@ -377,54 +437,10 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
     } else if (warp == 1) {
       // ---------------------------------------------------------------- TMA producer
       if (n > 0 && elect_one()) {
-        prefetch_tensormap(&tm_q);
-        prefetch_tensormap(&tm_g);
-        mbar_arrive_expect_tx(kv_full, 2 * C::TILE);
-#pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb) {
-          tma_load_4d(&tm_k, kv_full, sK + kb * 16384, kb * 64, hk, kt * 128, b);
-          tma_load_4d(&tm_v, kv_full, sV + kb * 16384, kb * 64, hk, kt * 128, b);
-        }
+        if (early == 0) load_resident();
         TileIter it = first;
-        bool ok = true;
-        for (int j = 0; j < n && ok; ++j) {
-          const int s = j % C::NS;
-          const int qt = it.next();
-          if ((p.debug_flags & 1) && j == 0) continue;  // test knob: never deliver tile 0
-          const uint32_t parity = ((j / C::NS) & 1) ^ 1;
-          const float* stats = p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
-          uint8_t* sS = smem + C::OFF_STAT + s * 1024;
-          auto free = [&](uint64_t* empty, int h) {
-            return j < C::NS || mbar_wait(&empty[2 * s + h], parity, wctx, MCS_WHERE_ATTN_PRODUCER);
-          };
-          auto box = [&](const CUtensorMap* map, uint64_t* bar, uint8_t* dst, int h) {
-#pragma unroll
-            for (int kb = 0; kb < C::KB; ++kb)
-              tma_load_4d(map, bar, dst + s * C::TILE + kb * 16384 + h * 8192, kb * 64, hk * p.g,
-                          qt * p.tpt + h * p.qbox, b);
-          };
-          if (halves) {
-#pragma unroll
-            for (int h = 0; h < 2 && ok; ++h) {
-              if (!(ok = free(q_empty, h))) break;
-              mbar_arrive_expect_tx(&q_full[2 * s + h], C::KB * 8192 + 512);
-              box(&tm_q, &q_full[2 * s + h], sQ, h);
-              bulk_load(&q_full[2 * s + h], sS + h * 256, stats + h * 64, 256);
-              bulk_load(&q_full[2 * s + h], sS + 512 + h * 256, stats + 128 + h * 64, 256);
-              if (!(ok = free(g_empty, h))) break;
-              mbar_arrive_expect_tx(&g_full[2 * s + h], C::KB * 8192);
-              box(&tm_g, &g_full[2 * s + h], sG, h);
-            }
-          } else {  // a half's border cuts a token: the first half's barriers take the whole tile
-            if (!(ok = free(q_empty, 0) && free(q_empty, 1))) break;
-            mbar_arrive_expect_tx(&q_full[2 * s], C::KB * rt * 128 + 1024);
-            box(&tm_q, &q_full[2 * s], sQ, 0);
-            bulk_load(&q_full[2 * s], sS, stats, 1024);
-            if (!(ok = free(g_empty, 0) && free(g_empty, 1))) break;
-            mbar_arrive_expect_tx(&g_full[2 * s], C::KB * rt * 128);
-            box(&tm_g, &g_full[2 * s], sG, 0);
-          }
-        }
+        it.cur += early;
+        load_queries(it, early, n);
       }
       __syncwarp();
     } else if (warp == 2 && DOC) {
@@ -674,7 +690,42 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
   const int4 mine = DOC ? p.q_ranges[static_cast<size_t>(b) * p.Tq + qt] : none;
   const int rt = p.tpt * p.g;
 
-  if (threadIdx.x == 0) {
+  const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
+  auto load_resident = [&]() {
+    mbar_arrive_expect_tx(qg_full, 2 * C::KB * rt * 128);
+#pragma unroll
+    for (int kb = 0; kb < C::KB; ++kb)
+      for (int h = 0; h < p.tpt / p.qbox; ++h) {
+        const int tok = qt * p.tpt + h * p.qbox;
+        tma_load_4d(&tm_q, qg_full, sQ + kb * 16384 + h * 8192, kb * 64, hk * p.g, tok, b);
+        tma_load_4d(&tm_g, qg_full, sG + kb * 16384 + h * 8192, kb * 64, hk * p.g, tok, b);
+      }
+  };
+  // the loads of list entries j0 .. j1 - 1 (their tiles from `it`), for one thread
+  auto load_keys = [&](TileIter& it, int j0, int j1) {
+    for (int j = j0; j < j1; ++j) {
+      const int sk = j % C::NK, sv = j % C::NV;
+      const int kt = it.next();
+      if (j >= C::NK && !mbar_wait(&k_empty[sk], ((j / C::NK) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+      if (!((p.debug_flags & 1) && j == 0)) {  // test knob: never deliver tile 0
+        mbar_arrive_expect_tx(&k_full[sk], C::TILE);
+#pragma unroll
+        for (int kb = 0; kb < C::KB; ++kb)
+          tma_load_4d(&tm_k, &k_full[sk], sK + sk * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
+      }
+      if (j >= C::NV && !mbar_wait(&v_empty[sv], ((j / C::NV) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+      mbar_arrive_expect_tx(&v_full[sv], C::TILE);
+#pragma unroll
+      for (int kb = 0; kb < C::KB; ++kb)
+        tma_load_4d(&tm_v, &v_full[sv], sV + sv * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
+    }
+  };
+  // without a document mask the list is known, and the first loads run beside the rest of the set-up
+  const int early = DOC ? 0 : max(0, min(hi, C::NV));
+
+  if (warp == 1 && elect_one()) {
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
     mbar_init(qg_full, 1);
     for (int s = 0; s < C::NK; ++s) {
       mbar_init(&k_full[s], 1);
@@ -695,6 +746,11 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
     *abort_flag = 0;
     count[0] = count[1] = count[2] = 0;
     fence_mbar_init();
+    if (early > 0) {
+      load_resident();
+      TileIter it{nullptr, nullptr, 0, 0};
+      load_keys(it, 0, early);
+    }
   }
   if (warp == 0) {
     tmem_alloc(tmem_slot, 512);
@@ -715,7 +771,6 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
     n = count[0];
   }
   const TileIter first{DOC ? tiles.meet : nullptr, nullptr, 0, 0};
-  const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
   // TMEM: S | dP 0 | dQ | dP 1
   auto dp_buf = [&](int i) { return tmem + ((i & 1) ? 384u : 128u); };
 
@@ -769,33 +824,10 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
     } else if (warp == 1) {
       // ---------------------------------------------------------------- TMA producer
       if (n > 0 && elect_one()) {
-        prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
-        mbar_arrive_expect_tx(qg_full, 2 * C::KB * rt * 128);
-#pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb)
-          for (int h = 0; h < p.tpt / p.qbox; ++h) {
-            const int tok = qt * p.tpt + h * p.qbox;
-            tma_load_4d(&tm_q, qg_full, sQ + kb * 16384 + h * 8192, kb * 64, hk * p.g, tok, b);
-            tma_load_4d(&tm_g, qg_full, sG + kb * 16384 + h * 8192, kb * 64, hk * p.g, tok, b);
-          }
+        if (early == 0) load_resident();
         TileIter it = first;
-        for (int j = 0; j < n; ++j) {
-          const int sk = j % C::NK, sv = j % C::NV;
-          const int kt = it.next();
-          if (j >= C::NK && !mbar_wait(&k_empty[sk], ((j / C::NK) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
-          if (!((p.debug_flags & 1) && j == 0)) {  // test knob: never deliver tile 0
-            mbar_arrive_expect_tx(&k_full[sk], C::TILE);
-#pragma unroll
-            for (int kb = 0; kb < C::KB; ++kb)
-              tma_load_4d(&tm_k, &k_full[sk], sK + sk * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
-          }
-          if (j >= C::NV && !mbar_wait(&v_empty[sv], ((j / C::NV) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
-          mbar_arrive_expect_tx(&v_full[sv], C::TILE);
-#pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_4d(&tm_v, &v_full[sv], sV + sv * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
-        }
+        it.cur += early;
+        load_keys(it, early, n);
       }
       __syncwarp();
     } else if (warp == 2 && DOC) {

@@ -132,7 +132,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (has1) r1 = p.q_ranges[b * p.Tq + qt0 + 1];
   }
 
-  if (threadIdx.x == 0) {
+  const int rt = p.tpt * p.g;
+  const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
+  // The loads of list entries j0 .. j1 - 1 (their tiles from `it`), for one thread.
+  auto load_q = [&]() {
+    const int tiles = has1 ? 2 : 1;
+    mbar_arrive_expect_tx(q_full, tiles * C::KB * rt * 128);
+    for (int t = 0; t < tiles; ++t)
+#pragma unroll
+      for (int kb = 0; kb < C::KB; ++kb)
+        tma_load_4d(&tm_q, q_full, sQ + t * C::TILE + kb * 16384, kb * 64, hk * p.g, (qt0 + t) * p.tpt, b);
+  };
+  auto load_kv = [&](TileIter& it, int j0, int j1) {
+    for (int j = j0; j < j1; ++j) {
+      const int s = j % C::NS;
+      const int kt = it.next();
+      if ((p.debug_flags & 1) && j == 0) continue;  // test knob: never deliver tile 0
+      if (j >= C::NS && !mbar_wait(&k_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+      mbar_arrive_expect_tx(&k_full[s], C::TILE);
+#pragma unroll
+      for (int kb = 0; kb < C::KB; ++kb)
+        tma_load_4d(&tm_k, &k_full[s], sK + s * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
+      if (j >= C::NS && !mbar_wait(&v_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
+      mbar_arrive_expect_tx(&v_full[s], C::TILE);
+#pragma unroll
+      for (int kb = 0; kb < C::KB; ++kb)
+        tma_load_4d(&tm_v, &v_full[s], sV + s * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
+    }
+  };
+  // without a document mask the list is known, and the first loads run beside the rest of the set-up
+  const int early = DOC ? 0 : max(0, min(hi - lo, C::NS));
+
+  if (warp == 1 && elect_one()) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
     mbar_init(q_full, 1);
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(&k_full[s], 1);
@@ -151,13 +185,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     count[0] = count[1] = count[2] = 0;
     fence_mbar_init();
+    if (early > 0) {
+      load_q();
+      TileIter it{nullptr, nullptr, lo, lo};
+      load_kv(it, 0, early);
+    }
   }
   if (warp == 0) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   // rows that no load writes (g does not divide 128) stay zero
-  const int rt = p.tpt * p.g;
   if (rt < 128) {
     for (int i = threadIdx.x; i < per * C::KB * (128 - rt) * 8; i += kThreads) {
       const int c = i & 7, row = rt + (i >> 3) % (128 - rt), blk = (i >> 3) / (128 - rt);
@@ -181,7 +219,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (n0 < 0) n0 = 0;
   if (single) n1 = n >> 1, n0 = n - n1;
   const TileIter first{DOC ? tiles.meet : nullptr, DOC ? tiles.meet2 : nullptr, lo, lo};
-  const WaitCtx wctx{abort_flag, p.status, p.wait_limit_ns};
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
@@ -326,31 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       // ---------------------------------------------------------------- TMA producer
       if (n > 0 && elect_one()) {
-        prefetch_tensormap(&tm_q);
-        prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
-        const int tiles = has1 ? 2 : 1;
-        mbar_arrive_expect_tx(q_full, tiles * C::KB * rt * 128);
-        for (int t = 0; t < tiles; ++t)
-#pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_4d(&tm_q, q_full, sQ + t * C::TILE + kb * 16384, kb * 64, hk * p.g, (qt0 + t) * p.tpt, b);
+        if (early == 0) load_q();
         TileIter it = first;
-        for (int j = 0; j < n; ++j) {
-          const int s = j % C::NS;
-          const int kt = it.next();
-          if ((p.debug_flags & 1) && j == 0) continue;  // test knob: never deliver tile 0
-          if (j >= C::NS && !mbar_wait(&k_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
-          mbar_arrive_expect_tx(&k_full[s], C::TILE);
-#pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_4d(&tm_k, &k_full[s], sK + s * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
-          if (j >= C::NS && !mbar_wait(&v_empty[s], ((j / C::NS) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
-          mbar_arrive_expect_tx(&v_full[s], C::TILE);
-#pragma unroll
-          for (int kb = 0; kb < C::KB; ++kb)
-            tma_load_4d(&tm_v, &v_full[s], sV + s * C::TILE + kb * 16384, kb * 64, hk, kt * 128, b);
-        }
+        it.cur += early;
+        load_kv(it, early, n);
       }
       __syncwarp();
     } else if (warp == 2 && DOC) {
