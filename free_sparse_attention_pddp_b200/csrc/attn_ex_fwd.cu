@@ -701,7 +701,9 @@ __global__ void __launch_bounds__(128) ex_doc_tiles(const ExTile p, int* k_ids, 
 // of request b is `per` query tiles (their key tiles) or, in the second CTA, one
 // key tile (its query tiles). A counting sort by one CTA: order[rank] = b jobs + i.
 __global__ void __launch_bounds__(1024) ex_doc_order(const ExTile p, int per, int* q_order, int* k_order) {
+  constexpr int kKept = 4096;  // jobs whose bins are kept from the first sweep for the second
   __shared__ int bins[4096 + 1];
+  __shared__ uint16_t kept[kKept];
   __shared__ int sums[32];
   const bool key = blockIdx.x == 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -736,7 +738,10 @@ __global__ void __launch_bounds__(1024) ex_doc_order(const ExTile p, int per, in
   };
   for (int at = warp; at < all; at += 32) {
     const int n = bin(at);
-    if (lane == 0) atomicAdd(&bins[n], 1);
+    if (lane == 0) {
+      atomicAdd(&bins[n], 1);
+      if (at < kKept) kept[at] = static_cast<uint16_t>(n);
+    }
   }
   __syncthreads();
   // exclusive sums of the bins, four to a thread (the last bin, empty jobs, comes after them)
@@ -765,7 +770,11 @@ __global__ void __launch_bounds__(1024) ex_doc_order(const ExTile p, int per, in
   __syncthreads();
   // Equal jobs land about in order (neighbours share their tiles in L2); the order decides when they run, not what
   // they compute.
-  for (int at = warp; at - warp < all; at += 32) {
+  for (int at = threadIdx.x; at - static_cast<int>(threadIdx.x) < min(all, kKept); at += 1024) {
+    if (at < min(all, kKept)) order[atomicAdd(&bins[kept[at]], 1)] = at;
+    __syncthreads();
+  }
+  for (int at = kKept + warp; at - warp < all; at += 32) {
     if (at < all) {
       const int n = bin(at);
       if (lane == 0) order[atomicAdd(&bins[n], 1)] = at;
