@@ -88,6 +88,20 @@ struct TileIter {
   }
 };
 
+// The entries of a forward CTA's K/V ring in order: one list of tiles or, zipped,
+// a's and b's tiles in turn for as long as both have some.
+struct EntryIter {
+  TileIter a, b;
+  int both;     // zipped: tiles of the shorter list, else 0
+  bool a_long;  // whose tiles remain
+  int i = 0;
+  __device__ __forceinline__ int next() {
+    const bool from_a = i < 2 * both ? !(i & 1) : a_long;
+    ++i;
+    return from_a ? a.next() : b.next();
+  }
+};
+
 // Document ids of a tile: smallest and largest id of its rows that are not
 // padding (an empty tile: INT_MAX, INT_MIN) and whether any row is padding.
 __device__ __forceinline__ bool docs_meet(int4 a, int4 b) { return a.x <= b.y && b.x <= a.y; }

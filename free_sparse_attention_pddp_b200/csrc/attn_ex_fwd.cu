@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kb = 0; kb < C::KB; ++kb)
         tma_load_4d(&tm_q, q_full, sQ + t * C::TILE + kb * 16384, kb * 64, hk * p.g, (qt0 + t) * p.tpt, b);
   };
-  auto load_kv = [&](TileIter& it, int j0, int j1) {
+  auto load_kv = [&](EntryIter& it, int j0, int j1) {
     for (int j = j0; j < j1; ++j) {
       const int s = j % C::NS;
       const int kt = it.next();
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     if (early > 0) {
       load_q();
-      TileIter it{nullptr, nullptr, lo, lo};
+      EntryIter it{TileIter{nullptr, nullptr, lo, lo}, TileIter{}, 0, true};
       load_kv(it, 0, early);
     }
   }
@@ -218,7 +218,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (n0 < 0) n0 = 0;
   if (single) n1 = n >> 1, n0 = n - n1;
-  const TileIter first{DOC ? tiles.meet : nullptr, DOC ? tiles.meet2 : nullptr, lo, lo};
+  // Two query tiles of different documents need different key tiles: beyond a fifth of them the slots go through their
+  // own lists side by side instead of waiting for each other in one.
+  const bool zip = DOC && !single && 4 * n > 5 * max(n0, n1) && min(n0, n1) > 0;
+  if (zip) n = n0 + n1;
+  const bool apart = single || zip;  // no tile serves both slots
+  const TileIter first{DOC ? tiles.meet : nullptr, DOC && !zip ? tiles.meet2 : nullptr, lo, lo};
+  const TileIter second{tiles.meet2, nullptr, lo, lo};
+  const EntryIter entries{first, second, zip ? min(n0, n1) : 0, !zip || n0 > n1};
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
@@ -257,17 +264,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = j % C::NS;
           return wait(&v_full[s], j / C::NS) && (!pad || wait(&v_ok[s], j / C::NS));
         };
-        TileIter it = first;
-        const int steps = single ? (n + 1) >> 1 : n;
+        TileIter it = first, it2 = second;
+        const int steps = single ? (n + 1) >> 1 : zip ? max(n0, n1) : n;
+        // the slots' list entries of a step
+        auto entry0 = [&](int step) { return single ? 2 * step : zip ? step + min(step, n1) : step; };
+        auto entry1 = [&](int step) { return single ? 2 * step + 1 : zip ? step + min(step + 1, n0) : step; };
         int i0 = 0, i1 = 0;     // the slots' steps
         int behind = -1;        // slot 1's list entry whose O += P V is to come
         bool behind_pad = false;
         bool ok = wait(q_full, 0);
         // step's slots (1, 2) and whether their V tiles hold padding (4, 8)
         auto look = [&](int step) {
-          const int j0 = single ? 2 * step : step, j1 = single ? j0 + 1 : j0;
+          const int j0 = entry0(step), j1 = entry1(step);
           int f = 0;
-          if (DOC) {
+          if (DOC && zip) {
+            if (step < n0) f |= tile_bit(tiles.pads, it.next() - lo) ? 5 : 1;
+            if (step < n1) f |= tile_bit(tiles.pads, it2.next() - lo) ? 10 : 2;
+          } else if (DOC) {
             if (j0 >= n) return 0;
             int kt = it.next() - lo;
             if (tile_bit(tiles.pads, kt)) f |= single ? 4 : 12;
@@ -287,14 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           // S of a step, then the products of the step before
           int prev = 0, o0 = 0, o1 = 0;
           for (int step = 0; ok && step <= steps; ++step) {
-            const int j0 = single ? 2 * step : step, j1 = single ? j0 + 1 : j0;
-            const int p0 = single ? j0 - 2 : j0 - 1, p1 = single ? j1 - 2 : j1 - 1;
+            const int j0 = entry0(step), j1 = entry1(step);
+            const int p0 = entry0(step - 1), p1 = entry1(step - 1);
             const int now = flags;
             if (now & 1) {
               if (!(ok = wait(&k_full[j0 % C::NS], j0 / C::NS) && (i0 == 0 || wait(&s_read[0], i0 - 1)))) break;
               tc_fence_after();
               issue_s(0, j0);
-              if (single || !(now & 2)) umma_commit(&k_empty[j0 % C::NS]);
+              if (apart || !(now & 2)) umma_commit(&k_empty[j0 % C::NS]);
               ++i0;
             }
             if (now & 2) {
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(ok = v_there(p0, prev & 4) && wait(&p_full[0], o0))) break;
               tc_fence_after();
               issue_o(0, o0, p0);
-              if (single || !(prev & 2)) umma_commit(&v_empty[p0 % C::NS]);
+              if (apart || !(prev & 2)) umma_commit(&v_empty[p0 % C::NS]);
               ++o0;
             }
             if (prev & 2) {
@@ -324,14 +337,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else
         // UMMAs run in order, so S_t(i + 1) overwrites P_t(i) only after the product that reads it
         for (int step = 0; ok && step <= steps; ++step) {
-          const int j0 = single ? 2 * step : step, j1 = single ? j0 + 1 : j0;
+          const int j0 = entry0(step), j1 = entry1(step);
           const int now = flags;
           const bool a0 = now & 1, a1 = now & 2, pad0 = now & 4, pad1 = now & 8;
           if (a0) {
             if (!(ok = wait(&k_full[j0 % C::NS], j0 / C::NS))) break;
             tc_fence_after();
             issue_s(0, j0);
-            if (single || !a1) umma_commit(&k_empty[j0 % C::NS]);
+            if (apart || !a1) umma_commit(&k_empty[j0 % C::NS]);
           }
           if (behind >= 0) {
             if (!(ok = v_there(behind, behind_pad) && wait(&p_full[1], i1 - 1))) break;
@@ -354,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = v_there(j0, pad0) && wait(&p_full[0], i0))) break;
             tc_fence_after();
             issue_o(0, i0, j0);
-            if (single || !a1) umma_commit(&v_empty[j0 % C::NS]);
+            if (apart || !a1) umma_commit(&v_empty[j0 % C::NS]);
             ++i0;
           }
         }
@@ -364,14 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- TMA producer
       if (n > 0 && elect_one()) {
         if (early == 0) load_q();
-        TileIter it = first;
-        it.cur += early;
+        EntryIter it = entries;
+        it.a.cur += early;
         load_kv(it, early, n);
       }
       __syncwarp();
     } else if (warp == 2 && DOC) {
       // ---------------------------------------------------------------- padded keys
-      TileIter it = first;
+      EntryIter it = entries;
       for (int j = 0; j < n; ++j) {
         const int s = j % C::NS;
         if (!mbar_wait_warp(&v_full[s], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;

@@ -321,3 +321,15 @@ def test_a_load_that_never_arrives_is_reported(mcs, docs, d):
         debug_set_flags(0)
     again = run(mcs, shape, q, k, v, d_o, **ids)
     assert all(torch.equal(again[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [1, 2])
+def test_neighbouring_query_tiles_of_different_documents(mcs, g, d):
+    """Pairs of query tiles whose documents need different keys, of equal and of very different number, with padding
+    between and inside them."""
+    for lengths in ([128, 900, 128, 300], [500, 140, 500, 30, 400], [256] * 6):
+        ids = torch.cat([torch.full((n,), i if n != 30 else -1) for i, n in enumerate(lengths)])[None].int()
+        ids[0, 200:203] = -1
+        N = ids.shape[1]
+        both(mcs, 1, 2 * g, 2, N, N, d, doc_q=ids, doc_k=ids, cap=30.0 * (g - 1), seed=N + g)
