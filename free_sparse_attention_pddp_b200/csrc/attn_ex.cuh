@@ -68,12 +68,33 @@ __device__ __forceinline__ void named_barrier_sync() {
   asm volatile("barrier.sync %0, %1;" ::"n"(ID), "n"(NTHREADS) : "memory");
 }
 
-// Tiles from `cur` on in order; with bitmaps, those that are in one of them
-// (bit 0 of word 0 is tile `base`).
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ float2 lds_pair(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_pair(uint32_t addr, float x, float y) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+
+// Tiles from `cur` on in order; with bitmaps (shared-memory addresses), those
+// that are in one of them (bit 0 of word 0 is tile `base`).
 struct TileIter {
-  const uint32_t *bits, *bits2;  // null: every tile, no second bitmap
+  uint32_t bits, bits2;  // 0: every tile, no second bitmap
   int cur, base;
-  __device__ __forceinline__ uint32_t word(int w) const { return bits2 ? bits[w] | bits2[w] : bits[w]; }
+  __device__ __forceinline__ uint32_t word(int w) const {
+    return bits2 ? lds32(bits + w * 4) | lds32(bits2 + w * 4) : lds32(bits + w * 4);
+  }
   __device__ __forceinline__ int next() {
     if (!bits) return cur++;
     int i = cur - base;
@@ -114,9 +135,9 @@ __device__ __forceinline__ bool docs_same(int4 a, int4 b) {  // every pair of ro
 // one is valid, and those with padding. `two`: for two tiles at once, the second
 // one's bitmaps behind the first one's.
 struct TileBits {
-  uint32_t *meet, *whole, *pads, *meet2, *whole2;
-  __device__ __forceinline__ TileBits(uint32_t* at, int tiles) {
-    const int w = (tiles + 31) >> 5;
+  uint32_t meet, whole, pads, meet2, whole2;  // shared-memory addresses
+  __device__ __forceinline__ TileBits(uint32_t at, int tiles) {
+    const int w = ((tiles + 31) >> 5) * 4;
     meet = at;
     whole = at + w;
     pads = at + 2 * w;
@@ -140,12 +161,12 @@ struct TileBits {
         a2 = __ballot_sync(0xffffffffu, docs_same(r, mine2));
       }
       if (lane == 0) {
-        meet[w] = m;
-        whole[w] = a;
-        pads[w] = z;
+        sts32(meet + w * 4, m);
+        sts32(whole + w * 4, a);
+        sts32(pads + w * 4, z);
         if (TWO) {
-          meet2[w] = m2;
-          whole2[w] = a2;
+          sts32(meet2 + w * 4, m2);
+          sts32(whole2 + w * 4, a2);
         }
         atomicAdd(&counts[0], __popc(m | m2));  // whole-number sums: their order is free
         atomicAdd(&counts[1], __popc(m));
@@ -155,7 +176,7 @@ struct TileBits {
     __syncthreads();
   }
 };
-__device__ __forceinline__ bool tile_bit(const uint32_t* bits, int i) { return (bits[i >> 5] >> (i & 31)) & 1u; }
+__device__ __forceinline__ bool tile_bit(uint32_t bits, int i) { return (lds32(bits + (i >> 5) * 4) >> (i & 31)) & 1u; }
 
 // s[c] <- cap log2(e) tanh(k s[c]), the capped score in log2 units, in place.
 // |k s| <= 0.625: s Q(s^2) with Q from x + x z P(z), z = x^2, P of degree 3

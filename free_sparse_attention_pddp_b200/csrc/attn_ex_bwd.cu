@@ -222,7 +222,6 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* count = reinterpret_cast<int*>(tmem_slot + 2);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform to the compiler too
   const int lane = threadIdx.x & 31;
@@ -336,7 +335,7 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
     fence_mbar_init();
     if (early > 0) {
       load_resident();
-      TileIter it{nullptr, nullptr, lo, lo};
+      TileIter it{0u, 0u, lo, lo};
       load_queries(it, 0, early);
     }
   }
@@ -357,12 +356,12 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int n = hi - lo;
-  TileBits tiles(bits, p.Tq);
+  TileBits tiles(smem_u32(smem + C::OFF_BITS), p.Tq);
   if (DOC) {
     tiles.build<false>(count, p.q_ranges + static_cast<size_t>(b) * p.Tq, lo, hi, mine, none);
     n = count[0];
   }
-  const TileIter first{DOC ? tiles.meet : nullptr, nullptr, lo, lo};
+  const TileIter first{DOC ? tiles.meet : 0u, 0u, lo, lo};
 
   if (warp < 4) {
     if (warp == 0) {
@@ -663,7 +662,6 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* count = reinterpret_cast<int*>(tmem_slot + 2);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
@@ -748,7 +746,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
     fence_mbar_init();
     if (early > 0) {
       load_resident();
-      TileIter it{nullptr, nullptr, 0, 0};
+      TileIter it{0u, 0u, 0, 0};
       load_keys(it, 0, early);
     }
   }
@@ -765,12 +763,12 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int n = hi;
-  TileBits tiles(bits, p.Tk);
+  TileBits tiles(smem_u32(smem + C::OFF_BITS), p.Tk);
   if (DOC) {
     tiles.build<false>(count, p.k_ranges + static_cast<size_t>(b) * p.Tk, 0, hi, mine, none);
     n = count[0];
   }
-  const TileIter first{DOC ? tiles.meet : nullptr, nullptr, 0, 0};
+  const TileIter first{DOC ? tiles.meet : 0u, 0u, 0, 0};
   // TMEM: S | dP 0 | dQ | dP 1
   auto dp_buf = [&](int i) { return tmem + ((i & 1) ? 384u : 128u); };
 

@@ -85,8 +85,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* count = reinterpret_cast<int*>(tmem_slot + 2);
-  float2* row_max = reinterpret_cast<float2*>(smem + C::OFF_MAX);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform to the compiler too
   const int lane = threadIdx.x & 31;
@@ -187,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     if (early > 0) {
       load_q();
-      EntryIter it{TileIter{nullptr, nullptr, lo, lo}, TileIter{}, 0, true};
+      EntryIter it{TileIter{0u, 0u, lo, lo}, TileIter{}, 0, true};
       load_kv(it, 0, early);
     }
   }
@@ -208,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // key tiles of this CTA and of its slots; the CTA's list holds what either slot needs
-  TileBits tiles(bits, p.Tk);
+  TileBits tiles(smem_u32(smem + C::OFF_BITS), p.Tk);
   int n = hi - lo, n0 = min(hi, T0) - lo, n1 = has1 ? n : 0;
   if (DOC) {
     tiles.build<true>(count, p.k_ranges + static_cast<size_t>(b) * p.Tk, lo, hi, r0, r1);
@@ -223,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool zip = DOC && !single && 4 * n > 5 * max(n0, n1) && min(n0, n1) > 0;
   if (zip) n = n0 + n1;
   const bool apart = single || zip;  // no tile serves both slots
-  const TileIter first{DOC ? tiles.meet : nullptr, DOC && !zip ? tiles.meet2 : nullptr, lo, lo};
-  const TileIter second{tiles.meet2, nullptr, lo, lo};
+  const TileIter first{DOC ? tiles.meet : 0u, DOC && !zip ? tiles.meet2 : 0u, lo, lo};
+  const TileIter second{tiles.meet2, 0u, lo, lo};
   const EntryIter entries{first, second, zip ? min(n0, n1) : 0, !zip || n0 > n1};
 
   if (warp < 4) {
@@ -419,17 +417,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int pos = p.lens ? p.P + min(max(row_valid ? p.lens[tok] : 0, 0), p.C) - 1 : off + tok;
     const int lim = limit(pos) - half * 64;
     const int lim_all = limit(off + qt * p.tpt);  // keys that every row of the tile sees
-    const uint32_t* whole = t == 0 || single ? tiles.whole : tiles.whole2;
+    const uint32_t whole = t == 0 || single ? tiles.whole : tiles.whole2;
     int my_doc = DOC && row_valid ? p.doc_q[static_cast<size_t>(b) * p.Nq + tok] : -2;
     if (my_doc < 0) my_doc = -2;  // a padded query matches no key
     const float mul = p.mul;  // what turns a score into log2 units
     const float slope = BIAS && row_valid ? p.slopes[head] * kLog2e / mul : 0.f;
     const uint64_t mul2 = f2_pack(mul, mul);
-    float2* my_max = row_max + (t * 2 + half) * 128 + row;
-    const float2* other_max = row_max + (t * 2 + (half ^ 1)) * 128 + row;
+    // the words of this row and half, and of the other half
+    const uint32_t my_max = smem_u32(smem + C::OFF_MAX) + ((t * 2 + half) * 128 + row) * 8;
+    const uint32_t other_max = smem_u32(smem + C::OFF_MAX) + ((t * 2 + (half ^ 1)) * 128 + row) * 8;
     const int pair_bar = 2 + t * 4 + wq;  // the two warps that share these rows
     TileIter it = first;
-    if (DOC && !single) it = TileIter{t == 0 ? tiles.meet : tiles.meet2, nullptr, lo, lo};
+    if (DOC && !single) it = TileIter{t == 0 ? tiles.meet : tiles.meet2, 0u, lo, lo};
     if (single && t == 1 && nt > 0) it.next();
     float m = -CUDART_INF_F;  // running max, log2 units (the same in both halves)
     float l = 0.f;            // this half's sum
@@ -484,9 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float half_max = fmaf(fmaxf(fmax3(mc[0], mc[1], mc[2]), mc[3]), mul, shift);
       // Both warps meet here in every step, with the step's own word on whether their waits held, and leave the loop
       // in the same step if one did not.
-      my_max[(i & 1) * 512] = make_float2(half_max, ok ? 0.f : 1.f);
+      sts_pair(my_max + (i & 1) * 4096, half_max, ok ? 0.f : 1.f);
       asm volatile("barrier.sync %0, 64;" ::"r"(pair_bar) : "memory");
-      const float2 other = other_max[(i & 1) * 512];
+      const float2 other = lds_pair(other_max + (i & 1) * 4096);
       ok = ok && other.y == 0.f;
       if (!ok) break;
       const float mx = fmaxf(half_max, other.x);
@@ -554,10 +553,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool fin = ok && (nt == 0 || mbar_wait_warp(&p_empty[t], (nt - 1) & 1, wctx, MCS_WHERE_ATTN_EPILOGUE));
     // the row's sum: both halves', exchanged like the maxima (every warp takes part, whatever happened)
     // a loop left early wrote the other parity's words
-    my_max[(nt & 1) * 512] = make_float2(l, 0.f);
+    sts_pair(my_max + (nt & 1) * 4096, l, 0.f);
     asm volatile("barrier.sync %0, 64;" ::"r"(pair_bar) : "memory");
-    l += other_max[(nt & 1) * 512].x;
+    l += lds_pair(other_max + (nt & 1) * 4096).x;
     if (fin && (t == 0 || single || has1)) {
+      // the row's place again (hidden from the compiler, which would hold it in registers through the loop)
+      int row2 = row;
+      asm volatile("" : "+r"(row2));
+      const int tok = qt * p.tpt + row2 / p.g, head = hk * p.g + row2 % p.g;
+      const bool row_valid = row2 < rt && tok < p.Nq;
       tc_fence_after();
       const bool partial = p.part_o != nullptr;
       const float inv = l > 0.f ? 1.f / l : 0.f;
