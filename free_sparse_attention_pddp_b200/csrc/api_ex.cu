@@ -95,29 +95,41 @@ ExParams ex_params(const mcs_attn_shape* s, const mcs_attn_opts* o) {
 
 // How the forward fills the GPU: tiles, key splits and the order of work.
 struct FwdPlan {
-  int tpt, Tq, Tk, single, nsplit, parts, chunk;
+  int tpt, Tq, Tk, single, nsplit, chunk;
 };
 
 constexpr int kSms = 148;
 
-// Few query tiles and an odd number of them (a pair would leave a slot without
-// work), at least four key tiles: both slots of a CTA take one query tile and
-// half of its keys. While a wave has room, the keys are split further, to one
-// tile per slot; a second launch joins the parts (about 4 us, two key tiles'
-// time).
+// A CTA takes two query tiles that share their key tiles, or one (single), half
+// of its keys to each slot. While a wave has room the keys are split further and
+// a second launch joins the parts, in about three steps' time (a step, one key
+// tile per slot, takes 2 us). The shorter of the two counts of steps wins: with 8
+// heads of 1024 tokens, d = 128, single takes 15.7 us where pairs take 20.7.
+// Pairs win a tie, since they read K and V half as often: 12 heads of 390
+// queries over 32760 keys take 98.5 us in pairs, 101.6 single. Beyond one wave
+// and five query tiles a head, waves blend into one another and pairs lose
+// nothing.
+constexpr int kJoinSteps = 3;
+
 FwdPlan fwd_plan(int B, int Hkv, int g, int Nq, int Nk, int d) {
   FwdPlan f;
   f.tpt = 128 / g;
   f.Tq = (Nq + f.tpt - 1) / f.tpt;
   f.Tk = (Nk + 127) / 128;
-  f.single = f.Tq <= 5 && f.Tq % 2 == 1 && f.Tk >= 4;
-  const long long ctas = static_cast<long long>(B) * Hkv * (f.single ? f.Tq : (f.Tq + 1) / 2);
-  f.nsplit = 1;
-  if (2 * ctas <= kSms && f.Tk >= (f.single ? 4 : 6)) {
-    const long long most = f.Tk / (f.single ? 2 : 1);
-    f.nsplit = static_cast<int>(std::max(1ll, std::min(kSms / ctas, most)));
-  }
-  f.parts = f.nsplit * (f.single ? 2 : 1);
+  const long long heads = static_cast<long long>(B) * Hkv;
+  // steps of the slowest SM, and the splits that lead there
+  auto cost = [&](bool single, int* nsplit) {
+    const long long ctas = heads * (single ? f.Tq : (f.Tq + 1) / 2);
+    const int steps = single ? (f.Tk + 1) / 2 : f.Tk;
+    *nsplit = static_cast<int>(std::max(1ll, std::min<long long>(kSms / ctas, steps)));
+    const int each = (steps + *nsplit - 1) / *nsplit;
+    if (steps - each < kJoinSteps) *nsplit = 1;
+    return (ctas * *nsplit + kSms - 1) / kSms * (*nsplit > 1 ? each + kJoinSteps : steps);
+  };
+  int one = 1;
+  const long long pairs = cost(false, &f.nsplit);
+  f.single = (heads * f.Tq <= kSms || f.Tq <= 5) && cost(true, &one) < pairs;
+  if (f.single) f.nsplit = one;
   // K and V of a chunk's heads take half of the 126 MB L2 at most
   const size_t head = static_cast<size_t>(Nk) * d * 4;
   const long long fit = static_cast<long long>((size_t(64) << 20) / head);
@@ -142,7 +154,7 @@ FwdWs fwd_layout(const FwdPlan& f, int B, int Hkv, int d) {
   w.k_ranges = take(static_cast<size_t>(B) * f.Tk * 16);
   w.q_ranges = take(static_cast<size_t>(B) * f.Tq * 16);
   w.order = take(static_cast<size_t>(B) * f.Tq * 4);
-  const size_t rows = f.parts > 1 ? static_cast<size_t>(f.parts) * B * Hkv * f.Tq * 128 : 0;
+  const size_t rows = f.nsplit > 1 ? static_cast<size_t>(f.nsplit) * B * Hkv * f.Tq * 128 : 0;
   w.part_lse = take(rows * 4);
   w.part_o = take(rows * d * 4);
   w.total = off;
@@ -262,7 +274,7 @@ DecodeWs decode_layout(const DecodePlan& f, const mcs_decode_shape* s) {
   };
   const bool parts = (f.nsplit > 1 && !f.cluster) || s->P > 0;
   const size_t rows = parts ? static_cast<size_t>(s->B) * s->Hq * f.nsplit : 0;
-  const size_t pre = s->P > 0 ? static_cast<size_t>(f.pre.parts) * s->Hkv * f.pre.Tq * 128 : 0;
+  const size_t pre = s->P > 0 ? static_cast<size_t>(f.pre.nsplit) * s->Hkv * f.pre.Tq * 128 : 0;
   w.part_lse = take(rows * 4);
   w.part_o = take(rows * s->d * 4);
   w.pre_lse = take(pre * 4);
@@ -326,7 +338,7 @@ mcs_status decode_call(const mcs_decode_shape* s, const void* q, const void* kp,
     if (launch_ex_fwd(s->d, &tq, &tk, &tv, t, stream) != cudaSuccess) return MCS_ERR_CUDA;
     p.pre_lse = t.part_lse;
     p.pre_o = t.part_o;
-    p.pre_parts = f.pre.parts;
+    p.pre_parts = f.pre.nsplit;
     p.pre_tiles = f.pre.Tq;
     p.pre_tpt = f.pre.tpt;
   }
@@ -386,12 +398,12 @@ mcs_status mcs_dense_ex(const mcs_attn_shape* s, const mcs_attn_opts* opts, cons
       t.order = order;
     }
   }
-  if (f.parts > 1) {
+  if (f.nsplit > 1) {
     t.part_lse = reinterpret_cast<float*>(base + w.part_lse);
     t.part_o = reinterpret_cast<float*>(base + w.part_o);
   }
   if (launch_ex_fwd(s->d, &tq, &tk, &tv, t, stream) != cudaSuccess) return MCS_ERR_CUDA;
-  return f.parts > 1 ? ok_or_cuda(launch_ex_combine(s->d, t, f.parts, stream)) : MCS_OK;
+  return f.nsplit > 1 ? ok_or_cuda(launch_ex_combine(s->d, t, f.nsplit, stream)) : MCS_OK;
 }
 
 mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, const void* q, const void* k,

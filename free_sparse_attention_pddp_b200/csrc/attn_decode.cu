@@ -271,21 +271,20 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat[w * MT * 16 + r].x);
     float L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M > -CUDART_INF_F) {
+    const float top = top_or_zero(M);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 st = stat[w * MT * 16 + r];
-        const float f = fast_exp2(st.x - M);
-        const float4 v = *reinterpret_cast<const float4*>(out + (w * MT * 16 + r) * (D + 4) + c);
-        L = fmaf(f, st.y, L);
-        a.x = fmaf(f, v.x, a.x);
-        a.y = fmaf(f, v.y, a.y);
-        a.z = fmaf(f, v.z, a.z);
-        a.w = fmaf(f, v.w, a.w);
-      }
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 st = stat[w * MT * 16 + r];
+      const float f = fast_exp2(st.x - top);
+      const float4 v = *reinterpret_cast<const float4*>(out + (w * MT * 16 + r) * (D + 4) + c);
+      L = fmaf(f, st.y, L);
+      a.x = fmaf(f, v.x, a.x);
+      a.y = fmaf(f, v.y, a.y);
+      a.z = fmaf(f, v.z, a.z);
+      a.w = fmaf(f, v.w, a.w);
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    const float lse2 = L > 0.f ? M + log2f(L) : -CUDART_INF_F;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float lse2 = L == 0.f ? -CUDART_INF_F : M + log2f(L);
     a.x *= inv, a.y *= inv, a.z *= inv, a.w *= inv;
     if (p.cluster) {
       // over the merged warps' own sums: this thread has read what it overwrites, and the other threads of the row
@@ -325,18 +324,18 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         if (ls[k] == -CUDART_INF_F) continue;
-        const float f = fast_exp2(ls[k] - M);
+        const float f = fast_exp2(ls[k] - top_or_zero(M));
         L += f;
         a.x = fmaf(f, v[k].x, a.x);
         a.y = fmaf(f, v[k].y, a.y);
         a.z = fmaf(f, v[k].z, a.z);
         a.w = fmaf(f, v[k].w, a.w);
       }
-      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const float inv = L == 0.f ? 0.f : 1.f / L;
       const size_t at = static_cast<size_t>(b) * p.Hq + head0 + r;
       *reinterpret_cast<uint2*>(p.o + at * D + c) =
           make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-      if (c == 0 && p.lse) p.lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : -CUDART_INF_F;
+      if (c == 0 && p.lse) p.lse[at] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
   }
@@ -380,8 +379,7 @@ __global__ void __launch_bounds__(256) decode_combine(const DecodeParams p) {
       }
     }
     const float mn = fmaxf(m, fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3])));
-    if (mn == -CUDART_INF_F) continue;
-    const float a = fast_exp2(m - mn);
+    const float top = top_or_zero(mn), a = fast_exp2(m - top);
     m = mn;
     l *= a;
 #pragma unroll
@@ -389,7 +387,7 @@ __global__ void __launch_bounds__(256) decode_combine(const DecodeParams p) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (ls[k] == -CUDART_INF_F) continue;
-      const float w = fast_exp2(ls[k] - m);
+      const float w = fast_exp2(ls[k] - top);
       l += w;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[k][e], o[e]);
@@ -403,18 +401,17 @@ __global__ void __launch_bounds__(256) decode_combine(const DecodeParams p) {
     float M = -CUDART_INF_F;
     for (int w = 0; w < warps; ++w) M = fmaxf(M, s_m[w]);
     float L = 0.f, a[E] = {};
-    if (M > -CUDART_INF_F)
-      for (int w = 0; w < warps; ++w) {
-        const float f = fast_exp2(s_m[w] - M);
-        L = fmaf(f, s_l[w], L);
+    for (int w = 0; w < warps; ++w) {
+      const float f = fast_exp2(s_m[w] - top_or_zero(M));
+      L = fmaf(f, s_l[w], L);
 #pragma unroll
-        for (int e = 0; e < E; ++e) a[e] = fmaf(f, s_o[w][lane * E + e], a[e]);
-      }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+      for (int e = 0; e < E; ++e) a[e] = fmaf(f, s_o[w][lane * E + e], a[e]);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + static_cast<size_t>(blockIdx.x) * D + lane * E);
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(a[e] * inv, a[e + 1] * inv);
-    if (lane == 0 && p.lse) p.lse[blockIdx.x] = L > 0.f ? (M + log2f(L)) * kLn2 : -CUDART_INF_F;
+    if (lane == 0 && p.lse) p.lse[blockIdx.x] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
   }
 }
 

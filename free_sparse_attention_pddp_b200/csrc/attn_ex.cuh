@@ -87,6 +87,10 @@ __device__ __forceinline__ void sts_pair(uint32_t addr, float x, float y) {
   asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
 }
 
+// What a maximum of -inf is counted from: the weights of parts that saw no key
+// are 2^-inf = 0, and NaN sums come through.
+__device__ __forceinline__ float top_or_zero(float m) { return m == -CUDART_INF_F ? 0.f : m; }
+
 // Tiles from `cur` on in order; with bitmaps (shared-memory addresses), those
 // that are in one of them (bit 0 of word 0 is tile `base`).
 struct TileIter {

@@ -11,8 +11,9 @@
 // products. Two ways to fill the slots:
 //   pair    two consecutive query tiles that share every key tile;
 //   single  one query tile whose even key tiles go to slot 0 and odd ones to
-//           slot 1 (few rows over many keys); the halves are joined by
-//           ex_combine like any other split of the keys.
+//           slot 1 (few rows over many keys); slot 0 joins the halves at the end
+//           through shared memory. With (m, l, O) of each slot, m = max(m0, m1):
+//           l = sum_t l_t 2^(m_t - m), O = sum_t O_t 2^(m_t - m).
 //
 // TMEM (512 columns): S_0 | S_1 (128 each) | O_0 | O_1 (D each). P_t (bf16
 // pairs, the TS-form A operand of O_t += P_t V) overwrites S_t where d = 128. With
@@ -556,7 +557,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     sts_pair(my_max + (nt & 1) * 4096, l, 0.f);
     asm volatile("barrier.sync %0, 64;" ::"r"(pair_bar) : "memory");
     l += lds_pair(other_max + (nt & 1) * 4096).x;
-    if (fin && (t == 0 || single || has1)) {
+    // One query tile for both slots: slot 1 hands its sums over in the K/V ring, which nobody reads any more once both
+    // slots' last products are done, and slot 0 joins them. Every warp takes part, whatever happened.
+    float* handed = reinterpret_cast<float*>(smem + C::OFF_K) + half * (D / 2) * 128 + row;  // [column][row]
+    const bool join = single && n1 > 0;
+    if (join) {
+      named_barrier_sync<10, 512>();
+      if (t == 1) {
+        sts_pair(my_max, m, l);
+        tc_fence_after();
+#pragma unroll
+        for (int cc = 0; cc < D / 64; ++cc) {
+          float ov[32];
+          tmem_ld32(tO + cc * 32, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) handed[(cc * 32 + e) * 128] = ov[e];
+        }
+      }
+      named_barrier_sync<10, 512>();
+    }
+    if (fin && (t == 0 || has1)) {
       // the row's place again (hidden from the compiler, which would hold it in registers through the loop)
       int row2 = row;
       asm volatile("" : "+r"(row2));
@@ -564,10 +585,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool row_valid = row2 < rt && tok < p.Nq;
       tc_fence_after();
       const bool partial = p.part_o != nullptr;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? m + log2f(l) : -CUDART_INF_F;
+      float w0 = 1.f, w1 = 0.f;
+      if (join) {
+        const float2 ml = lds_pair(my_max + 2 * 128 * 8);  // slot 1's
+        const float both = fmaxf(m, ml.x), top = top_or_zero(both);
+        w0 = fast_exp2(m - top);
+        w1 = fast_exp2(ml.x - top);
+        l = l * w0 + ml.y * w1;
+        m = both;
+      }
+      const float inv = l == 0.f ? 0.f : w0 / l, inv1 = l == 0.f ? 0.f : w1 / l;
+      const float lse2 = l == 0.f ? -CUDART_INF_F : m + log2f(l);
       const size_t bht = static_cast<size_t>(bh) * p.Tq + qt;
-      const size_t slice = static_cast<size_t>(single ? 2 * split + t : split) * BH * p.Tq;
+      const size_t slice = static_cast<size_t>(split) * BH * p.Tq;
       if (row_valid && half == 0) {
         if (partial) p.part_lse[(slice + bht) * 128 + row] = lse2;
         else if (p.lse) p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok] = lse2 * kLn2;
@@ -583,7 +613,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!row_valid) continue;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) ov[e] = l > 0.f ? ov[e] * inv : 0.f;
+        for (int e = 0; e < 32; ++e) ov[e] = l == 0.f ? 0.f : ov[e] * inv;
+        if (join) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = l == 0.f ? 0.f : fmaf(handed[(cc * 32 + e) * 128], inv1, ov[e]);
+        }
         if (partial) {
           float4* d4 = reinterpret_cast<float4*>(prow + cc * 32);
 #pragma unroll
@@ -660,8 +694,7 @@ __global__ void __launch_bounds__(128) ex_combine(const ExTile p, int parts) {
       }
     }
     const float mn = fmaxf(m, fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3])));
-    if (mn == -CUDART_INF_F) continue;
-    const float a = fast_exp2(m - mn);
+    const float top = top_or_zero(mn), a = fast_exp2(m - top);
     m = mn;
     l *= a;
 #pragma unroll
@@ -669,18 +702,18 @@ __global__ void __launch_bounds__(128) ex_combine(const ExTile p, int parts) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (ls[k] == -CUDART_INF_F) continue;
-      const float w = fast_exp2(ls[k] - m);
+      const float w = fast_exp2(ls[k] - top);
       l += w;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[k][e], o[e]);
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + static_cast<size_t>(r) * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
   if (p.lse && lane == 0)
-    p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+    p.lse[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }
 
 // Document ids as the tiles read them. Key tiles: ids of 128 keys (-1 past Nk and

@@ -166,6 +166,20 @@ def test_a_batch_does_not_read_its_neighbour(mcs):
         attn_ref.check(r[name][:1], want[name], name)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Hq,Hkv,Nq,Nk", [(2, 2, 100, 90), (4, 2, 300, 300), (2, 2, 130, 5000), (40, 40, 700, 256)])
+def test_a_bad_query_shows_in_its_row_alone(mcs, Hq, Hkv, Nq, Nk, bad):
+    """One slot, both slots with one tile, split keys, both slots with tiles of their own."""
+    q, k, v, _ = inputs(1, Hq, Hkv, Nq, Nk, 64, seed=22)
+    shape = mcs.AttnShape(1, Hq, Hkv, Nq, Nk, 64)
+    good = run(mcs, shape, q, k, v)
+    q[0, 77, 1, 5] = bad
+    r = run(mcs, shape, q, k, v)
+    assert r["o"][0, 77, 1].isnan().all() and r["lse"][0, 1, 77].isnan()
+    r["o"][0, 77, 1], r["lse"][0, 1, 77] = good["o"][0, 77, 1], good["lse"][0, 1, 77]
+    assert torch.equal(r["o"], good["o"]) and torch.equal(r["lse"], good["lse"])
+
+
 def test_scale_and_large_scores(mcs):
     both(mcs, 1, 2, 2, 100, 300, 64, scale=1.0, gain=1.0, seed=13)
     both(mcs, 1, 2, 2, 100, 300, 64, scale=1e-4, gain=1.0, seed=14)

@@ -92,6 +92,32 @@ def test_cache_behind_the_last_key_may_hold_anything(mcs, junk, P):
     run(mcs, 3, 8, 2, 200, 128, [1, 70, 199], P=P, junk=junk, seed=4)
 
 
+@pytest.mark.parametrize("B,C,P", [(200, 40, 0), (1, 400, 0), (3, 60000, 0), (3, 40, 130)])
+def test_a_bad_query_shows_in_its_row_alone(mcs, B, C, P):
+    """Whole requests, chunks joined within a cluster and by a second launch, a shared prefix."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q, k, v = rand(g, B, 8, 64), rand(g, B, C, 2, 64), rand(g, B, C, 2, 64)
+    kp, vp = rand(g, P or 1, 2, 64), rand(g, P or 1, 2, 64)
+    lens = torch.full((B,), C, dtype=torch.int32, device="cuda")
+    shape = mcs.DecodeShape(B, 8, 2, C, 64, P=P)
+    ws = mcs.decode_workspace(shape)
+
+    def call():
+        o, lse = torch.empty_like(q), torch.empty(B, 8, device="cuda")
+        if P:
+            mcs.mcs_decode_shared(shape, q, kp, vp, k, v, lens, o, lse, ws)
+        else:
+            mcs.mcs_decode(shape, q, k, v, lens, o, lse, ws)
+        return o, lse
+
+    good = call()
+    q[0, 3, 9] = float("nan")
+    o, lse = call()
+    assert o[0, 3].isnan().all() and lse[0, 3].isnan()
+    o[0, 3], lse[0, 3] = good[0][0, 3], good[1][0, 3]
+    assert torch.equal(o, good[0]) and torch.equal(lse, good[1])
+
+
 @pytest.mark.parametrize("P", [0, 64])
 def test_a_length_out_of_range_is_reported_and_bounded(mcs, P):
     run(mcs, 3, 4, 2, 50, 64, [12, 51, -3], P=P, junk=0.5, seed=5, status=5)
