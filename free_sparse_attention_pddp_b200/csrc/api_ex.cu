@@ -139,7 +139,7 @@ FwdPlan fwd_plan(int B, int Hkv, int g, int Nq, int Nk, int d) {
 
 // workspace: status | document tiles | partials of the key splits
 struct FwdWs {
-  size_t k_ids, k_ranges, q_ranges, order, part_lse, part_o, total;
+  size_t k_ids, k_ranges, q_ranges, order, counts, part_lse, part_o, total;
 };
 
 FwdWs fwd_layout(const FwdPlan& f, int B, int Hkv, int d) {
@@ -153,7 +153,8 @@ FwdWs fwd_layout(const FwdPlan& f, int B, int Hkv, int d) {
   w.k_ids = take(static_cast<size_t>(B) * f.Tk * 512);
   w.k_ranges = take(static_cast<size_t>(B) * f.Tk * 16);
   w.q_ranges = take(static_cast<size_t>(B) * f.Tq * 16);
-  w.order = take(static_cast<size_t>(B) * f.Tq * 4);
+  w.order = take(static_cast<size_t>(B) * f.Tq * 4 + 4);
+  w.counts = take(static_cast<size_t>(B) * f.Tq * 16);
   const size_t rows = f.nsplit > 1 ? static_cast<size_t>(f.nsplit) * B * Hkv * f.Tq * 128 : 0;
   w.part_lse = take(rows * 4);
   w.part_o = take(rows * d * 4);
@@ -163,7 +164,7 @@ FwdWs fwd_layout(const FwdPlan& f, int B, int Hkv, int d) {
 
 // workspace: status | document tiles | statistics of the packed rows
 struct BwdWs {
-  size_t k_ids, k_ranges, q_ids, q_ranges, order, k_order, stats, part_kv, total;
+  size_t k_ids, k_ranges, q_ids, q_ranges, order, k_order, counts, stats, part_kv, total;
   int kv_splits;
 };
 
@@ -194,8 +195,9 @@ BwdWs bwd_layout(const FwdPlan& f, int B, int Hkv, int Nk, int d) {
   w.k_ranges = take(static_cast<size_t>(B) * f.Tk * 16);
   w.q_ids = take(static_cast<size_t>(B) * f.Tq * 512);
   w.q_ranges = take(static_cast<size_t>(B) * f.Tq * 16);
-  w.order = take(static_cast<size_t>(B) * f.Tq * 4);
-  w.k_order = take(static_cast<size_t>(B) * f.Tk * 4);
+  w.order = take(static_cast<size_t>(B) * f.Tq * 4 + 4);
+  w.k_order = take(static_cast<size_t>(B) * f.Tk * 4 + 4);
+  w.counts = take(static_cast<size_t>(B) * (f.Tq + f.Tk) * 16);
   w.stats = take(static_cast<size_t>(B) * Hkv * f.Tq * 1024);
   w.kv_splits = kv_splits(f, B, Hkv);
   w.part_kv = take(w.kv_splits > 1 ? static_cast<size_t>(w.kv_splits) * 2 * B * Nk * Hkv * d * 4 : 0);
@@ -392,9 +394,10 @@ mcs_status mcs_dense_ex(const mcs_attn_shape* s, const mcs_attn_opts* opts, cons
     t.k_ranges = kr;
     t.q_ranges = qr;
     // with more jobs than SMs their order matters
-    if (!f.single && static_cast<long long>(p.B) * p.Hkv * ((f.Tq + 1) / 2) > kSms) {
+    if (static_cast<long long>(p.B) * p.Hkv * (f.single ? f.Tq : (f.Tq + 1) / 2) > kSms) {
       int* order = reinterpret_cast<int*>(base + w.order);
-      if (launch_ex_doc_order(t, 2, order, nullptr, stream) != cudaSuccess) return MCS_ERR_CUDA;
+      int4* counts = reinterpret_cast<int4*>(base + w.counts);
+      if (launch_ex_doc_order(t, f.single ? 1 : 2, counts, order, nullptr, stream) != cudaSuccess) return MCS_ERR_CUDA;
       t.order = order;
     }
   }
@@ -454,7 +457,8 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
     if (static_cast<long long>(p.B) * p.Hkv * std::max(f.Tq, f.Tk) > kSms) {
       int* order = reinterpret_cast<int*>(base + w.order);
       int* k_order = reinterpret_cast<int*>(base + w.k_order);
-      if (launch_ex_doc_order(t, 1, order, k_order, stream) != cudaSuccess) return MCS_ERR_CUDA;
+      int4* counts = reinterpret_cast<int4*>(base + w.counts);
+      if (launch_ex_doc_order(t, 1, counts, order, k_order, stream) != cudaSuccess) return MCS_ERR_CUDA;
       t.order = order;
       t.k_order = k_order;
     }

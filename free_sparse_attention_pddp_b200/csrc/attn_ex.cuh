@@ -266,12 +266,15 @@ __device__ __forceinline__ float add_bias(float* s, float slope, float base) {
 
 // CTA u of an ordered launch: chunk by chunk of heads (whose K and V fit L2
 // together), the B x jobs jobs in their order, the chunk's heads side by side.
-// Returns b Hkv + head and the job.
-__device__ __forceinline__ int ordered_job(const ExTile& p, const int* order, int jobs, int u, int* job) {
-  const int most = min(p.Hkv, max(1, p.chunk / p.B)), all = p.B * jobs;
+// Returns b Hkv + head (-1: no work is left for this CTA), the job and its part:
+// 0 the whole job, 1 and 2 the first and the second query tile of a pair.
+__device__ __forceinline__ int ordered_job(const ExTile& p, const int* order, int jobs, int u, int* job, int* part) {
+  const int most = min(p.Hkv, max(1, p.chunk / p.B)), all = order[0];
   const int ch = u / (most * all), in = u % (most * all);
   const int heads = min(most, p.Hkv - ch * most);
-  const int at = order[in / heads];
+  if (heads <= 0 || in >= heads * all) return -1;
+  const int entry = order[1 + in / heads], at = entry >> 2;
+  *part = entry & 3;
   *job = at % jobs;
   return at / jobs * p.Hkv + ch * most + in % heads;
 }

@@ -231,7 +231,8 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
   cta /= p.kv_splits;
   int kt, bh;
   if (DOC && p.k_order) {  // the tiles with the most work first
-    bh = ordered_job(p, p.k_order, p.Tk, cta, &kt);
+    int part;
+    bh = ordered_job(p, p.k_order, p.Tk, cta, &kt, &part);
   } else if (p.causal) {
     const int per_chunk = p.chunk * p.Tk;
     const int ch = cta / per_chunk, in = cta % per_chunk;
@@ -668,7 +669,8 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
   const int BH = p.B * p.Hkv;
   int qt, bh;
   if (DOC && p.order) {
-    bh = ordered_job(p, p.order, p.Tq, cta, &qt);
+    int part;
+    bh = ordered_job(p, p.order, p.Tq, cta, &qt, &part);
   } else if (p.causal) {  // the last query tiles see the most keys and go first
     const int per_chunk = p.chunk * p.Tq;
     const int ch = cta / per_chunk, in = cta % per_chunk;

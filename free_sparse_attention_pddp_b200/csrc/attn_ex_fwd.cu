@@ -42,6 +42,15 @@ constexpr int kSoftRegs = kExSoftRegs;
 // as below 1, and most tiles leave O alone.
 constexpr float kRescale = 4.0f;
 
+// Whether the two tiles of a pair take their own lists of key tiles side by side, n0 and n1 long, instead of the n that
+// either needs.
+__device__ __forceinline__ bool apart_pays(int n, int n0, int n1) {
+  return 4 * n > 5 * max(n0, n1) && min(n0, n1) > 0;
+}
+// Pairs of query tiles beyond half of an SM's share of all steps, of which there are fewer than this (two on each of
+// 148 SMs), are cut.
+constexpr int kMostCuts = 296;
+
 template <int D>
 struct FwdCfg {
   // With d = 64 the accumulators leave 128 TMEM columns for P, so S(i + 1) need not wait for O += P(i) V.
@@ -89,8 +98,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform to the compiler too
   const int lane = threadIdx.x & 31;
-  const bool single = p.single;
-  const int per = single ? 1 : 2;  // query tiles of a CTA
+  bool single = p.single;
+  const int per = single ? 1 : 2;  // query tiles of a job
   const int groups = (p.Tq + per - 1) / per;
   // Work order: splits of one job side by side; then, for causal masks, the
   // heads of a chunk (whose K and V fit L2 together) with the longest query
@@ -98,10 +107,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int u = blockIdx.x;
   const int split = u % p.nsplit;
   u /= p.nsplit;
-  int job, bh;
+  int job, bh, part = 0;
   const int BH = p.B * p.Hkv;
   if (DOC && p.order) {  // the jobs with the most key tiles first
-    bh = ordered_job(p, p.order, groups, u, &job);
+    bh = ordered_job(p, p.order, groups, u, &job, &part);
+    if (bh < 0) return;
+    if (part) single = true;  // a long pair, whose tiles have a CTA each
   } else if (p.causal) {
     const int per_chunk = p.chunk * groups;
     const int ch = u / per_chunk, in = u % per_chunk;
@@ -113,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bh = u / groups;
   }
   const int b = bh / p.Hkv, hk = bh % p.Hkv;
-  const int qt0 = job * per;
+  const int qt0 = job * per + (part >> 1);
   const bool has1 = !single && qt0 + 1 < p.Tq;  // slot 1 has a query tile of its own
   const int prefix = p.prefix ? p.prefix[b] : 0;
   // keys below limit(position) pass the causal and prefix masks
@@ -183,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
     count[0] = count[1] = count[2] = 0;
+    count[3] = single;
     fence_mbar_init();
     if (early > 0) {
       load_q();
@@ -219,13 +231,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (single) n1 = n >> 1, n0 = n - n1;
   // Two query tiles of different documents need different key tiles: beyond a fifth of them the slots go through their
   // own lists side by side instead of waiting for each other in one.
-  const bool zip = DOC && !single && 4 * n > 5 * max(n0, n1) && min(n0, n1) > 0;
+  const bool zip = DOC && !single && apart_pays(n, n0, n1);
   if (zip) n = n0 + n1;
   const bool apart = single || zip;  // no tile serves both slots
   const TileIter first{DOC ? tiles.meet : 0u, DOC && !zip ? tiles.meet2 : 0u, lo, lo};
   const TileIter second{tiles.meet2, 0u, lo, lo};
   const EntryIter entries{first, second, zip ? min(n0, n1) : 0, !zip || n0 > n1};
 
+  // read again where it is needed, since a register for it would spill another
+  const uint32_t mode_at = smem_u32(count + 3);
+  auto one_tile = [&]() { return DOC ? lds32(mode_at) != 0 : single; };
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
     if (warp == 0) {
@@ -238,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dV = sdesc_sw128(smem_u32(sV), 16384, 1024);
         // S_t = Q_t K^T with the CTA's list entry j
         auto issue_s = [&](int t, int j) {
-          const uint64_t dQt = sdesc_advance(dQ, single ? 0 : t * C::TILE);
+          const uint64_t dQt = sdesc_advance(dQ, one_tile() ? 0 : t * C::TILE);
           const uint64_t dKs = sdesc_advance(dK, (j % C::NS) * C::TILE);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -264,10 +279,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           return wait(&v_full[s], j / C::NS) && (!pad || wait(&v_ok[s], j / C::NS));
         };
         TileIter it = first, it2 = second;
-        const int steps = single ? (n + 1) >> 1 : zip ? max(n0, n1) : n;
+        const int steps = one_tile() ? (n + 1) >> 1 : zip ? max(n0, n1) : n;
         // the slots' list entries of a step
-        auto entry0 = [&](int step) { return single ? 2 * step : zip ? step + min(step, n1) : step; };
-        auto entry1 = [&](int step) { return single ? 2 * step + 1 : zip ? step + min(step + 1, n0) : step; };
+        auto entry0 = [&](int step) { return one_tile() ? 2 * step : zip ? step + min(step, n1) : step; };
+        auto entry1 = [&](int step) { return one_tile() ? 2 * step + 1 : zip ? step + min(step + 1, n0) : step; };
         int i0 = 0, i1 = 0;     // the slots' steps
         int behind = -1;        // slot 1's list entry whose O += P V is to come
         bool behind_pad = false;
@@ -282,15 +297,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else if (DOC) {
             if (j0 >= n) return 0;
             int kt = it.next() - lo;
-            if (tile_bit(tiles.pads, kt)) f |= single ? 4 : 12;
-            if (single) {
+            if (tile_bit(tiles.pads, kt)) f |= one_tile() ? 4 : 12;
+            if (one_tile()) {
               f |= 1;
               if (j1 < n) f |= tile_bit(tiles.pads, it.next() - lo) ? 10 : 2;
             } else {
               f |= (tile_bit(tiles.meet, kt) ? 1 : 0) | (tile_bit(tiles.meet2, kt) ? 2 : 0);
             }
           } else {
-            f = (j0 < (single ? n : n0) ? 1 : 0) | (j1 < (single || has1 ? n : 0) ? 2 : 0);
+            f = (j0 < (one_tile() ? n : n0) ? 1 : 0) | (j1 < (one_tile() || has1 ? n : 0) ? 2 : 0);
           }
           return f;
         };
@@ -411,14 +426,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tP = C::AHEAD ? tmem + lane_addr + 384 + t * 64 + half * 32 : tS;
     const uint32_t tO = tmem + lane_addr + 256 + t * D + half * (D / 2);  // this half's output columns
     const int nt = t == 0 ? n0 : n1;
-    const int qt = single ? qt0 : qt0 + t;
+    const int qt = one_tile() ? qt0 : qt0 + t;
     const int tok = qt * p.tpt + row / p.g;
     const int head = hk * p.g + row % p.g;
-    const bool row_valid = row < rt && tok < p.Nq && (t == 0 || single || has1);
+    const bool row_valid = row < rt && tok < p.Nq && (t == 0 || one_tile() || has1);
     const int pos = p.lens ? p.P + min(max(row_valid ? p.lens[tok] : 0, 0), p.C) - 1 : off + tok;
     const int lim = limit(pos) - half * 64;
     const int lim_all = limit(off + qt * p.tpt);  // keys that every row of the tile sees
-    const uint32_t whole = t == 0 || single ? tiles.whole : tiles.whole2;
+    const uint32_t whole = t == 0 || one_tile() ? tiles.whole : tiles.whole2;
     int my_doc = DOC && row_valid ? p.doc_q[static_cast<size_t>(b) * p.Nq + tok] : -2;
     if (my_doc < 0) my_doc = -2;  // a padded query matches no key
     const float mul = p.mul;  // what turns a score into log2 units
@@ -429,14 +444,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t other_max = smem_u32(smem + C::OFF_MAX) + ((t * 2 + (half ^ 1)) * 128 + row) * 8;
     const int pair_bar = 2 + t * 4 + wq;  // the two warps that share these rows
     TileIter it = first;
-    if (DOC && !single) it = TileIter{t == 0 ? tiles.meet : tiles.meet2, 0u, lo, lo};
-    if (single && t == 1 && nt > 0) it.next();
+    if (DOC && !one_tile()) it = TileIter{t == 0 ? tiles.meet : tiles.meet2, 0u, lo, lo};
+    if (one_tile() && t == 1 && nt > 0) it.next();
     float m = -CUDART_INF_F;  // running max, log2 units (the same in both halves)
     float l = 0.f;            // this half's sum
     bool ok = true;
     for (int i = 0; i < nt; ++i) {
       const int kt = it.next();
-      if (single && i + 1 < nt) it.next();
+      if (one_tile() && i + 1 < nt) it.next();
       // where the tile's documents differ: the ids of keys `lane` and 32 + `lane` of this half, under way while S is
       const bool mixed = DOC && !tile_bit(whole, kt - lo);
       int id0 = 0, id1 = 0;
@@ -560,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // One query tile for both slots: slot 1 hands its sums over in the K/V ring, which nobody reads any more once both
     // slots' last products are done, and slot 0 joins them. Every warp takes part, whatever happened.
     float* handed = reinterpret_cast<float*>(smem + C::OFF_K) + half * (D / 2) * 128 + row;  // [column][row]
-    const bool join = single && n1 > 0;
+    const bool join = one_tile() && n1 > 0;
     if (join) {
       named_barrier_sync<10, 512>();
       if (t == 1) {
@@ -746,51 +761,102 @@ __global__ void __launch_bounds__(128) ex_doc_tiles(const ExTile p, int* k_ids, 
   if (i == 0) (key ? k_ranges : q_ranges)[at] = make_int4(s_min, s_max, s_pad, 0);
 }
 
-// Order of the jobs of a document mask, those with the most tiles first: the
-// documents' lengths differ, and a long job that starts last runs alone. Job i
-// of request b is `per` query tiles (their key tiles) or, in the second CTA, one
-// key tile (its query tiles). A counting sort by one CTA: order[rank] = b jobs + i.
-__global__ void __launch_bounds__(1024) ex_doc_order(const ExTile p, int per, int* q_order, int* k_order) {
-  constexpr int kKept = 4096;  // jobs whose bins are kept from the first sweep for the second
+// What the jobs of a document mask have to do, one warp per job: job i of request
+// b is `per` query tiles (their key tiles) or, behind the query jobs, one key
+// tile (its query tiles). counts[b jobs + i] = (steps, tiles of the first and of
+// the second query tile).
+__global__ void __launch_bounds__(256) ex_doc_counts(const ExTile p, int per, int q_all, int all, int4* counts) {
+  const int job = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (job >= all) return;
+  const bool key = job >= q_all;
+  const int at = key ? job - q_all : job;
+  const int jobs = key ? p.Tk : (p.Tq + per - 1) / per;
+  const int b = at / jobs, i = at % jobs, off = p.Nk - p.Nq;
+  const int prefix = p.prefix ? p.prefix[b] : 0;
+  const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
+  const int4* ranges = key ? p.q_ranges + static_cast<size_t>(b) * p.Tq : p.k_ranges + static_cast<size_t>(b) * p.Tk;
+  int lo = 0, hi = key ? p.Tq : p.Tk;
+  int4 r0, r1 = none;
+  if (key) {
+    r0 = p.k_ranges[static_cast<size_t>(b) * p.Tk + i];
+    if (p.causal && i * 128 >= prefix) lo = min(p.Tq, max(0, i * 128 - off) / p.tpt);
+  } else {
+    r0 = p.q_ranges[static_cast<size_t>(b) * p.Tq + i * per];
+    if (per == 2 && i * per + 1 < p.Tq) r1 = p.q_ranges[static_cast<size_t>(b) * p.Tq + i * per + 1];
+    const int last = off + min(p.Nq, (i + 1) * per * p.tpt) - 1;
+    if (p.causal) hi = (min(p.Nk, max(max(last + 1, prefix), 0)) + 127) >> 7;
+  }
+  int n0 = 0, n1 = 0, n = 0;
+  for (int t0 = lo; t0 < hi; t0 += 256) {  // eight tiles a lane, whose loads overlap
+    int4 r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int t = t0 + e * 32 + lane;
+      r[e] = t < hi ? ranges[t] : none;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int a0 = docs_meet(r[e], r0), a1 = docs_meet(r[e], r1);
+      n0 += a0;
+      n1 += a1;
+      n += a0 | a1;
+    }
+  }
+  n0 = __reduce_add_sync(0xffffffffu, n0);
+  n1 = __reduce_add_sync(0xffffffffu, n1);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) counts[job] = make_int4(apart_pays(n, n0, n1) ? max(n0, n1) : n, n0, n1, 0);
+}
+
+// Order of these jobs, those with the most steps first: the documents' lengths
+// differ, and a long job that starts last runs alone. A pair of query tiles that
+// takes more than half of an SM's share of the whole is cut into its tiles: each
+// goes to both slots of a CTA of its own, with half of its key tiles to a slot.
+// (Documents of 6000 tokens on average in 32760, 2 heads: the longest pair has 123
+// steps, and cutting takes 270 instead of 365 us. Cut everywhere, calls whose jobs
+// are many and short take 20 % longer: twice as many set-ups.) A counting sort by
+// one CTA for the query jobs and one for the key tiles: order[0] entries
+// b jobs + i, times 4, plus 0 or the tile's number, 1 or 2.
+__global__ void __launch_bounds__(1024) ex_doc_order(const ExTile p, int per, const int4* counts, int* q_order,
+                                                     int* k_order) {
   __shared__ int bins[4096 + 1];
-  __shared__ uint16_t kept[kKept];
   __shared__ int sums[32];
+  __shared__ int4 cut[kMostCuts];  // a cut job, its tiles' bins, whether there is a second
+  __shared__ int cuts, seconds;
+  __shared__ unsigned long long total_steps;
   const bool key = blockIdx.x == 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int jobs = key ? p.Tk : (p.Tq + per - 1) / per, all = jobs * p.B;
-  const int tiles = key ? p.Tq : p.Tk;
-  const int4* ranges = key ? p.q_ranges : p.k_ranges;
+  const int q_jobs = (p.Tq + per - 1) / per, jobs = key ? p.Tk : q_jobs, all = jobs * p.B;
+  if (key) counts += q_jobs * p.B;
   int* order = key ? k_order : q_order;
-  const int step = (tiles + 4095) / 4096;  // tiles per bin
+  const int step = ((key ? p.Tq : p.Tk) + 4095) / 4096;  // steps per bin
+  auto bin = [&](int n) { return 4096 - n / step; };
   for (int i = threadIdx.x; i <= 4096; i += 1024) bins[i] = 0;
+  if (threadIdx.x == 0) cuts = seconds = 0, total_steps = 0;
   __syncthreads();
-  const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
-  auto bin = [&](int at) {  // a whole warp: 4096 less the job's tiles
-    const int b = at / jobs, i = at % jobs, off = p.Nk - p.Nq;
-    const int prefix = p.prefix ? p.prefix[b] : 0;
-    int lo = 0, hi = tiles;
-    int4 r0, r1 = none;
-    if (key) {
-      r0 = p.k_ranges[static_cast<size_t>(b) * p.Tk + i];
-      if (p.causal && i * 128 >= prefix) lo = min(p.Tq, max(0, i * 128 - off) / p.tpt);
+  // whole-number sums: the atomics' order changes nothing but the order of equal jobs
+  unsigned long long some = 0;
+  for (int at = threadIdx.x; at < all; at += 1024) some += counts[at].x;
+#pragma unroll
+  for (int w = 16; w >= 1; w >>= 1) some += __shfl_xor_sync(0xffffffffu, some, w);
+  if (lane == 0) atomicAdd(&total_steps, some);
+  __syncthreads();
+  // n > share / (2 SMs), so there are fewer than kMostCuts of them (each is there for every head)
+  const unsigned long long share = total_steps * p.Hkv;
+  auto long_job = [&](int n) { return per == 2 && !key && static_cast<unsigned long long>(n) * kMostCuts > share; };
+  for (int at = threadIdx.x; at < all; at += 1024) {
+    const int4 n = counts[at];
+    if (long_job(n.x)) {
+      const int second = at % jobs * 2 + 1 < p.Tq;
+      const int4 c = make_int4(at, bin((n.y + 1) / 2), bin((n.z + 1) / 2), second);
+      cut[atomicAdd(&cuts, 1)] = c;
+      atomicAdd(&bins[c.y], 1);
+      if (second) {
+        atomicAdd(&bins[c.z], 1);
+        atomicAdd(&seconds, 1);
+      }
     } else {
-      r0 = p.q_ranges[static_cast<size_t>(b) * p.Tq + i * per];
-      if (per == 2 && i * per + 1 < p.Tq) r1 = p.q_ranges[static_cast<size_t>(b) * p.Tq + i * per + 1];
-      const int last = off + min(p.Nq, (i + 1) * per * p.tpt) - 1;
-      if (p.causal) hi = (min(p.Nk, max(max(last + 1, prefix), 0)) + 127) >> 7;
-    }
-    int n = 0;
-    for (int t = lo + lane; t < hi; t += 32) {
-      const int4 r = ranges[static_cast<size_t>(b) * tiles + t];
-      n += docs_meet(r, r0) || docs_meet(r, r1);
-    }
-    return 4096 - __reduce_add_sync(0xffffffffu, n) / step;
-  };
-  for (int at = warp; at < all; at += 32) {
-    const int n = bin(at);
-    if (lane == 0) {
-      atomicAdd(&bins[n], 1);
-      if (at < kKept) kept[at] = static_cast<uint16_t>(n);
+      atomicAdd(&bins[bin(n.x)], 1);
     }
   }
   __syncthreads();
@@ -817,17 +883,20 @@ __global__ void __launch_bounds__(1024) ex_doc_order(const ExTile p, int per, in
     before += mine[e];
   }
   if (threadIdx.x == 1023) bins[4096] = before;
+  if (threadIdx.x == 0) order[0] = all + seconds;
   __syncthreads();
   // Equal jobs land about in order (neighbours share their tiles in L2); the order decides when they run, not what
   // they compute.
-  for (int at = threadIdx.x; at - static_cast<int>(threadIdx.x) < min(all, kKept); at += 1024) {
-    if (at < min(all, kKept)) order[atomicAdd(&bins[kept[at]], 1)] = at;
-    __syncthreads();
+  ++order;
+  for (int i = threadIdx.x; i < cuts; i += 1024) {
+    const int4 c = cut[i];
+    order[atomicAdd(&bins[c.y], 1)] = c.x * 4 + 1;
+    if (c.w) order[atomicAdd(&bins[c.z], 1)] = c.x * 4 + 2;
   }
-  for (int at = kKept + warp; at - warp < all; at += 32) {
+  for (int at = threadIdx.x; at - static_cast<int>(threadIdx.x) < all; at += 1024) {
     if (at < all) {
-      const int n = bin(at);
-      if (lane == 0) order[atomicAdd(&bins[n], 1)] = at;
+      const int n = counts[at].x;
+      if (!long_job(n)) order[atomicAdd(&bins[bin(n)], 1)] = at * 4;
     }
     __syncthreads();
   }
@@ -843,7 +912,8 @@ cudaError_t launch_fwd(const CUtensorMap* tq, const CUtensorMap* tk, const CUten
   const cudaError_t e = make_ready(ready, kern, FwdCfg<D>::SMEM + 2560, kLaunchRegs);  // 2^12 tiles
   if (e != cudaSuccess) return e;
   const int per = p.single ? 1 : 2;
-  const long long grid = static_cast<long long>(p.B) * p.Hkv * ((p.Tq + per - 1) / per) * p.nsplit;
+  long long grid = static_cast<long long>(p.B) * p.Hkv * ((p.Tq + per - 1) / per) * p.nsplit;
+  if (p.order && per == 2) grid += std::min<long long>(grid, kMostCuts);  // CTAs for the second tiles of cut pairs
   kern<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(*tq, *tk, *tv, p);
   note_launches(1);
   return cudaGetLastError();
@@ -866,9 +936,11 @@ cudaError_t launch_ex_combine(int d, const ExTile& p, int parts, cudaStream_t s)
   return cudaGetLastError();
 }
 
-cudaError_t launch_ex_doc_order(const ExTile& p, int per, int* q_order, int* k_order, cudaStream_t s) {
-  ex_doc_order<<<k_order ? 2 : 1, 1024, 0, s>>>(p, per, q_order, k_order);
-  note_launches(1);
+cudaError_t launch_ex_doc_order(const ExTile& p, int per, int4* counts, int* q_order, int* k_order, cudaStream_t s) {
+  const int q_all = p.B * ((p.Tq + per - 1) / per), all = q_all + (k_order ? p.B * p.Tk : 0);
+  ex_doc_counts<<<(all + 7) / 8, 256, 0, s>>>(p, per, q_all, all, counts);
+  ex_doc_order<<<k_order ? 2 : 1, 1024, 0, s>>>(p, per, counts, q_order, k_order);
+  note_launches(2);
   return cudaGetLastError();
 }
 

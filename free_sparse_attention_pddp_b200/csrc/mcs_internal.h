@@ -156,7 +156,8 @@ struct ExTile {
   const int32_t *doc_q, *doc_k;    // null without a document mask, and then so are the next five
   const int4 *q_ranges, *k_ranges;  // [B,Tq], [B,Tk]: smallest and largest id, any padding
   const int *q_ids, *k_ids;        // [B,Tq,128] (backward), [B,Tk,128]
-  const int *order, *k_order;      // document mask: the order of the query jobs and of the key tiles, or null
+  const int *order, *k_order;      // document mask: the order of the query jobs and of the key tiles (their number,
+                                   // then 4 job + part), or null
   const int32_t* lens;             // shared prefix: the requests' lengths give the positions
   int P, C;
   uint16_t* o;                     // outputs, or the partials of the splits
@@ -183,7 +184,7 @@ cudaError_t launch_ex_row_stats(int d, const ExTile& p, const uint16_t* o, const
 cudaError_t launch_ex_bwd(int d, const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk,
                           const CUtensorMap* tv, const ExTile& p, cudaStream_t s);
 // order of the jobs (of `per` query tiles) and, unless null, of the key tiles: [B jobs], [B Tk]
-cudaError_t launch_ex_doc_order(const ExTile& p, int per, int* q_order, int* k_order, cudaStream_t s);
+cudaError_t launch_ex_doc_order(const ExTile& p, int per, int4* counts, int* q_order, int* k_order, cudaStream_t s);
 cudaError_t launch_ex_doc_tiles(const ExTile& p, int* k_ids, int4* k_ranges, int* q_ids, int4* q_ranges,
                                 cudaStream_t s);
 

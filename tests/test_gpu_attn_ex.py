@@ -125,6 +125,18 @@ def test_documents(mcs, mean, pad, shuffle, causal, g, d):
     both(mcs, 2, 2 * g, 2, 700, 700, d, causal=causal, doc_q=ids, doc_k=ids, cap=30.0 if g == 3 else 0.0, seed=g)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hkv,N,lengths,causal", [(1, 16, 1250, (900, 20, 330), False), (1, 16, 1210, (70, 1000), True),
+                                                    (2, 10, 1170, (1100, 40), False), (1, 38, 1100, (900, 60, 70), False)])
+def test_documents_of_very_different_lengths(mcs, B, Hkv, N, lengths, causal, d):
+    """More pairs of query tiles than SMs, some of which are cut into their tiles; odd numbers of tiles."""
+    ids = torch.repeat_interleave(torch.arange(len(lengths)), torch.tensor(lengths))
+    ids = torch.cat([ids, torch.full((N - len(ids),), -1)])[None].repeat(B, 1)
+    if B > 1:
+        ids[1] = ids[1].flip(0)
+    both(mcs, B, 2 * Hkv, Hkv, N, N, d, causal=causal, doc_q=ids, doc_k=ids, seed=N)
+
+
 def test_documents_of_queries_and_keys_differ(mcs):
     """Cross-attention: a query document without keys, a key document without queries, large and negative ids."""
     dq = torch.full((1, 260), 7)
