@@ -15,6 +15,10 @@
 // instead of 12 from Python for a single request's 480 keys). Keys past the request's length are never
 // read (cp.async fills zeros), so the cache may hold anything there.
 //
+// 1 request of 75600 keys (8 KV heads, 40 query heads, d = 128): 54 us for 310 MB,
+// 5.7 TB/s of the 6.46 that a copy reaches, and 7 us for the join; 64 requests
+// of ragged lengths run at a copy's rate.
+//
 // P is split into two bf16 terms for P V: the products are free here, and the
 // output keeps fp32 accuracy.
 #include "attn_ex.cuh"

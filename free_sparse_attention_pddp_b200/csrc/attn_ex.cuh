@@ -45,10 +45,11 @@ cudaError_t with_options(int d, const ExTile& p, F f) {
 // CTA of the tile kernels: warp 0 issues the UMMAs, warp 1 the TMA loads, warp
 // 2 clears padded rows, warp 3 only completes their warpgroup; 16 softmax warps,
 // four to each SM sub-partition, so that one warp's TMEM loads, barriers and
-// dependent arithmetic hide behind the others' exponentials. (With 8 softmax
-// warps of twice the columns the forward kernel ran at 1004 instead of XXXX
-// TFLOP/s on 37 heads of 8192 tokens, d = 128.) setmaxnreg moves registers from
-// the first warpgroup to the softmax.
+// dependent arithmetic hide behind the others' exponentials. (37 heads of 8192
+// tokens, d = 128, forward, against 8 softmax warps of twice the columns: plain
+// scores 1001 and 1004 TFLOP/s, capped 716 and 653, biased 833 and 781.) In the
+// forward kernel setmaxnreg moves registers from the first warpgroup to the
+// softmax; the gradients' kernel runs at the launch's count.
 constexpr int kExThreads = 640;
 constexpr int kExLaunchRegs = 96;
 constexpr int kExLowRegs = 64;
