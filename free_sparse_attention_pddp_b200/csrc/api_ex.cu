@@ -137,6 +137,10 @@ FwdPlan fwd_plan(int B, int Hkv, int g, int Nq, int Nk, int d) {
   return f;
 }
 
+// Jobs of a document mask: their order matters where there are more than SMs;
+// its entries, four times a job's number, are 32-bit.
+bool order_matters(long long jobs) { return jobs > kSms && jobs < (1ll << 28); }
+
 // workspace: status | document tiles | partials of the key splits
 struct FwdWs {
   size_t k_ids, k_ranges, q_ranges, order, counts, part_lse, part_o, total;
@@ -393,8 +397,7 @@ mcs_status mcs_dense_ex(const mcs_attn_shape* s, const mcs_attn_opts* opts, cons
     t.k_ids = ids;
     t.k_ranges = kr;
     t.q_ranges = qr;
-    // with more jobs than SMs their order matters
-    if (static_cast<long long>(p.B) * p.Hkv * (f.single ? f.Tq : (f.Tq + 1) / 2) > kSms) {
+    if (order_matters(static_cast<long long>(p.B) * p.Hkv * (f.single ? f.Tq : (f.Tq + 1) / 2))) {
       int* order = reinterpret_cast<int*>(base + w.order);
       int4* counts = reinterpret_cast<int4*>(base + w.counts);
       if (launch_ex_doc_order(t, f.single ? 1 : 2, counts, order, nullptr, stream) != cudaSuccess) return MCS_ERR_CUDA;
@@ -454,7 +457,7 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
     t.k_ranges = kr;
     t.q_ids = qid;
     t.q_ranges = qr;
-    if (static_cast<long long>(p.B) * p.Hkv * std::max(f.Tq, f.Tk) > kSms) {
+    if (order_matters(static_cast<long long>(p.B) * p.Hkv * std::max(f.Tq, f.Tk))) {
       int* order = reinterpret_cast<int*>(base + w.order);
       int* k_order = reinterpret_cast<int*>(base + w.k_order);
       int4* counts = reinterpret_cast<int4*>(base + w.counts);
