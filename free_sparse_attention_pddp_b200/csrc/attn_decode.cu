@@ -91,6 +91,7 @@ struct DecCfg {
 
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams p) {
+  await_previous();
   using C = DecCfg<D, MT>;
   constexpr int NT = D / 8;   // output column tiles
   constexpr int KS = D / 16;  // k steps of the scores
@@ -251,6 +252,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
 
+  next_may_start();  // not before: what waits beside the loop costs it 6 % (one request of 75600 keys)
+
   // join the four warps: outputs and (max, sum) of each row through shared memory
   float* out = reinterpret_cast<float*>(smem);
   float2* stat = reinterpret_cast<float2*>(smem + C::SMEM - C::STAT);
@@ -352,6 +355,8 @@ namespace {
 // turn, then the warps' sums are added in order.
 template <int D>
 __global__ void __launch_bounds__(256) decode_combine(const DecodeParams p) {
+  next_may_start();
+  await_previous();
   constexpr int E = D / 32;
   __shared__ float s_m[8], s_l[8], s_o[8][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -440,9 +445,8 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
     note_launches(1);
     return cudaLaunchKernelEx(&cfg, decode_kernel<D, MT>, p);
   }
-  decode_kernel<D, MT><<<static_cast<unsigned>(grid), kThreads, DecCfg<D, MT>::SMEM, s>>>(p);
-  note_launches(1);
-  return cudaGetLastError();
+  return launch_in_sequence(decode_kernel<D, MT>, static_cast<unsigned>(grid), kThreads, DecCfg<D, MT>::SMEM, s,
+                            p.pre_parts > 0, p);
 }
 
 }  // namespace
@@ -456,10 +460,7 @@ cudaError_t launch_decode_combine(int d, const DecodeParams& p, cudaStream_t s) 
   const int parts = p.pre_parts + p.nsplit;
   const int warps = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
   const unsigned grid = static_cast<unsigned>(p.B) * p.Hq;
-  if (d == 64) decode_combine<64><<<grid, warps * 32, 0, s>>>(p);
-  else decode_combine<128><<<grid, warps * 32, 0, s>>>(p);
-  note_launches(1);
-  return cudaGetLastError();
+  return launch_in_sequence(d == 64 ? decode_combine<64> : decode_combine<128>, grid, warps * 32, 0, s, true, p);
 }
 
 }  // namespace mcs

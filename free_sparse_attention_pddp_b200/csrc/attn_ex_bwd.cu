@@ -164,6 +164,8 @@ __device__ __forceinline__ void teardown(volatile int* abort_flag, uint64_t* don
 template <int D>
 __global__ void __launch_bounds__(256) ex_row_stats(const ExTile p, const uint16_t* o, const uint16_t* d_o,
                                                     const float* lse, float* stats) {
+  next_may_start();
+  await_previous();
   constexpr int LANES = D / 8;             // of a row
   constexpr int PASS = 256 / LANES;        // rows at a time
   const int qt = blockIdx.x % p.Tq, bh = blockIdx.x / p.Tq;
@@ -987,6 +989,8 @@ template <int D, bool CAP, bool BIAS, bool DOC>
 __global__ void __launch_bounds__(kThreads, 1)
     ex_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
+  next_may_start();
+  await_previous();
   const int keys = p.B * p.Hkv * p.Tk * p.kv_splits;
   if (static_cast<int>(blockIdx.x) < keys) dkv_tile<D, CAP, BIAS, DOC>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x);
   else dq_tile<D, CAP, BIAS, DOC, false>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x - keys);
@@ -998,6 +1002,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ex_delta_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const ExTile p) {
+  next_may_start();
+  await_previous();
   dq_tile<D, CAP, BIAS, DOC, true>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x);
 }
 
@@ -1005,6 +1011,8 @@ namespace {
 
 // dV and dK as the sums of their parts over the query tiles, in the parts' order; four values per thread.
 __global__ void __launch_bounds__(256) ex_sum_parts(const ExTile p) {
+  next_may_start();
+  await_previous();
   const size_t quads = p.kv_size / 4;
   const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= 2 * quads) return;
@@ -1038,14 +1046,15 @@ cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUten
     auto delta = ex_delta_kernel<D, CAP, BIAS, DOC>;
     const cudaError_t e2 = make_ready(ready_delta, delta, most_q, 0);
     if (e2 != cudaSuccess) return e2;
-    delta<<<p.B * p.Hkv * p.Tq, kThreads, DqCfg<D>::SMEM + (DOC ? (p.Tk + 31) / 32 * 12u : 0u), s>>>(*tq, *tg, *tk,
-                                                                                                  *tv, p);
-    note_launches(1);
+    const unsigned smem_delta = DqCfg<D>::SMEM + (DOC ? (p.Tk + 31) / 32 * 12u : 0u);
+    const cudaError_t e3 = launch_in_sequence(delta, p.B * p.Hkv * p.Tq, kThreads, smem_delta, s, DOC, *tq, *tg, *tk,
+                                              *tv, p);
+    if (e3 != cudaSuccess) return e3;
   }
-  kern<<<p.B * p.Hkv * (p.Tk * p.kv_splits + p.Tq), kThreads, smem, s>>>(*tq, *tg, *tk, *tv, p);
-  if (p.part_kv) ex_sum_parts<<<static_cast<unsigned>((p.kv_size / 2 + 255) / 256), 256, 0, s>>>(p);
-  note_launches(p.part_kv ? 2 : 1);
-  return cudaGetLastError();
+  const cudaError_t e4 = launch_in_sequence(kern, p.B * p.Hkv * (p.Tk * p.kv_splits + p.Tq), kThreads, smem, s, true, *tq,
+                                            *tg, *tk, *tv, p);
+  if (e4 != cudaSuccess || !p.part_kv) return e4;
+  return launch_in_sequence(ex_sum_parts, static_cast<unsigned>((p.kv_size / 2 + 255) / 256), 256, 0, s, true, p);
 }
 
 }  // namespace
@@ -1053,10 +1062,8 @@ cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUten
 cudaError_t launch_ex_row_stats(int d, const ExTile& p, const uint16_t* o, const uint16_t* d_o, const float* lse,
                                 float* stats, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(p.B) * p.Hkv * p.Tq;
-  if (d == 64) ex_row_stats<64><<<grid, 256, 0, s>>>(p, o, d_o, lse, stats);
-  else ex_row_stats<128><<<grid, 256, 0, s>>>(p, o, d_o, lse, stats);
-  note_launches(1);
-  return cudaGetLastError();
+  return launch_in_sequence(d == 64 ? ex_row_stats<64> : ex_row_stats<128>, grid, 256, 0, s, p.doc_q != nullptr, p, o,
+                            d_o, lse, stats);
 }
 
 cudaError_t launch_ex_bwd(int d, const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk,

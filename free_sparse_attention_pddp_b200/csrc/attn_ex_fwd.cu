@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ex_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
   using C = FwdCfg<D>;
+  next_may_start();
+  await_previous();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + C::OFF_Q;
@@ -694,6 +696,8 @@ namespace {
 // row, lane l holds d/32 columns; the splits are summed in their order.
 template <int D>
 __global__ void __launch_bounds__(128) ex_combine(const ExTile p, int parts) {
+  next_may_start();
+  await_previous();
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);  // (b, tok, head)
@@ -745,6 +749,8 @@ __global__ void __launch_bounds__(128) ex_combine(const ExTile p, int parts) {
 // empty rows). One CTA of 128 threads per tile.
 __global__ void __launch_bounds__(128) ex_doc_tiles(const ExTile p, int* k_ids, int4* k_ranges, int* q_ids,
                                                     int4* q_ranges) {
+  next_may_start();
+  await_previous();
   __shared__ int s_min, s_max, s_pad;
   const int b = blockIdx.x / (p.Tk + p.Tq), at_b = blockIdx.x % (p.Tk + p.Tq);
   const bool key = at_b < p.Tk;
@@ -774,6 +780,8 @@ __global__ void __launch_bounds__(128) ex_doc_tiles(const ExTile p, int* k_ids, 
 // tile (its query tiles). counts[b jobs + i] = (steps, tiles of the first and of
 // the second query tile).
 __global__ void __launch_bounds__(256) ex_doc_counts(const ExTile p, int per, int q_all, int all, int4* counts) {
+  next_may_start();
+  await_previous();
   const int job = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (job >= all) return;
   const bool key = job >= q_all;
@@ -827,6 +835,8 @@ __global__ void __launch_bounds__(256) ex_doc_counts(const ExTile p, int per, in
 // b jobs + i, times 4, plus 0 or the tile's number, 1 or 2.
 __global__ void __launch_bounds__(1024) ex_doc_order(const ExTile p, int per, const int4* counts, int* q_order,
                                                      int* k_order) {
+  next_may_start();
+  await_previous();
   __shared__ int bins[4096 + 1];
   __shared__ int sums[32];
   __shared__ int4 cut[kMostCuts];  // a cut job, its tiles' bins, whether there is a second
@@ -922,9 +932,7 @@ cudaError_t launch_fwd(const CUtensorMap* tq, const CUtensorMap* tk, const CUten
   const int per = p.single ? 1 : 2;
   long long grid = static_cast<long long>(p.B) * p.Hkv * ((p.Tq + per - 1) / per) * p.nsplit;
   if (p.order && per == 2) grid += std::min<long long>(grid, kMostCuts);  // CTAs for the second tiles of cut pairs
-  kern<<<static_cast<unsigned>(grid), kThreads, smem, s>>>(*tq, *tk, *tv, p);
-  note_launches(1);
-  return cudaGetLastError();
+  return launch_in_sequence(kern, static_cast<unsigned>(grid), kThreads, smem, s, DOC, *tq, *tk, *tv, p);
 }
 
 }  // namespace
@@ -938,25 +946,19 @@ cudaError_t launch_ex_fwd(int d, const CUtensorMap* tq, const CUtensorMap* tk, c
 
 cudaError_t launch_ex_combine(int d, const ExTile& p, int parts, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>((static_cast<long long>(p.B) * p.Nq * p.Hq + 3) / 4);
-  if (d == 64) ex_combine<64><<<grid, 128, 0, s>>>(p, parts);
-  else ex_combine<128><<<grid, 128, 0, s>>>(p, parts);
-  note_launches(1);
-  return cudaGetLastError();
+  return launch_in_sequence(d == 64 ? ex_combine<64> : ex_combine<128>, grid, 128, 0, s, true, p, parts);
 }
 
 cudaError_t launch_ex_doc_order(const ExTile& p, int per, int4* counts, int* q_order, int* k_order, cudaStream_t s) {
   const int q_all = p.B * ((p.Tq + per - 1) / per), all = q_all + (k_order ? p.B * p.Tk : 0);
-  ex_doc_counts<<<(all + 7) / 8, 256, 0, s>>>(p, per, q_all, all, counts);
-  ex_doc_order<<<k_order ? 2 : 1, 1024, 0, s>>>(p, per, counts, q_order, k_order);
-  note_launches(2);
-  return cudaGetLastError();
+  const cudaError_t e = launch_in_sequence(ex_doc_counts, (all + 7) / 8, 256, 0, s, true, p, per, q_all, all, counts);
+  if (e != cudaSuccess) return e;
+  return launch_in_sequence(ex_doc_order, k_order ? 2 : 1, 1024, 0, s, true, p, per, counts, q_order, k_order);
 }
 
 cudaError_t launch_ex_doc_tiles(const ExTile& p, int* k_ids, int4* k_ranges, int* q_ids, int4* q_ranges,
                                 cudaStream_t s) {
-  ex_doc_tiles<<<p.B * (p.Tk + p.Tq), 128, 0, s>>>(p, k_ids, k_ranges, q_ids, q_ranges);
-  note_launches(1);
-  return cudaGetLastError();
+  return launch_in_sequence(ex_doc_tiles, p.B * (p.Tk + p.Tq), 128, 0, s, false, p, k_ids, k_ranges, q_ids, q_ranges);
 }
 
 }  // namespace mcs

@@ -241,4 +241,26 @@ int debug_flags();
 // count of kernel launches this library made in the process (diagnostics)
 void note_launches(int n);
 
+// Launches a kernel that begins with await_previous(). `after`: behind another such
+// kernel of the same call, whose end it awaits itself. (Forward and gradients of
+// 2 x 601 tokens with documents and a cap, six launches: 62.6 us, 70.3 one after the
+// other; 8 requests behind a shared prefix of 4096 keys, three launches: 19.0 and
+// 23.6.) A call's first kernel starts after whatever the stream held before.
+template <class... P, class... A>
+cudaError_t launch_in_sequence(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                               bool after, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = after ? 1 : 0;
+  note_launches(1);
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 }  // namespace mcs

@@ -106,6 +106,14 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Kernels of one call that follow one another. The next may be set up beside this
+// one once every CTA of this one has passed next_may_start() (or has ended), and
+// waits in await_previous(), before its first access to memory, until this one has
+// ended and its writes are visible. Every thread of every kernel of such a
+// sequence passes there, so each kernel also ends after all kernels before it.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // packed fp32 arithmetic and a polynomial exp2 (FMA pipe)
 // ---------------------------------------------------------------------------
