@@ -59,6 +59,29 @@ __device__ __forceinline__ bool apart_pays(int n, int n0, int n1) {
 // 148 SMs), are cut.
 constexpr int kMostCuts = 296;
 
+// 2^x for x <= 2^21 on the FMA pipe. t = x + 1.5 2^23, rounded down, holds n =
+// floor(x) in its low bits; 2^(x - n) is a polynomial of degree 5 with p(0) = 1,
+// fitted to [0, 1] by iteratively reweighted least squares (relative error at most
+// 8.3e-8); n is added to its exponent. x <= -127 gives exactly 0.
+__device__ __forceinline__ void exp2_fma(float& x0, float& x1) {
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));  // -127
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x1));
+  const uint64_t x = f2_pack(x0, x1), shift = f2_pack(12582912.f, 12582912.f);
+  uint64_t t;
+  asm("add.rm.f32x2 %0, %1, %2;" : "=l"(t) : "l"(x), "l"(shift));
+  const uint64_t r = f2_add(x, f2_sub(shift, t));
+  uint64_t p = f2_fma(f2_pack(.00186713017f, .00186713017f), r, f2_pack(.00901702978f, .00901702978f));
+  p = f2_fma(p, r, f2_pack(.0557999127f, .0557999127f));
+  p = f2_fma(p, r, f2_pack(.240164444f, .240164444f));
+  p = f2_fma(p, r, f2_pack(.693151295f, .693151295f));
+  p = f2_fma(p, r, f2_pack(1.f, 1.f));
+  float p0, p1, t0, t1;
+  f2_unpack(p, p0, p1);
+  f2_unpack(t, t0, t1);
+  x0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  x1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
+
 template <int D>
 struct FwdCfg {
   // With d = 64 the accumulators leave 128 TMEM columns for P, so S(i + 1) need not wait for O += P(i) V.
@@ -84,6 +107,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     ex_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const ExTile p) {
   using C = FwdCfg<D>;
+  // An eighth of the exponentials on the FMA pipe: 2 to 4 % less time for plain and biased scores (4096 tokens, 16/4
+  // heads, causal, biased: 88.5 us, 92 without; a quarter: 92). With a cap's arithmetic or a document mask's
+  // comparisons beside them they cost up to 4 %.
+  constexpr bool SHARE = !CAP && !DOC;
   next_may_start();
   await_previous();
   extern __shared__ uint8_t smem_raw[];
@@ -529,8 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = 0; q < 16; ++q) {
           float x0, x1;
           f2_unpack(f2_fma(f2_pack(v[2 * q], v[2 * q + 1]), mul2, e2), x0, x1);
-          v[2 * q] = fast_exp2(x0);
-          v[2 * q + 1] = fast_exp2(x1);
+          if (SHARE && q % 8 == 7) {
+            exp2_fma(x0, x1);
+          } else {
+            x0 = fast_exp2(x0);
+            x1 = fast_exp2(x1);
+          }
+          v[2 * q] = x0;
+          v[2 * q + 1] = x1;
           pk[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
         }
         if (C::AHEAD && h2 == 0 && i > 0) {  // O += P(i-1) V has read P(i-1), and O may be scaled
