@@ -207,3 +207,60 @@ def test_few_requests_whose_keys_are_split(mcs, C):
     for B, Hq, Hkv in ((1, 12, 12), (3, 20, 1), (2, 40, 1)):
         run(mcs, B, Hq, Hkv, C, 64, [C, 1, 0][:B], cap=20.0, slopes=[.02] * Hq, seed=C + B)
         run(mcs, B, Hq, Hkv, C, 128, [C - 1, min(70, C - 1), 33][:B], seed=C)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_back_to_back(mcs, graph):
+    """Calls of several kernels each, one behind the other on one workspace, give what they give alone."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    Hq, Hkv, N, d, R, P, C = 32, 16, 1250, 64, 6, 700, 90
+    q, k, v, d_o = rand(g, 1, N, Hq, d), rand(g, 1, N, Hkv, d), rand(g, 1, N, Hkv, d), rand(g, 1, N, Hq, d)
+    ids = torch.repeat_interleave(torch.arange(3), torch.tensor([900, 20, 330]))[None].int().cuda()
+    q1, kp, vp = rand(g, R, Hq, d), rand(g, P, Hkv, d), rand(g, P, Hkv, d)
+    kc, vc = rand(g, R, C, Hkv, d), rand(g, R, C, Hkv, d)
+    lens = torch.tensor([90, 1, 0, 33, 64, 65], dtype=torch.int32, device="cuda")
+    shape, step = mcs.AttnShape(1, Hq, Hkv, N, N, d), mcs.DecodeShape(R, Hq, Hkv, C, d, P=P)
+    few = mcs.AttnShape(1, Hq, Hkv, 100, N, d)  # keys split, parts joined
+    need = [mcs.mcs_attn_workspace_bytes(shape, mcs.MCS_OP_DENSE_EX), mcs.mcs_attn_workspace_bytes(few, mcs.MCS_OP_DENSE_EX),
+            mcs.mcs_attn_workspace_bytes(shape, mcs.MCS_OP_DENSE_BWD), mcs.mcs_decode_workspace_bytes(step)]
+    ws = torch.zeros(max(need), dtype=torch.uint8, device="cuda")
+
+    def outputs():
+        return {"o": torch.empty_like(q), "lse": torch.empty(1, Hq, N, device="cuda"), "dq": torch.empty_like(q),
+                "dk": torch.empty_like(k), "dv": torch.empty_like(v), "o1": torch.empty_like(q1),
+                "l1": torch.empty(R, Hq, device="cuda"), "of": torch.empty_like(q[:, :100]).contiguous()}
+
+    q_few = q[:, :100].contiguous()
+
+    def calls(r):
+        return [lambda: mcs.mcs_dense_ex(shape, q, k, v, r["o"], r["lse"], ws, doc_q=ids, doc_k=ids),
+                lambda: mcs.mcs_dense_ex(few, q_few, k, v, r["of"], None, ws),
+                lambda: mcs.mcs_dense_bwd(shape, q, k, v, r["o"], r["lse"], d_o, r["dq"], r["dk"], r["dv"], ws,
+                                          doc_q=ids, doc_k=ids),
+                lambda: mcs.mcs_decode_shared(step, q1, kp, vp, kc, vc, lens, r["o1"], r["l1"], ws)]
+
+    alone = outputs()
+    for call in calls(alone):
+        call()
+        torch.cuda.synchronize()
+    runs = [outputs() for _ in range(8)]
+
+    def run_all():
+        for r in runs:
+            for call in calls(r):
+                call()
+
+    if graph:
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            run_all()
+        for r in runs:
+            for t in r.values():
+                t.zero_()
+        captured.replay()
+    else:
+        run_all()
+    assert mcs.mcs_poll_status(ws)[0] == 0
+    for r in runs:
+        for name, t in r.items():
+            assert torch.equal(t.view(torch.uint8), alone[name].view(torch.uint8)), name
