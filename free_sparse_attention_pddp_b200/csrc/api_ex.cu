@@ -243,7 +243,12 @@ mcs_status check_decode(const mcs_decode_shape* s) {
 // How single tokens fill the GPU. Two CTAs to an SM; the keys are cut so that
 // about eight waves of them cover the batch (lengths differ, and a late long
 // request should not run alone), in chunks of at least 512 keys, less only
-// where the batch would not fill one wave.
+// where the batch would not fill one wave. A single request has nothing to be
+// balanced against: its length, whatever the cache could hold, is cut into the
+// fewest waves that leave less than 3 % of the slots empty (75600 keys, d = 128:
+// 8 KV heads 57 us, 64 in chunks of 512; 40 KV heads in three waves 239, in one,
+// as clusters of 7 that do not pack into it, 340). Chunks of up to 512 keys fill
+// one wave as far as they go.
 struct DecodePlan {
   int gsplit, chunk, nsplit, cluster;
   FwdPlan pre;
@@ -258,9 +263,15 @@ DecodePlan decode_plan(const mcs_decode_shape* s) {
     const long long per_job = std::max(1ll, ctas / jobs);
     return ((s->C + per_job - 1) / per_job + 63) / 64 * 64;
   };
-  f.chunk = static_cast<int>(std::max(64ll, std::max(cut(8 * slots), std::min(512ll, cut(slots)))));
+  if (s->B == 1) {
+    int waves = 1;
+    while (waves < 8 && cut(slots) > 512 && 100 * (waves * slots / jobs * jobs) < 97 * waves * slots) ++waves;
+    f.chunk = static_cast<int>(std::max(64ll, cut(waves * slots)));
+  } else {
+    f.chunk = static_cast<int>(std::max(64ll, std::max(cut(8 * slots), std::min(512ll, cut(slots)))));
+  }
   f.nsplit = (s->C + f.chunk - 1) / f.chunk;
-  f.cluster = s->P == 0 && f.nsplit > 1 && f.nsplit <= 8 && jobs * f.nsplit <= slots;
+  f.cluster = s->P == 0 && f.nsplit > 1 && f.nsplit <= 8 && f.chunk <= 512 && jobs * f.nsplit <= slots;
   if (s->P > 0) f.pre = fwd_plan(1, s->Hkv, g, s->B, s->P, s->d);
   return f;
 }

@@ -15,8 +15,8 @@
 // instead of 12 from Python for a single request's 480 keys). Keys past the request's length are never
 // read (cp.async fills zeros), so the cache may hold anything there.
 //
-// 1 request of 75600 keys (8 KV heads, 40 query heads, d = 128): 54 us for 310 MB,
-// 5.7 TB/s of the 6.46 that a copy reaches, and 7 us for the join; 64 requests
+// 1 request of 75600 keys (8 KV heads, 40 query heads, d = 128): 51 us for 310 MB,
+// 6.1 TB/s of the 6.46 that a copy reaches, and 5 us for the join; 64 requests
 // of ragged lengths run at a copy's rate.
 //
 // P is split into two bf16 terms for P V: the products are free here, and the
@@ -77,6 +77,11 @@ __device__ __forceinline__ float4 cluster_load(uint32_t addr) {
 // length of request b, bounded to [0, C]
 __device__ __forceinline__ int request_len(const DecodeParams& p, int b) { return min(max(p.lens[b], 0), p.C); }
 
+// keys of a request's chunks; a single request's are its length's share, whole blocks of the four warps
+__device__ __forceinline__ int chunk_keys(const DecodeParams& p, int len) {
+  return p.B > 1 ? p.chunk : max(64, ((len + p.nsplit - 1) / p.nsplit + 63) / 64 * 64);
+}
+
 template <int D, int MT>
 struct DecCfg {
   static constexpr int ROW = D * 2;                        // bytes of a key
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
   const int len = request_len(p, b);
   if (threadIdx.x == 0 && chunk == 0 && r0 == 0 && hk == 0 && len != p.lens[b])
     record_status(p.status, MCS_ERR_BAD_INDEX, p.lens[b]);
-  const int k0 = chunk * p.chunk, k1 = min(len, k0 + p.chunk);
+  const int keys = chunk_keys(p, len), k0 = chunk * keys, k1 = min(len, k0 + keys);
   if (k0 >= k1 && p.part_o) return;  // nothing of this request: the join does not look here
   // in a cluster every chunk takes part in the join, an empty one with lse = -inf
   const int rows = min(p.g - r0, MT * 16);
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(256) decode_combine(const DecodeParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int head = blockIdx.x % p.Hq, b = blockIdx.x / p.Hq;
   const int len = request_len(p, b);
-  const int chunks = (len + p.chunk - 1) / p.chunk;
+  const int keys = chunk_keys(p, len), chunks = (len + keys - 1) / keys;
   const int parts = p.pre_parts + chunks;
   const size_t own = (static_cast<size_t>(b) * p.Hq + head) * p.nsplit;
   // the prefix's parts lie in packed tiles: request b is token b of the one batch row

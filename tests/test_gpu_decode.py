@@ -264,3 +264,10 @@ def test_calls_back_to_back(mcs, graph):
     for r in runs:
         for name, t in r.items():
             assert torch.equal(t.view(torch.uint8), alone[name].view(torch.uint8)), name
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (40, 40), (33, 1)])
+@pytest.mark.parametrize("C,n", [(20000, 20000), (20000, 19937), (20000, 301), (20000, 1), (20000, 0), (5000, 4990)])
+def test_a_single_request_of_any_length(mcs, Hq, Hkv, C, n):
+    """Its keys are cut by its length, not by the cache's capacity."""
+    run(mcs, 1, Hq, Hkv, C, 64, [n], P=130 if n == 301 else 0, seed=n)
