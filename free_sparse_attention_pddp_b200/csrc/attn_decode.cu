@@ -448,7 +448,8 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t s) {
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     note_launches(1);
-    return cudaLaunchKernelEx(&cfg, decode_kernel<D, MT>, p);
+    const cudaError_t launched = cudaLaunchKernelEx(&cfg, decode_kernel<D, MT>, p);
+    return launched == cudaSuccess ? launched : cudaGetLastError();
   }
   return launch_in_sequence(decode_kernel<D, MT>, static_cast<unsigned>(grid), kThreads, DecCfg<D, MT>::SMEM, s,
                             p.pre_parts > 0, p);

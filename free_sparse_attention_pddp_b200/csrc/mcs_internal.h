@@ -260,7 +260,8 @@ cudaError_t launch_in_sequence(void (*kernel)(P...), unsigned grid, unsigned blo
   cfg.attrs = &at;
   cfg.numAttrs = after ? 1 : 0;
   note_launches(1);
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  return e == cudaSuccess ? e : cudaGetLastError();  // reported here, not to the next caller
 }
 
 }  // namespace mcs
