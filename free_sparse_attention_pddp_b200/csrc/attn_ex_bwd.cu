@@ -27,8 +27,8 @@
 //
 // Four threads work on a row of a tile, 32 of its columns each.
 //
-// What bounds it: the products. 37 heads of 8192 tokens, d = 128: 3.06 ms, 1035
-// TFLOP/s on the formulas' five products, 1450 of the 1684 that a plain product
+// What bounds it: the products. 37 heads of 8192 tokens, d = 128: 3.06 to
+// 3.17 ms, 1000 to 1035 TFLOP/s on the formulas' five products, 1400 to 1450 of the 1684 that a plain product
 // reaches on the seven that run; capped scores 3.9 ms; d = 64 2.25 ms (the
 // exponentials and the roundings of P and dS are as many for half the products).
 #include <algorithm>

@@ -31,10 +31,10 @@
 // What bounds it: a slot's step is a chain of 3700 cycles at d = 128 (softmax
 // 2130, of which the exponentials are 1550 where the special-function unit needs
 // 1083; O += P V and S 512 each; hand-overs 570) and two slots overlap, so the
-// tensor pipe works 2048 of them. 37 heads of 8192 tokens, d = 128: 1.06 ms,
-// 1195 TFLOP/s of the 1684 that a plain product reaches; capped scores 1.50 ms,
-// biased 1.49; d = 64, where the exponentials are as many for half the products,
-// 1.08 ms.
+// tensor pipe works 2048 of them. 37 heads of 8192 tokens, d = 128, on GPUs at
+// their power limit: 1.06 to 1.09 ms, 1165 to 1195 TFLOP/s of the 1684 that a
+// plain product reaches; capped scores 1.50 to 1.67, biased 1.3 to 1.5; d = 64,
+// where the exponentials are as many for half the products, 1.07 to 1.10 ms.
 #include "attn_ex.cuh"
 
 namespace mcs {
