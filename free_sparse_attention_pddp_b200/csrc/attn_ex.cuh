@@ -280,6 +280,11 @@ __device__ __forceinline__ int ordered_job(const ExTile& p, const int* order, in
   return at / jobs * p.Hkv + ch * most + in % heads;
 }
 
+// Test knob: the warp that clears padded rows falls 20 us behind in every tile, which is ten steps.
+__device__ __forceinline__ void hold_cleaner(const ExTile& p) {
+  if (p.debug_flags & 8) __nanosleep(20000);
+}
+
 // Zeroes the rows of a swizzled tile (KB column blocks of 128 rows x 128 bytes)
 // whose document id is negative, so that whatever padding holds (NaN) meets
 // the zero probabilities of its row as zero. One warp; `ids`: 128 document ids.

@@ -397,7 +397,8 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
                          (!start || kk > 0) ? 1u : 0u);
         };
         auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
-        // Q or d_o of list entry j, half h; `pad`: once the padded rows are clear
+        // Q or d_o of list entry j, half h; `pad`: once the padded rows are clear. Of a tile without padding the
+        // clearing warp's word is awaited before its first release only (below), when it has long been given.
         auto ready = [&](uint64_t* full, int j, int h, bool pad) {
           const int s = j % C::NS;
           const bool there = wait(&full[halves ? 2 * s + h : 2 * s], j / C::NS) && (!pad || wait(&qg_ok[s], j / C::NS));
@@ -419,7 +420,8 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
           if (DOC && i + 1 < n) pad = tile_bit(tiles.pads, it.next() - lo);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!(ok = wait(&p_full[h], i))) break;
+            // no stage is released before the clearing warp has left it, so that warp is never a phase behind
+            if (!(ok = wait(&p_full[h], i) && (!DOC || h > 0 || wait(&qg_ok[i % C::NS], i / C::NS)))) break;
             tc_fence_after();
             accumulate(tmem + 256, tmem + h * 64, sdesc_advance(dGm, at + h * 8192), i == 0 && h == 0);
             umma_commit(&g_empty[2 * (i % C::NS) + h]);
@@ -461,6 +463,7 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
                   mbar_wait_warp(&g_full[2 * s + h], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER);
         if (!there) break;
         const int qt = it.next();
+        hold_cleaner(p);
         if (tile_bit(tiles.pads, qt - lo)) {
           const size_t at = static_cast<size_t>(b) * p.Tq + qt;
           zero_padded_rows<C::KB>(sQ + s * C::TILE, p.q_ids + at * 128);
@@ -816,7 +819,8 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
         bool ok = wait(qg_full, 0) && both(0);
         for (int i = 0; ok && i < n; ++i) {
           if (i + 1 < n && !both(i + 1)) break;
-          if (!wait(&ds_full[i & 1], i >> 1)) break;
+          // no stage is released before the clearing warp has left it, so that warp is never a phase behind
+          if (!wait(&ds_full[i & 1], i >> 1) || (DOC && !wait(&k_ok[i % C::NK], i / C::NK))) break;
           tc_fence_after();
           const uint64_t bb = sdesc_advance(dKm, (i % C::NK) * C::TILE);
 #pragma unroll
@@ -844,6 +848,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
         const int s = j % C::NK;
         if (!mbar_wait_warp(&k_full[s], (j / C::NK) & 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
         const int kt = it.next();
+        hold_cleaner(p);
         if (tile_bit(tiles.pads, kt)) {
           const size_t at = static_cast<size_t>(b) * p.Tk + kt;
           zero_padded_rows<C::KB>(sK + s * C::TILE, p.k_ids + at * 128);

@@ -310,37 +310,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_commit(&p_empty[t]);
         };
         auto wait = [&](uint64_t* bar, int k) { return mbar_wait(bar, k & 1, wctx, MCS_WHERE_ATTN_MMA); };
-        // V of list entry j; `pad`: once its padded rows are clear
-        auto v_there = [&](int j, bool pad) {
+        // V of list entry j. Under a document mask, once the warp that clears padded rows is done with it, in tiles
+        // without padding too: no stage is released before that warp has left it, so it is never a phase behind.
+        auto v_there = [&](int j) {
           const int s = j % C::NS;
-          return wait(&v_full[s], j / C::NS) && (!pad || wait(&v_ok[s], j / C::NS));
+          return wait(&v_full[s], j / C::NS) && (!DOC || wait(&v_ok[s], j / C::NS));
         };
-        TileIter it = first, it2 = second;
+        TileIter it = first;
         const int steps = one_tile() ? (n + 1) >> 1 : zip ? max(n0, n1) : n;
         // the slots' list entries of a step
         auto entry0 = [&](int step) { return one_tile() ? 2 * step : zip ? step + min(step, n1) : step; };
         auto entry1 = [&](int step) { return one_tile() ? 2 * step + 1 : zip ? step + min(step + 1, n0) : step; };
         int i0 = 0, i1 = 0;     // the slots' steps
         int behind = -1;        // slot 1's list entry whose O += P V is to come
-        bool behind_pad = false;
         bool ok = wait(q_full, 0);
-        // step's slots (1, 2) and whether their V tiles hold padding (4, 8)
+        // step's slots (1, 2)
         auto look = [&](int step) {
           const int j0 = entry0(step), j1 = entry1(step);
           int f = 0;
           if (DOC && zip) {
-            if (step < n0) f |= tile_bit(tiles.pads, it.next() - lo) ? 5 : 1;
-            if (step < n1) f |= tile_bit(tiles.pads, it2.next() - lo) ? 10 : 2;
-          } else if (DOC) {
+            f = (step < n0 ? 1 : 0) | (step < n1 ? 2 : 0);
+          } else if (DOC && !one_tile()) {
             if (j0 >= n) return 0;
-            int kt = it.next() - lo;
-            if (tile_bit(tiles.pads, kt)) f |= one_tile() ? 4 : 12;
-            if (one_tile()) {
-              f |= 1;
-              if (j1 < n) f |= tile_bit(tiles.pads, it.next() - lo) ? 10 : 2;
-            } else {
-              f |= (tile_bit(tiles.meet, kt) ? 1 : 0) | (tile_bit(tiles.meet2, kt) ? 2 : 0);
-            }
+            const int kt = it.next() - lo;
+            f = (tile_bit(tiles.meet, kt) ? 1 : 0) | (tile_bit(tiles.meet2, kt) ? 2 : 0);
           } else {
             f = (j0 < (one_tile() ? n : n0) ? 1 : 0) | (j1 < (one_tile() || has1 ? n : 0) ? 2 : 0);
           }
@@ -370,14 +363,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             flags = look(step + 1);
             if (prev & 1) {
-              if (!(ok = v_there(p0, prev & 4) && wait(&p_full[0], o0))) break;
+              if (!(ok = v_there(p0) && wait(&p_full[0], o0))) break;
               tc_fence_after();
               issue_o(0, o0, p0);
               if (apart || !(prev & 2)) umma_commit(&v_empty[p0 % C::NS]);
               ++o0;
             }
             if (prev & 2) {
-              if (!(ok = v_there(p1, prev & 8) && wait(&p_full[1], o1))) break;
+              if (!(ok = v_there(p1) && wait(&p_full[1], o1))) break;
               tc_fence_after();
               issue_o(1, o1, p1);
               umma_commit(&v_empty[p1 % C::NS]);
@@ -390,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int step = 0; ok && step <= steps; ++step) {
           const int j0 = entry0(step), j1 = entry1(step);
           const int now = flags;
-          const bool a0 = now & 1, a1 = now & 2, pad0 = now & 4, pad1 = now & 8;
+          const bool a0 = now & 1, a1 = now & 2;
           if (a0) {
             if (!(ok = wait(&k_full[j0 % C::NS], j0 / C::NS))) break;
             tc_fence_after();
@@ -398,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (apart || !a1) umma_commit(&k_empty[j0 % C::NS]);
           }
           if (behind >= 0) {
-            if (!(ok = v_there(behind, behind_pad) && wait(&p_full[1], i1 - 1))) break;
+            if (!(ok = v_there(behind) && wait(&p_full[1], i1 - 1))) break;
             tc_fence_after();
             issue_o(1, i1 - 1, behind);
             umma_commit(&v_empty[behind % C::NS]);
@@ -410,12 +403,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             issue_s(1, j1);
             umma_commit(&k_empty[j1 % C::NS]);
             behind = j1;
-            behind_pad = pad1;
             ++i1;
           }
           flags = look(step + 1);  // beside the softmax that the next product waits for
           if (a0) {
-            if (!(ok = v_there(j0, pad0) && wait(&p_full[0], i0))) break;
+            if (!(ok = v_there(j0) && wait(&p_full[0], i0))) break;
             tc_fence_after();
             issue_o(0, i0, j0);
             if (apart || !a1) umma_commit(&v_empty[j0 % C::NS]);
@@ -440,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = j % C::NS;
         if (!mbar_wait_warp(&v_full[s], (j / C::NS) & 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
         const int kt = it.next();
+        hold_cleaner(p);
         if (tile_bit(tiles.pads, kt - lo)) {
           zero_padded_rows<C::KB>(sV + s * C::TILE, p.k_ids + (static_cast<size_t>(b) * p.Tk + kt) * 128);
           fence_proxy_async_smem();

@@ -18,6 +18,9 @@ extern "C" {
  * Bit 2: mcs_dense at d = 128 runs the one-query-tile kernel instead of the
  * kernel over pairs of query tiles (both compute the same attention; for
  * comparisons).
+ * Bit 3: under a document mask, the warp that clears padded rows of
+ * mcs_dense_ex's and mcs_dense_bwd's tiles waits 20 us before each tile (the
+ * results must not change).
  */
 void mcs_debug_set_flags(int flags);
 

@@ -359,3 +359,29 @@ def test_neighbouring_query_tiles_of_different_documents(mcs, g, d):
         ids[0, 200:203] = -1
         N = ids.shape[1]
         both(mcs, 1, 2 * g, 2, N, N, d, doc_q=ids, doc_k=ids, cap=30.0 * (g - 1), seed=N + g)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,lengths,pads", [(1, 1, (2300,), ()), (1, 1, (2100,), (150, 2099)), (40, 40, (500, 900, 260), (0, 700)),
+                                                 (6, 2, (1300, 30, 760), (1299,))])
+def test_a_slow_clearing_warp_changes_nothing(mcs, Hq, Hkv, lengths, pads, d):
+    """The warp that clears padded rows falls ten steps behind in every tile (debug flag bit 3): the rings wait for it,
+    whether tiles hold padding or not. One tile in both slots, pairs, slots with lists of their own."""
+    from free_sparse_attention_pddp_b200.binding import debug_set_flags
+
+    ids = torch.repeat_interleave(torch.arange(len(lengths)), torch.tensor(lengths))[None].int()
+    ids[0, list(pads)] = -1
+    N = ids.shape[1]
+    q, k, v, d_o = inputs(1, Hq, Hkv, N, N, d, seed=34)
+    for t in (q, k, v, d_o):
+        t[ids.cuda() < 0] = float("nan")
+    ids = ids.cuda()
+    shape = mcs.AttnShape(1, Hq, Hkv, N, N, d)
+    want = run(mcs, shape, q, k, v, d_o, doc_q=ids, doc_k=ids)
+    assert all(torch.isfinite(want[n]).all() for n in ("o", "dq", "dk", "dv"))
+    debug_set_flags(8)
+    try:
+        got = run(mcs, shape, q, k, v, d_o, doc_q=ids, doc_k=ids)
+    finally:
+        debug_set_flags(0)
+    assert all(torch.equal(got[n], want[n]) for n in want)
