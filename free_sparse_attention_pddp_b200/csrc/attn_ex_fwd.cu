@@ -62,7 +62,9 @@ constexpr int kMostCuts = 296;
 // 2^x for x <= 2^21 on the FMA pipe. t = x + 1.5 2^23, rounded down, holds n =
 // floor(x) in its low bits; 2^(x - n) is a polynomial of degree 5 with p(0) = 1,
 // fitted to [0, 1] by iteratively reweighted least squares (relative error at most
-// 8.3e-8); n is added to its exponent. x <= -127 gives exactly 0.
+// 8.3e-8). It is multiplied by 2^n, whose bits are made of n: added to the
+// polynomial's exponent field instead, n would turn a NaN into a number. x < -126
+// gives exactly 0, NaN stays NaN.
 __device__ __forceinline__ void exp2_fma(float& x0, float& x1) {
   asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));  // -127
   asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x1));
@@ -75,11 +77,11 @@ __device__ __forceinline__ void exp2_fma(float& x0, float& x1) {
   p = f2_fma(p, r, f2_pack(.240164444f, .240164444f));
   p = f2_fma(p, r, f2_pack(.693151295f, .693151295f));
   p = f2_fma(p, r, f2_pack(1.f, 1.f));
-  float p0, p1, t0, t1;
-  f2_unpack(p, p0, p1);
+  float t0, t1;
   f2_unpack(t, t0, t1);
-  x0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-  x1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+  const float n0 = __uint_as_float((__float_as_uint(t0) << 23) + 0x3f800000u);
+  const float n1 = __uint_as_float((__float_as_uint(t1) << 23) + 0x3f800000u);
+  f2_unpack(f2_mul(p, f2_pack(n0, n1)), x0, x1);
 }
 
 template <int D>

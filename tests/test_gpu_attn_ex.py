@@ -385,3 +385,26 @@ def test_a_slow_clearing_warp_changes_nothing(mcs, Hq, Hkv, lengths, pads, d):
     finally:
         debug_set_flags(0)
     assert all(torch.equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("opts", [dict(), dict(slopes=[.5, .01]), dict(cap=20.0)], ids=["plain", "biased", "capped"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_key_shows_in_every_row_that_sees_it(mcs, bad, opts, d):
+    """Request b's key b holds a bad element: NaN in o and lse of the rows from b on, whatever column of a tile it
+    lies in, and the rows before it as they were. An infinite score without a cap is such a row too."""
+    if bad == float("inf") and "cap" in opts:
+        pytest.skip("a cap makes a finite score of an infinite product")
+    N = 200
+    q, k, v, _ = inputs(N, 2, 1, N, N, d, seed=35)
+    q[..., 3] = q[..., 3].abs() + 0.5  # so that an infinite element gives +inf
+    slopes = None if "slopes" not in opts else torch.tensor(opts["slopes"], device="cuda")
+    shape = mcs.AttnShape(N, 2, 1, N, N, d, cap=opts.get("cap", 0.0), causal=True)
+    good = run(mcs, shape, q, k, v, slopes=slopes)
+    at = torch.arange(N, device="cuda")
+    k[at, at, 0, 3] = bad
+    got = run(mcs, shape, q, k, v, slopes=slopes)
+    sees = at[None] >= at[:, None]  # [request, row]
+    assert got["o"][sees].isnan().all() and got["lse"].transpose(1, 2)[sees].isnan().all()
+    assert torch.equal(got["o"][~sees], good["o"][~sees])
+    assert torch.equal(got["lse"].transpose(1, 2)[~sees], good["lse"].transpose(1, 2)[~sees])
