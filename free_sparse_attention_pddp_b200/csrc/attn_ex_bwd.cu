@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(256) ex_row_stats(const ExTile p, const uint16
       const size_t at = ((static_cast<size_t>(b) * p.Nq + tok) * p.Hq + head) * D + c * 8;
       const uint4 x = *reinterpret_cast<const uint4*>(o + at), y = *reinterpret_cast<const uint4*>(d_o + at);
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-      if (L > -CUDART_INF_F) {
+      if (L != -CUDART_INF_F) {  // NaN passes on
         nl = -L * kLog2e;
         if (p.slopes) nl = fmaf(-p.slopes[head] * kLog2e, static_cast<float>(t), nl);
 #pragma unroll
@@ -870,7 +870,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
     const bool row_valid = row < rt && tok < p.Nq;
     const float* st = p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
     const float lse = row_valid ? p.lse_in[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok] : -CUDART_INF_F;
-    const float negl = lse > -CUDART_INF_F ? -lse * kLog2e : -CUDART_INF_F, delta = DELTA ? 0.f : st[128 + row];
+    const float negl = lse == -CUDART_INF_F ? lse : -lse * kLog2e, delta = DELTA ? 0.f : st[128 + row];
     uint64_t d2 = 0;  // DELTA: the sum of P dP, over even and odd columns
     const uint64_t negl2 = f2_pack(negl, negl), delta2 = f2_pack(delta, delta);
     const int pos = off + tok;
@@ -973,7 +973,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
       sums[quarter * 128 + row] = even + odd;
       named_barrier_sync<2, 512>();
       if (fin && quarter == 0) {
-        const bool live = negl > -CUDART_INF_F;
+        const bool live = negl != -CUDART_INF_F;  // NaN passes on
         float* out = p.stats_out + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
         out[row] = BIAS && live ? fmaf(-p.slopes[head] * kLog2e, static_cast<float>(row / p.g), negl) : negl;
         out[128 + row] = live ? (sums[row] + sums[128 + row]) + (sums[256 + row] + sums[384 + row]) : 0.f;

@@ -408,3 +408,29 @@ def test_a_bad_key_shows_in_every_row_that_sees_it(mcs, bad, opts, d):
     assert got["o"][sees].isnan().all() and got["lse"].transpose(1, 2)[sees].isnan().all()
     assert torch.equal(got["o"][~sees], good["o"][~sees])
     assert torch.equal(got["lse"].transpose(1, 2)[~sees], good["lse"].transpose(1, 2)[~sees])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("docs", [False, True])
+@pytest.mark.parametrize("N", [200, 600])
+def test_a_bad_row_shows_in_its_gradients(mcs, N, docs, d):
+    """A row whose o and lse are NaN is not an empty row: its dq is NaN, and dk and dv of the keys that it sees."""
+    q, k, v, d_o = inputs(1, 2, 2, N, N, d, seed=36)
+    ids = torch.repeat_interleave(torch.arange(2), torch.tensor([90, N - 90]))[None].int().cuda()
+    opts = dict(doc_q=ids, doc_k=ids) if docs else {}
+    shape = mcs.AttnShape(1, 2, 2, N, N, d, causal=True)
+    good = run(mcs, shape, q, k, v, d_o, **opts)
+    o, lse = good["o"].clone(), good["lse"].clone()
+    o[0, 150, 1], lse[0, 1, 150] = float("nan"), float("nan")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws = mcs.attn_workspace(shape, mcs.MCS_OP_DENSE_BWD)
+    mcs.mcs_dense_bwd(shape, q, k, v, o, lse, d_o, dq, dk, dv, ws, **opts)
+    assert mcs.mcs_poll_status(ws)[0] == 0
+    seen = torch.zeros(N, dtype=torch.bool, device="cuda")
+    seen[90 if docs else 0:151] = True
+    assert dq[0, 150, 1].isnan().all() and dk[0, seen, 1].isnan().all() and dv[0, seen, 1].isnan().all()
+    dq[0, 150, 1] = good["dq"][0, 150, 1]
+    assert torch.equal(dq, good["dq"])
+    for n, t in (("dk", dk), ("dv", dv)):
+        t[0, seen, 1] = good[n][0, seen, 1]
+        assert torch.equal(t, good[n]), n
