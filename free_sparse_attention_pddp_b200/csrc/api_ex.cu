@@ -11,7 +11,6 @@ using namespace mcs;
 namespace {
 
 constexpr int kMaxGroup = 128;            // query heads of one KV head: one 128-row tile holds a token's
-constexpr int kExactDeltaKeys = 256;      // up to so many keys D is summed from P dP (ex_row_stats)
 constexpr int kMaxDocQueryTiles = 1 << 16;  // tiles of a document mask's bitmaps: over query tiles
 constexpr int kMaxDocKeyTiles = 1 << 12;    // and over key tiles (the dQ kernel has 1 KB left for it)
 
@@ -458,6 +457,8 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
   float* stats = reinterpret_cast<float*>(base + w.stats);
   t.stats = stats;
   t.lse_in = lse;
+  t.o_in = static_cast<const uint16_t*>(o);
+  t.do_in = static_cast<const uint16_t*>(d_o);
   if (p.doc_q) {
     int* kid = reinterpret_cast<int*>(base + w.k_ids);
     int* qid = reinterpret_cast<int*>(base + w.q_ids);
@@ -477,10 +478,14 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
       t.k_order = k_order;
     }
   }
-  if (p.Nk <= kExactDeltaKeys) t.stats_out = stats;
-  else if (launch_ex_row_stats(s->d, t, static_cast<const uint16_t*>(o), static_cast<const uint16_t*>(d_o), lse, stats,
-                          stream) != cudaSuccess)
-    return MCS_ERR_CUDA;
+  // every row's D from o, then anew in the first tiles of a causal mask, whose rows see few keys; or, where all rows do
+  // or documents may be short, both from one kernel, tile by tile
+  t.stats_out = stats;
+  const bool any_tile = p.doc_q || p.Nk <= kFewKeys;
+  t.few_tiles = any_tile   ? f.Tq
+                : p.causal ? std::min(f.Tq, std::max(0, kFewKeys - (p.Nk - p.Nq) + f.tpt - 1) / f.tpt)
+                           : 0;
+  if (!any_tile && launch_ex_row_stats(s->d, t, stream) != cudaSuccess) return MCS_ERR_CUDA;
   return ok_or_cuda(launch_ex_bwd(s->d, &tq, &tg, &tk, &tv, t, stream));
 }
 

@@ -141,6 +141,9 @@ struct CapFn {
 constexpr float kTanhP0 = -0.333323412f, kTanhP1 = 0.133081745f, kTanhP2 = -0.0519478787f, kTanhP3 = 0.0151953385f;
 constexpr float kTanhR0 = -0.333318822f, kTanhR1 = 0.132776282f, kTanhR2 = -0.0477941821f;  // degree 2, |x| <= 0.4
 
+// A row that sees at most so many keys takes D from P dP (ex_delta_kernel in attn_ex_bwd.cu).
+constexpr int kFewKeys = 256;
+
 // The tile kernels' view of a call (attn_ex_fwd.cu, attn_ex_bwd.cu).
 struct ExTile {
   int B, Hq, Hkv, g, tpt, Nq, Nk;  // tpt: tokens of a packed query tile
@@ -163,11 +166,13 @@ struct ExTile {
   uint16_t* o;                     // outputs, or the partials of the splits
   float* lse;
   const float* stats;              // backward: [B,Hkv,Tq][2][128], -lse in log2 units and d_o . o
-  const float* lse_in;             // backward: the forward's lse
+  const float* lse_in;             // backward: the forward's lse,
+  const uint16_t *o_in, *do_in;    // its o, and the gradient of o
   int kv_splits;                   // backward: CTAs that share a key tile's queries
   size_t kv_size;                  // elements of dk
   float* part_kv;                  // [2 (dv, dk)][kv_splits][B,Nk,Hkv,d], null unless kv_splits > 1
-  float* stats_out;                // not null: the statistics come from the sweep over the keys
+  float* stats_out;                // where the statistics go
+  int few_tiles;                   // backward: leading query tiles whose rows may see few keys
   uint16_t *dq, *dk, *dv;
   float *part_o, *part_lse;        // [parts][B,Hkv,Tq,128](,d), lse in log2 units
   int* status;
@@ -179,8 +184,7 @@ cudaError_t launch_ex_fwd(int d, const CUtensorMap* tq, const CUtensorMap* tk, c
                           cudaStream_t s);
 cudaError_t launch_ex_combine(int d, const ExTile& p, int parts, cudaStream_t s);
 // packed rows' statistics, then the gradients; tg: the map of d_o
-cudaError_t launch_ex_row_stats(int d, const ExTile& p, const uint16_t* o, const uint16_t* d_o, const float* lse,
-                                float* stats, cudaStream_t s);
+cudaError_t launch_ex_row_stats(int d, const ExTile& p, cudaStream_t s);
 cudaError_t launch_ex_bwd(int d, const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk,
                           const CUtensorMap* tv, const ExTile& p, cudaStream_t s);
 // order of the jobs (of `per` query tiles) and, unless null, of the key tiles: [B jobs], [B Tk]

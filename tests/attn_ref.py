@@ -44,7 +44,8 @@ def attn(q, k, v, d_o=None, scale=None, cap=0.0, slopes=None, pos=None, valid=No
     """q [B,Nq,Hq,d], k, v [B,Nk,Hkv,d] of any type; pos [B or 1, Nq] query positions; valid bool [B,Nq,Nk].
 
     Returns a dict of (value, bound) pairs, fp64: o [B,Nq,Hq,d], lse [B,Hq,Nq] and,
-    with d_o, dq, dk, dv. Rows that no pair needs may hold NaN. exact_d: D is summed from P dP in fp32."""
+    with d_o, dq, dk, dv. Rows that no pair needs may hold NaN. exact_d: D is summed from P dP in fp32, in
+    all rows (True) or in those of a mask [B, Nq]."""
     B, Nq, Hq, d = q.shape
     Nk, Hkv = k.shape[1:3]
     g = Hq // Hkv
@@ -86,8 +87,9 @@ def attn(q, k, v, d_o=None, scale=None, cap=0.0, slopes=None, pos=None, valid=No
         dS = P * (dP - D) * w
         edp = (d + 8) * E * (G.abs() @ V.abs().transpose(-1, -2))
         ed = (G.abs() * (tol_o + (d + 8) * E * o.abs())).sum(-1, keepdim=True)
-        if exact_d:  # dP's and P's errors, and the sum's
-            ed = (P * (edp + Ep * dP.abs())).sum(-1, keepdim=True)
+        if exact_d is not False:  # dP's and P's errors, and the sum's
+            rows = torch.as_tensor(exact_d, device=q.device).expand(B, Nq)[:, None, :, None]
+            ed = torch.where(rows, (P * (edp + Ep * dP.abs())).sum(-1, keepdim=True), ed)
         et = 2.0 ** -20 + (es / cap if cap else 0.0)  # of t
         tol_dS = U * dS.abs() + P * w * (edp + ed + Ep * (dP - D).abs()) + P * (dP - D).abs() * 2 * t.abs() * et
         if not cap:

@@ -434,3 +434,35 @@ def test_a_bad_row_shows_in_its_gradients(mcs, N, docs, d):
     for n, t in (("dk", dk), ("dv", dv)):
         t[0, seen, 1] = good[n][0, seen, 1]
         assert torch.equal(t, good[n]), n
+
+
+def few_keys(mcs, B, Hq, Hkv, Nq, Nk, d, gain, seed, causal=False, prefix=None, ids=None, cap=0.0, slopes=None):
+    """The gradients of rows that see at most 256 keys are held to the bound without o's rounding, row by row."""
+    q, k, v, d_o = inputs(B, Hq, Hkv, Nq, Nk, d, seed, gain)
+    dev = lambda x, t: None if x is None else torch.as_tensor(x, dtype=t).cuda().contiguous()  # noqa: E731
+    prefix, slopes, doc_k = dev(prefix, torch.int32), dev(slopes, torch.float32), dev(ids, torch.int32)
+    doc_q = None if ids is None else doc_k[:, Nk - Nq:].contiguous()
+    shape = mcs.AttnShape(B, Hq, Hkv, Nq, Nk, d, cap=cap, causal=causal)
+    got = run(mcs, shape, q, k, v, d_o, slopes=slopes, prefix=prefix, doc_q=doc_q, doc_k=doc_k)
+    valid = attn_ref.valid_mask(B, Nq, Nk, causal, prefix, doc_q, doc_k, "cuda")
+    few = valid.sum(-1) <= 256
+    assert few.any()
+    want = attn_ref.attn(q, k, v, d_o, cap=cap, slopes=slopes, valid=valid, exact_d=few)
+    for name in ("lse", "o", "dv", "dk", "dq"):
+        attn_ref.check(got[name], want[name], name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gain", [2.0, 6.0])
+def test_few_keys_of_a_row_in_a_long_call(mcs, gain, d):
+    """Short documents packed into long rows, alone, beside long ones in one tile and interleaved; the first rows of
+    causal masks; prefixes on both sides of 256."""
+    few_keys(mcs, 1, 6, 2, 1500, 1500, d, gain, 41, ids=packed_ids(1, 1500, 16, 5, 40))
+    mixed = torch.repeat_interleave(torch.arange(9), torch.tensor([3, 900, 7, 1, 500, 260, 16, 256, 257]))[None]
+    few_keys(mcs, 1, 2, 2, mixed.shape[1], mixed.shape[1], d, gain, 42, ids=mixed)
+    few_keys(mcs, 1, 3, 1, mixed.shape[1], mixed.shape[1], d, gain, 43, ids=mixed, causal=True, cap=30.0)
+    few_keys(mcs, 2, 2, 1, 1900, 2000, d, gain, 44, ids=packed_ids(2, 2000, 40, 6, 70, shuffle=True))
+    few_keys(mcs, 1, 4, 4, 1100, 1100, d, gain, 45, causal=True)
+    few_keys(mcs, 3, 5, 1, 700, 700, d, gain, 46, causal=True, prefix=[0, 255, 257], slopes=[.01 * h for h in range(5)])
+    few_keys(mcs, 1, 2, 2, 300, 500, d, gain, 47, causal=True)
+    few_keys(mcs, 1, 2, 1, 800, 300, d, gain, 48, causal=True, cap=30.0)
