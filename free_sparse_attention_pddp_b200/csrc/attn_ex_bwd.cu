@@ -287,7 +287,7 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
     for (int j = j0; j < j1 && ok; ++j) {
       const int s = j % C::NS;
       const int qt = it.next();
-      if ((p.debug_flags & 1) && j == 0) continue;  // test knob: never deliver tile 0
+      if ((p.debug_flags & 17) && j == 0) continue;  // test knob: never deliver tile 0
       const uint32_t parity = ((j / C::NS) & 1) ^ 1;
       const float* stats = p.stats + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
       uint8_t* sS = smem + C::OFF_STAT + s * 1024;
@@ -771,7 +771,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
       const int sk = j % C::NK, sv = j % C::NV;
       const int kt = it.next();
       if (j >= C::NK && !mbar_wait(&k_empty[sk], ((j / C::NK) & 1) ^ 1, wctx, MCS_WHERE_ATTN_PRODUCER)) break;
-      if (!((p.debug_flags & 1) && j == 0)) {  // test knob: never deliver tile 0
+      if (!((p.debug_flags & (DELTA ? 65 : 33)) && j == 0)) {  // test knob: never deliver tile 0
         mbar_arrive_expect_tx(&k_full[sk], C::TILE);
 #pragma unroll
         for (int kb = 0; kb < C::KB; ++kb)

@@ -466,3 +466,31 @@ def test_few_keys_of_a_row_in_a_long_call(mcs, gain, d):
     few_keys(mcs, 3, 5, 1, 700, 700, d, gain, 46, causal=True, prefix=[0, 255, 257], slopes=[.01 * h for h in range(5)])
     few_keys(mcs, 1, 2, 2, 300, 500, d, gain, 47, causal=True)
     few_keys(mcs, 1, 2, 1, 800, 300, d, gain, 48, causal=True, cap=30.0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("docs", [False, True])
+@pytest.mark.parametrize("flag,Nk", [(16, 300), (32, 300), (64, 200)], ids=["key_tiles", "query_tiles", "few_keys"])
+def test_a_load_that_never_arrives_in_one_kind_of_gradient_cta(mcs, flag, Nk, docs, d):
+    """Only one kind of CTA misses its tile: it reports, and what the others compute is right."""
+    from free_sparse_attention_pddp_b200.binding import debug_set_flags
+
+    q, k, v, d_o = inputs(1, 2, 1, 140, Nk, d, seed=37)
+    shape = mcs.AttnShape(1, 2, 1, 140, Nk, d)
+    ids = dict(doc_q=torch.zeros(1, 140, dtype=torch.int32, device="cuda"),
+               doc_k=torch.zeros(1, Nk, dtype=torch.int32, device="cuda")) if docs else {}
+    want = run(mcs, shape, q, k, v, d_o, **ids)
+    dq, dk, dv = (torch.full_like(t, 7.0) for t in (q, k, v))
+    ws = mcs.attn_workspace(shape, mcs.MCS_OP_DENSE_BWD)
+    debug_set_flags(flag)
+    try:
+        mcs.mcs_dense_bwd(shape, q, k, v, want["o"], want["lse"], d_o, dq, dk, dv, ws, **ids)
+        assert mcs.mcs_poll_status(ws)[0] == 4  # MCS_ERR_TIMEOUT
+    finally:
+        debug_set_flags(0)
+    if flag == 16:
+        assert torch.equal(dq, want["dq"]) and (dk == 7).all() and (dv == 7).all()
+    if flag == 32:
+        assert torch.equal(dk, want["dk"]) and torch.equal(dv, want["dv"]) and (dq == 7).all()
+    again = run(mcs, shape, q, k, v, d_o, **ids)
+    assert all(torch.equal(again[n], want[n]) for n in want)

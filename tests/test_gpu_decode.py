@@ -271,3 +271,32 @@ def test_calls_back_to_back(mcs, graph):
 def test_a_single_request_of_any_length(mcs, Hq, Hkv, C, n):
     """Its keys are cut by its length, not by the cache's capacity."""
     run(mcs, 1, Hq, Hkv, C, 64, [n], P=130 if n == 301 else 0, seed=n)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_load_of_the_prefix_that_never_arrives_is_reported(mcs, d):
+    """The prefix's producer withholds its first tile (debug flag bit 0): the bounded waits run out, the status says
+    so, and the next call computes."""
+    from free_sparse_attention_pddp_b200.binding import debug_set_flags
+
+    g = torch.Generator(device="cuda").manual_seed(10)
+    B, Hq, Hkv, C, P = 3, 4, 2, 40, 300
+    q, kp, vp = rand(g, B, Hq, d), rand(g, P, Hkv, d), rand(g, P, Hkv, d)
+    k, v = rand(g, B, C, Hkv, d), rand(g, B, C, Hkv, d)
+    lens = torch.tensor([40, 0, 7], dtype=torch.int32, device="cuda")
+    shape = mcs.DecodeShape(B, Hq, Hkv, C, d, P=P)
+    ws = mcs.decode_workspace(shape)
+
+    def call(status):
+        o, lse = torch.empty_like(q), torch.empty(B, Hq, device="cuda")
+        mcs.mcs_decode_shared(shape, q, kp, vp, k, v, lens, o, lse, ws)
+        assert mcs.mcs_poll_status(ws)[0] == status
+        return o, lse
+
+    want = call(0)
+    debug_set_flags(1)
+    try:
+        call(4)  # MCS_ERR_TIMEOUT
+    finally:
+        debug_set_flags(0)
+    assert all(torch.equal(x, y) for x, y in zip(call(0), want))
