@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const DecodeParams 
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = m * 16 + (lane >> 2) + e * 8;
-      slope[m][e] = p.slopes && r < rows ? p.slopes[head0 + r] * kLog2e : 0.f;
+      slope[m][e] = p.slopes && r < rows ? slope_of(p.slopes, head0 + r) * kLog2e : 0.f;
+      if (p.slopes && r < rows) check_slope(p.slopes, head0 + r, p.status);
     }
   float o[MT][NT][4] = {};
   float mx[MT][2], l[MT][2] = {};

@@ -246,6 +246,18 @@ __device__ __forceinline__ uint64_t cap_slope2(uint64_t y, const CapFn& f) {
   return f2_fma(f2_mul(y, f2_pack(f.neg_icl2, f.neg_icl2)), y, f2_pack(1.f, 1.f));
 }
 
+// A head's slope, within +-64. The tiles add the bias as slope (c - base) with the two products rounded by themselves
+// (add_bias below, the statistics of dK/dV), which leaves up to 2^-15 |slope| in a score, 2^-9 at the bound; and
+// within it no distance makes the bias infinite.
+constexpr float kMaxSlope = 64.f;
+__device__ __forceinline__ float slope_of(const float* slopes, int head) {
+  return fminf(fmaxf(slopes[head], -kMaxSlope), kMaxSlope);
+}
+// Reports a slope outside the bound, or NaN.
+__device__ __forceinline__ void check_slope(const float* slopes, int head, int* status) {
+  if (!(fabsf(slopes[head]) <= kMaxSlope)) record_status(status, MCS_ERR_INVALID_ARG, head);
+}
+
 // Distance bias of a row: s[c] <- s[c] - slope |base - c| - r, where `base` is the
 // distance at c = 0 and the returned r is the same for the whole row. Where the
 // warp's distances all have one sign the bias is linear in c, and r = -slope base

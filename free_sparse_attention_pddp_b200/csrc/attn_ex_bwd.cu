@@ -186,7 +186,7 @@ __device__ __forceinline__ void row_stats(const ExTile& p, int bh, int qt) {
       const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
       if (L != -CUDART_INF_F) {  // NaN passes on
         nl = -L * kLog2e;
-        if (p.slopes) nl = fmaf(-p.slopes[head] * kLog2e, static_cast<float>(t), nl);
+        if (p.slopes) nl = fmaf(-slope_of(p.slopes, head) * kLog2e, static_cast<float>(t), nl);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
@@ -360,7 +360,7 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
     tmem_relinquish();
   }
   if (threadIdx.x < 128) {
-    row_slope[threadIdx.x] = p.slopes ? p.slopes[hk * p.g + threadIdx.x % p.g] * kLog2e : 0.f;
+    row_slope[threadIdx.x] = p.slopes ? slope_of(p.slopes, hk * p.g + threadIdx.x % p.g) * kLog2e : 0.f;
     row_tok[threadIdx.x] = static_cast<float>(threadIdx.x / p.g);
   }
   if (rt < 128) {
@@ -938,7 +938,8 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
     const int lim_all = limit(off + qt * p.tpt);
     const int my_doc = DOC ? p.q_ids[(static_cast<size_t>(b) * p.Tq + qt) * 128 + row] : 0;  // padding: -2
     const float mul = p.mul;
-    const float slope = BIAS && row_valid ? p.slopes[head] * kLog2e / mul : 0.f;
+    const float slope = BIAS && row_valid ? slope_of(p.slopes, head) * kLog2e / mul : 0.f;
+    if (BIAS && row_valid) check_slope(p.slopes, head, p.status);
     const uint64_t mul2 = f2_pack(mul, mul);
     TileIter it = first;
     bool ok = true;
@@ -1035,7 +1036,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
       if (fin && quarter == 0) {
         const bool live = negl != -CUDART_INF_F;  // NaN passes on
         float* out = p.stats_out + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
-        out[row] = BIAS && live ? fmaf(-p.slopes[head] * kLog2e, static_cast<float>(row / p.g), negl) : negl;
+        out[row] = BIAS && live ? fmaf(-slope_of(p.slopes, head) * kLog2e, static_cast<float>(row / p.g), negl) : negl;
         out[128 + row] = live ? (sums[row] + sums[128 + row]) + (sums[256 + row] + sums[384 + row]) : 0.f;
       }
     } else if (fin) {

@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int my_doc = DOC && row_valid ? p.doc_q[static_cast<size_t>(b) * p.Nq + tok] : -2;
     if (my_doc < 0) my_doc = -2;  // a padded query matches no key
     const float mul = p.mul;  // what turns a score into log2 units
-    const float slope = BIAS && row_valid ? p.slopes[head] * kLog2e / mul : 0.f;
+    const float slope = BIAS && row_valid ? slope_of(p.slopes, head) * kLog2e / mul : 0.f;
+    if (BIAS && row_valid) check_slope(p.slopes, head, p.status);
     const uint64_t mul2 = f2_pack(mul, mul);
     // the words of this row and half, and of the other half
     const uint32_t my_max = smem_u32(smem + C::OFF_MAX) + ((t * 2 + half) * 128 + row) * 8;

@@ -58,7 +58,7 @@ extern "C" {
 
 typedef enum mcs_status {
   MCS_OK = 0,
-  MCS_ERR_INVALID_ARG = 1,  /* null pointer, bad size, misalignment, small workspace */
+  MCS_ERR_INVALID_ARG = 1,  /* null pointer, bad size, misalignment, small workspace; a slope (on poll) */
   MCS_ERR_UNSUPPORTED = 2,  /* d not in {64,128}, group != 128, no sm_100 device   */
   MCS_ERR_CUDA = 3,         /* a CUDA runtime/driver call failed                   */
   MCS_ERR_TIMEOUT = 4,      /* a bounded device wait expired (reported on poll)    */
@@ -263,7 +263,9 @@ typedef struct mcs_attn_shape {
 
 /* Device arrays, each nullable; 4-byte aligned. Constants of the call: they get no gradient. */
 typedef struct mcs_attn_opts {
-  const float* slopes;   /* fp32 [Hq]: distance bias, finite */
+  const float* slopes;   /* fp32 [Hq]: distance bias, each within +-64 (one outside, or NaN, is recorded as
+                            MCS_ERR_INVALID_ARG in ws and acts as a bound); a score carries a rounding of up to
+                            2^-15 of its size */
   const int32_t* prefix; /* int32 [B]: keys j < prefix[b] are valid to every query (needs MCS_ATTN_CAUSAL);
                             values outside [0, Nk] act as the nearest bound */
   const int32_t* doc_q;  /* int32 [B, Nq] and */
@@ -298,7 +300,8 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* shape, const mcs_attn_opts* opts,
  * One token per request over a cache, with the scores of mcs_dense_ex (cap and
  * distance bias). q, o: bf16 [B, Hq, d]; k, v: the caches, bf16 [B, C, Hkv, d];
  * lens: int32 [B], the valid keys of each request (its newest token's key and
- * value included); lse (nullable): fp32 [B, Hq]; slopes (nullable): fp32 [Hq].
+ * value included); lse (nullable): fp32 [B, Hq]; slopes (nullable): fp32 [Hq],
+ * as in mcs_attn_opts.
  * The query of request b stands at position P + lens[b] - 1. Cache rows from
  * lens[b] on are never used and may hold anything. lens[b] == 0 with P == 0
  * gives o = 0 and lse = -inf. A length outside [0, C] is recorded as

@@ -40,12 +40,13 @@ def valid_mask(B, Nq, Nk, causal=False, prefix=None, doc_q=None, doc_k=None, dev
     return ok
 
 
-def attn(q, k, v, d_o=None, scale=None, cap=0.0, slopes=None, pos=None, valid=None, exact_d=False):
+def attn(q, k, v, d_o=None, scale=None, cap=0.0, slopes=None, pos=None, valid=None, exact_d=False, slope_error=0.0):
     """q [B,Nq,Hq,d], k, v [B,Nk,Hkv,d] of any type; pos [B or 1, Nq] query positions; valid bool [B,Nq,Nk].
 
     Returns a dict of (value, bound) pairs, fp64: o [B,Nq,Hq,d], lse [B,Hq,Nq] and,
     with d_o, dq, dk, dv. Rows that no pair needs may hold NaN. exact_d: D is summed from P dP in fp32, in
-    all rows (True) or in those of a mask [B, Nq]."""
+    all rows (True) or in those of a mask [B, Nq].
+    slope_error: what a score may be off by, times its head's slope."""
     B, Nq, Hq, d = q.shape
     Nk, Hkv = k.shape[1:3]
     g = Hq // Hkv
@@ -67,6 +68,8 @@ def attn(q, k, v, d_o=None, scale=None, cap=0.0, slopes=None, pos=None, valid=No
         s = s - slopes.double()[None, :, None, None] * dist[:, None]
     ok = valid[:, None]
     es = ex + 2.0 ** -20 * (1 + s.abs())
+    if slope_error:
+        es = es + slope_error * slopes.double().abs()[None, :, None, None]
     s = s.masked_fill(~ok, -math.inf)
     Es = es.masked_fill(~ok, 0.0).amax(-1)
     lse = torch.logsumexp(s, -1)

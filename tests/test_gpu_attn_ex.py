@@ -494,3 +494,42 @@ def test_a_load_that_never_arrives_in_one_kind_of_gradient_cta(mcs, flag, Nk, do
         assert torch.equal(dk, want["dk"]) and torch.equal(dv, want["dv"]) and (dq == 7).all()
     again = run(mcs, shape, q, k, v, d_o, **ids)
     assert all(torch.equal(again[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal,mean", [(False, 0), (True, 0), (False, 1), (True, 5), (False, 90)])
+def test_steep_slopes(mcs, causal, mean, d):
+    """Slopes up to the bound, with rows that see near keys only. A score may be off by 2^-15 of the slope: in a tile of
+    128 rows or 64 keys slope times row (or key) and slope times base are rounded by themselves, at most four
+    roundings of 2^-24 of 128 slopes."""
+    N, slopes = 300, torch.tensor([64.0, -64.0, 30.0, -7.0], device="cuda")
+    q, k, v, d_o = inputs(1, 4, 2, N, N, d, seed=38)
+    ids = packed_ids(1, N, mean, 9).cuda() if mean else None
+    shape = mcs.AttnShape(1, 4, 2, N, N, d, causal=causal)
+    got = run(mcs, shape, q, k, v, d_o, slopes=slopes, doc_q=ids, doc_k=ids)
+    valid = attn_ref.valid_mask(1, N, N, causal, None, ids, ids, "cuda")
+    want = attn_ref.attn(q, k, v, d_o, slopes=slopes, valid=valid, exact_d=valid.sum(-1) <= 256, slope_error=2.0 ** -15)
+    for name in ("lse", "o", "dv", "dk", "dq"):
+        attn_ref.check(got[name], want[name], name)
+
+
+@pytest.mark.parametrize("bad", [65.0, -1e38, float("inf"), float("nan")])
+def test_a_slope_out_of_range_is_reported(mcs, bad):
+    q, k, v, d_o = inputs(1, 2, 2, 100, 300, 64, seed=39)
+    slopes = torch.tensor([0.5, bad], device="cuda")
+    shape = mcs.AttnShape(1, 2, 2, 100, 300, 64)
+    o, lse = torch.empty_like(q), torch.empty(1, 2, 100, device="cuda")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws, wb = (mcs.attn_workspace(shape, op) for op in (mcs.MCS_OP_DENSE_EX, mcs.MCS_OP_DENSE_BWD))
+    mcs.mcs_dense_ex(shape, q, k, v, o, lse, ws, slopes=slopes)
+    mcs.mcs_dense_bwd(shape, q, k, v, o, lse, d_o, dq, dk, dv, wb, slopes=slopes)
+    lens = torch.tensor([300], dtype=torch.int32, device="cuda")
+    one, shared = mcs.DecodeShape(1, 2, 2, 300, 64), mcs.DecodeShape(1, 2, 2, 300, 64, P=300)
+    w1, w2 = mcs.decode_workspace(one), mcs.decode_workspace(shared)
+    qt, ot = q[:, 0].contiguous(), torch.empty(1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    mcs.mcs_decode(one, qt, k, v, lens, ot, None, w1, slopes=slopes)
+    mcs.mcs_decode_shared(shared, qt, k[0], v[0], k, v, lens, ot, None, w2, slopes=slopes)
+    for w in (ws, wb, w1, w2):
+        status, info = mcs.mcs_poll_status(w)
+        assert (status, info[1]) == (1, 1)  # MCS_ERR_INVALID_ARG, head 1
+    assert torch.isfinite(o).all() and torch.isfinite(ot).all()
