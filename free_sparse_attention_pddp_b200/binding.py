@@ -256,8 +256,8 @@ def _refuse(what, name, t, dtype, shape):
 
 
 def _fits(what, ws, *tensors):
-    """Refuses tensors that are not what the kernels read: each (name, tensor, dtype, shape); None passes. All lie
-    on the current CUDA device, whose index is returned."""
+    """Refuses tensors that are not what the kernels read: each (name, tensor, dtype, shape); None passes, which the
+    library refuses where it needs the tensor. All lie on the current CUDA device, whose index is returned."""
     import torch
 
     dev = ws.get_device()
@@ -303,7 +303,7 @@ def mcs_dense_ex(shape, q, k, v, o, lse, ws, slopes=None, prefix=None, doc_q=Non
     dev = _fits("mcs_dense_ex", ws, ("q", q, bf16, qs), ("k", k, bf16, ks), ("v", v, bf16, ks), ("o", o, bf16, qs),
                 ("lse", lse, torch.float32, (s.B, s.Hq, s.Nq)))
     opts = _opts("mcs_dense_ex", s, ws, slopes, prefix, doc_q, doc_k)
-    _check(load().mcs_dense_ex(ctypes.byref(s), opts, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+    _check(load().mcs_dense_ex(ctypes.byref(s), opts, _at(q), _at(k), _at(v), _at(o),
                                _at(lse), ws.data_ptr(), ws.numel(), _on(stream, dev)), "mcs_dense_ex")
 
 
@@ -318,8 +318,8 @@ def mcs_dense_bwd(shape, q, k, v, o, lse, d_o, dq, dk, dv, ws, slopes=None, pref
                 ("lse", lse, torch.float32, (s.B, s.Hq, s.Nq)), ("d_o", d_o, bf16, qs), ("dq", dq, bf16, qs),
                 ("dk", dk, bf16, ks), ("dv", dv, bf16, ks))
     opts = _opts("mcs_dense_bwd", s, ws, slopes, prefix, doc_q, doc_k)
-    _check(load().mcs_dense_bwd(ctypes.byref(s), opts, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                _at(lse), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws.data_ptr(),
+    _check(load().mcs_dense_bwd(ctypes.byref(s), opts, _at(q), _at(k), _at(v), _at(o),
+                                _at(lse), _at(d_o), _at(dq), _at(dk), _at(dv), ws.data_ptr(),
                                 ws.numel(), _on(stream, dev)), "mcs_dense_bwd")
 
 
@@ -332,8 +332,8 @@ def mcs_decode(shape, q, k, v, lens, o, lse, ws, slopes=None, stream=None):
     dev = _fits("mcs_decode", ws, ("q", q, bf16, qs), ("k", k, bf16, cs), ("v", v, bf16, cs),
                 ("lens", lens, torch.int32, (s.B,)), ("o", o, bf16, qs), ("lse", lse, f32, (s.B, s.Hq)),
                 ("slopes", slopes, f32, (s.Hq,)))
-    _check(load().mcs_decode(ctypes.byref(s), q.data_ptr(), k.data_ptr(), v.data_ptr(), lens.data_ptr(), _at(slopes),
-                             o.data_ptr(), _at(lse), ws.data_ptr(), ws.numel(), _on(stream, dev)), "mcs_decode")
+    _check(load().mcs_decode(ctypes.byref(s), _at(q), _at(k), _at(v), _at(lens), _at(slopes),
+                             _at(o), _at(lse), ws.data_ptr(), ws.numel(), _on(stream, dev)), "mcs_decode")
 
 
 def mcs_decode_shared(shape, q, kp, vp, k, v, lens, o, lse, ws, slopes=None, stream=None):
@@ -345,8 +345,8 @@ def mcs_decode_shared(shape, q, kp, vp, k, v, lens, o, lse, ws, slopes=None, str
     dev = _fits("mcs_decode_shared", ws, ("q", q, bf16, qs), ("kp", kp, bf16, ps), ("vp", vp, bf16, ps),
                 ("k", k, bf16, cs), ("v", v, bf16, cs), ("lens", lens, torch.int32, (s.B,)), ("o", o, bf16, qs),
                 ("lse", lse, f32, (s.B, s.Hq)), ("slopes", slopes, f32, (s.Hq,)))
-    _check(load().mcs_decode_shared(ctypes.byref(s), q.data_ptr(), kp.data_ptr(), vp.data_ptr(), k.data_ptr(),
-                                    v.data_ptr(), lens.data_ptr(), _at(slopes), o.data_ptr(), _at(lse), ws.data_ptr(),
+    _check(load().mcs_decode_shared(ctypes.byref(s), _at(q), _at(kp), _at(vp), _at(k),
+                                    _at(v), _at(lens), _at(slopes), _at(o), _at(lse), ws.data_ptr(),
                                     ws.numel(), _on(stream, dev)), "mcs_decode_shared")
 
 

@@ -533,3 +533,22 @@ def test_a_slope_out_of_range_is_reported(mcs, bad):
         status, info = mcs.mcs_poll_status(w)
         assert (status, info[1]) == (1, 1)  # MCS_ERR_INVALID_ARG, head 1
     assert torch.isfinite(o).all() and torch.isfinite(ot).all()
+
+
+def test_missing_tensors_are_refused(mcs):
+    """None in the place of a tensor that a call needs is refused like any other argument."""
+    q, k, v, d_o = inputs(1, 2, 2, 10, 30, 64, seed=40)
+    lse = torch.empty(1, 2, 10, device="cuda")
+    shape = mcs.AttnShape(1, 2, 2, 10, 30, 64)
+    ws, wb = (mcs.attn_workspace(shape, op) for op in (mcs.MCS_OP_DENSE_EX, mcs.MCS_OP_DENSE_BWD))
+    lens = torch.tensor([30], dtype=torch.int32, device="cuda")
+    one, shared = mcs.DecodeShape(1, 2, 2, 30, 64), mcs.DecodeShape(1, 2, 2, 30, 64, P=30)
+    qt, wd = q[:, 0].contiguous(), mcs.decode_workspace(shared)
+    for call, args, tail in ((lambda *a: mcs.mcs_dense_ex(shape, *a), (q, k, v, q), (lse, ws)),
+                             (lambda *a: mcs.mcs_dense_bwd(shape, *a), (q, k, v, q, lse, d_o, q, k, v), (wb,)),
+                             (lambda *a: mcs.mcs_decode(one, *a), (qt, k, v, lens, qt), (None, wd)),
+                             (lambda *a: mcs.mcs_decode_shared(shared, *a), (qt, k[0], v[0], k, v, lens, qt), (None, wd))):
+        for i in range(len(args)):
+            with pytest.raises(mcs.MCSError) as e:
+                call(*args[:i], None, *args[i + 1:], *tail)
+            assert e.value.code == 1
