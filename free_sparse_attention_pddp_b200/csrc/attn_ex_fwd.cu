@@ -62,7 +62,7 @@ constexpr int kMostCuts = 296;
 // 2^x for x <= 2^21 on the FMA pipe. t = x + 1.5 2^23, rounded down, holds n =
 // floor(x) in its low bits; 2^(x - n) is a polynomial of degree 5 with p(0) = 1,
 // fitted to [0, 1] by iteratively reweighted least squares (relative error at most
-// 8.3e-8). It is multiplied by 2^n, whose bits are made of n: added to the
+// 9.5e-8). It is multiplied by 2^n, whose bits are made of n: added to the
 // polynomial's exponent field instead, n would turn a NaN into a number. x < -126
 // gives exactly 0, NaN stays NaN.
 __device__ __forceinline__ void exp2_fma(float& x0, float& x1) {
