@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "mcs_internal.h"
 
@@ -22,7 +23,7 @@ bool finite(float x) { return x == x && !isinf(x); }
 mcs_status check_heads(int Hq, int Hkv, int d, float scale, float cap) {
   if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1) return MCS_ERR_INVALID_ARG;
   if (!finite(scale) || (scale > 0.f && (scale < 1e-12f || scale > 1e12f))) return MCS_ERR_INVALID_ARG;
-  if (!finite(cap) || cap < 0.f || (cap > 0.f && cap < 1e-6f)) return MCS_ERR_INVALID_ARG;
+  if (!finite(cap) || cap < 0.f || (cap > 0.f && cap < 1e-6f) || cap > 1e20f) return MCS_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return MCS_ERR_UNSUPPORTED;
   if (Hq / Hkv > kMaxGroup) return MCS_ERR_UNSUPPORTED;
   return MCS_OK;
@@ -58,22 +59,28 @@ float scale_of(float scale, int d) { return scale > 0.f ? scale : static_cast<fl
 
 CapFn cap_fn(float scale, float cap) {
   CapFn f{};
+  const double ratio = static_cast<double>(scale) / cap, cl = cap * 1.4426950408889634074;
   if (!(cap > 0.f)) return f;
   f.on = 1;
-  const double k = static_cast<double>(scale) / cap, cl = cap * 1.4426950408889634074;
-  f.k2 = static_cast<float>(2.0 * k * 1.4426950408889634074);
   f.cl = static_cast<float>(cl);
+  f.icl = static_cast<float>(1.0 / cl);
   const double p3[5] = {1.0, kTanhP0, kTanhP1, kTanhP2, kTanhP3}, p2[4] = {1.0, kTanhR0, kTanhR1, kTanhR2};
-  bool fits = true;
-  double pow = cl * k;
-  for (int i = 0; i < 5; ++i, pow *= k * k) {
-    f.a[i] = static_cast<float>(p3[i] * pow);
-    fits = fits && finite(f.a[i]);
-    if (i < 4) f.b[i] = static_cast<float>(p2[i] * pow);
-  }
-  f.z2 = fits ? static_cast<float>((0.4 / k) * (0.4 / k)) : -1.f;
-  f.z3 = fits ? static_cast<float>((0.625 / k) * (0.625 / k)) : -1.f;
-  f.neg_icl2 = static_cast<float>(-1.0 / (cl * cl));
+  auto coefficients = [&](double pre) {  // false: one of them is no normal fp32 number
+    const double k = ratio / pre;
+    f.pre = static_cast<float>(pre);
+    f.k2 = static_cast<float>(2.0 * k * 1.4426950408889634074);
+    f.z2 = static_cast<float>((0.4 / k) * (0.4 / k));
+    f.z3 = static_cast<float>((0.625 / k) * (0.625 / k));
+    bool normal = std::isfinite(f.z3);
+    double pow = cl * k;
+    for (int i = 0; i < 5; ++i, pow *= k * k) {
+      f.a[i] = static_cast<float>(p3[i] * pow);
+      normal = normal && std::isnormal(f.a[i]);
+      if (i < 4) f.b[i] = static_cast<float>(p2[i] * pow);
+    }
+    return normal;
+  };
+  if (!coefficients(1.0)) coefficients(ldexp(1.0, ilogb(ratio) + 1));
   return f;
 }
 

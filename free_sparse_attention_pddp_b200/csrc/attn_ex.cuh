@@ -183,8 +183,8 @@ struct TileBits {
 };
 __device__ __forceinline__ bool tile_bit(uint32_t bits, int i) { return (lds32(bits + (i >> 5) * 4) >> (i & 31)) & 1u; }
 
-// s[c] <- cap log2(e) tanh(k s[c]), the capped score in log2 units, in place.
-// |k s| <= 0.625: s Q(s^2) with Q from x + x z P(z), z = x^2, P of degree 3
+// s[c] <- cap log2(e) tanh(k s[c]), the capped score in log2 units, in place (s times
+// f.pre first, where that is not 1). |k s| <= 0.625: s Q(s^2) with Q from x + x z P(z), z = x^2, P of degree 3
 // fitted to (tanh(x)/x - 1)/z by iteratively reweighted least squares on the
 // relative error of tanh (1.3e-7 at most); up to 0.4 degree 2 is as exact. The
 // factors k and cap log2(e) are in Q's coefficients: six (five) packed FMAs per
@@ -201,6 +201,10 @@ __device__ __forceinline__ float cap_far(float s, const CapFn& f) {
 template <int N>
 __device__ __forceinline__ void cap_scores(float* s, const CapFn& f) {
   constexpr int W = N < 16 ? N : 16;
+  if (f.pre != 1.f) {
+#pragma unroll
+    for (int c = 0; c < N; ++c) s[c] *= f.pre;
+  }
 #pragma unroll
   for (int c0 = 0; c0 < N; c0 += W) {
     float* v = s + c0;
@@ -241,9 +245,15 @@ __device__ __forceinline__ void cap_scores(float* s, const CapFn& f) {
   }
 }
 
-// 1 - tanh^2 from a capped score
+// tanh^2 - 1 from a capped score: minus the cap's slope, so that no square of the cap is needed
 __device__ __forceinline__ uint64_t cap_slope2(uint64_t y, const CapFn& f) {
-  return f2_fma(f2_mul(y, f2_pack(f.neg_icl2, f.neg_icl2)), y, f2_pack(1.f, 1.f));
+  const uint64_t t = f2_mul(y, f2_pack(f.icl, f.icl));
+  return f2_fma(t, t, f2_pack(-1.f, -1.f));
+}
+// dP - D; its negative beside the cap's negative slope
+template <bool CAP>
+__device__ __forceinline__ uint64_t dp_less_d(uint64_t dp, uint64_t d) {
+  return CAP ? f2_sub(d, dp) : f2_sub(dp, d);
 }
 
 // A head's slope, within +-64. The tiles add the bias as slope (c - base) with the two products rounded by themselves

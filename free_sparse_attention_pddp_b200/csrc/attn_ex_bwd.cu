@@ -524,8 +524,8 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
         break;
       }
       tc_fence_after();
-      float pv[32];  // score, P, then P (1 - t^2)
-      float w[32];   // 1 - t^2
+      float pv[32];  // score, P, then with a cap P (t^2 - 1)
+      float w[32];   // t^2 - 1
       tmem_ld32(tS, pv);
       tmem_wait_ld();
       if (CAP) {
@@ -621,9 +621,9 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
 #pragma unroll
       for (int c = 0; c < 32; c += 4) {
         const float4 dl = dl4[c >> 2];
-        f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_sub(f2_pack(w[c], w[c + 1]), f2_pack(dl.x, dl.y))), w[c],
+        f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), dp_less_d<CAP>(f2_pack(w[c], w[c + 1]), f2_pack(dl.x, dl.y))), w[c],
                   w[c + 1]);
-        f2_unpack(f2_mul(f2_pack(pv[c + 2], pv[c + 3]), f2_sub(f2_pack(w[c + 2], w[c + 3]), f2_pack(dl.z, dl.w))),
+        f2_unpack(f2_mul(f2_pack(pv[c + 2], pv[c + 3]), dp_less_d<CAP>(f2_pack(w[c + 2], w[c + 3]), f2_pack(dl.z, dl.w))),
                   w[c + 2], w[c + 3]);
       }
       if (partial) {  // a padded key's V may be NaN
@@ -955,8 +955,8 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
         break;
       }
       tc_fence_after();
-      float pv[32];  // score, P, then P (1 - t^2)
-      float w[32];   // 1 - t^2
+      float pv[32];  // score, P, then with a cap P (t^2 - 1)
+      float w[32];   // t^2 - 1
       tmem_ld32(tmem + lane_addr + quarter * 32, pv);
       tmem_wait_ld();
       tc_fence_before();
@@ -1016,7 +1016,7 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
           float a, b2;
-          f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_sub(f2_pack(w[c], w[c + 1]), delta2)), a, b2);
+          f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), dp_less_d<CAP>(f2_pack(w[c], w[c + 1]), delta2)), a, b2);
           pk[c / 2] = pack_bf16(a, b2);
         }
         tmem_st16u(tP, pk);  // over dP columns that this thread has read

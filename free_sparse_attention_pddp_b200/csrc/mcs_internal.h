@@ -129,13 +129,14 @@ struct ExParams {
   int* status;
 };
 
-// The score cap: y(s) = cap log2(e) tanh(k s), k = scale / cap, for products s = q . k (cap_scores in attn_ex.cuh).
+// The score cap: y(s) = cap log2(e) tanh(k pre s), k pre = scale / cap, for products s = q . k (cap_scores in
+// attn_ex.cuh). pre is 1, or the power of two that brings k near 1 where the coefficients would leave fp32's range.
 struct CapFn {
   int on;
-  float k2, cl;      // 2 k log2 e, cap log2 e
-  float z2, z3;      // s^2 up to which the coefficients b, and a, hold (-1: never)
-  float a[5], b[4];  // y = s Q(s^2)
-  float neg_icl2;    // -1 / cl^2
+  float pre;
+  float k2, cl, icl;  // 2 k log2 e, cap log2 e and its inverse
+  float z2, z3;       // (pre s)^2 up to which the coefficients b, and a, hold
+  float a[5], b[4];   // y = x Q(x^2), x = pre s
 };
 // tanh(x) = x + x z P(z), z = x^2: the coefficients of P, degree 3
 constexpr float kTanhP0 = -0.333323412f, kTanhP1 = 0.133081745f, kTanhP2 = -0.0519478787f, kTanhP3 = 0.0151953385f;

@@ -248,8 +248,10 @@ mcs_status mcs_dense(const mcs_shape* shape, const void* q, const void* k, const
  * through it. A negative document id marks padding: a padded query's row is
  * empty and a padded key is read by nobody, so the contents of padded rows of
  * q, k, v and of the incoming gradient may be anything, NaN included; their
- * gradients are 0. Every other row must be finite. Scores are fp32, P and dS
- * are rounded to bf16 for their tensor-core products, sums are fp32.
+ * gradients are 0. Every other row must be finite. Scores and lse are fp32, so
+ * that P carries a relative error of up to 2^-20 (1 + |s|) from scores of size |s|;
+ * from about 1e7 on the gradients' P may be infinite. P and dS are rounded to bf16
+ * for their tensor-core products, sums are fp32.
  * Outputs must not overlap inputs. Results are bit-identical from run to run.
  */
 #define MCS_ATTN_CAUSAL 1
@@ -257,7 +259,7 @@ mcs_status mcs_dense(const mcs_shape* shape, const void* q, const void* k, const
 typedef struct mcs_attn_shape {
   int B, Hq, Hkv, Nq, Nk, d; /* d in {64, 128}; B*Nq*Hq and B*Nk*Hkv < 2^31 */
   float scale;               /* <= 0 selects 1/sqrt(d); else in [1e-12, 1e12] */
-  float cap;                 /* score cap, at least 1e-6; 0: none */
+  float cap;                 /* score cap, in [1e-6, 1e20]; 0: none */
   int flags;                 /* MCS_ATTN_CAUSAL or 0 */
 } mcs_attn_shape;
 

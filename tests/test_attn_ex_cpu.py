@@ -170,3 +170,11 @@ def test_wrappers_refuse_tensors_that_do_not_fit(mcs):
     qd, kd = torch.zeros(2, 4, 64, dtype=torch.bfloat16), torch.zeros(2, 8, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(mcs.MCSError):
         mcs.mcs_decode(d, qd, kd, kd, torch.zeros(2, dtype=torch.int64), qd, None, ws)
+
+
+def test_caps_beyond_their_range_are_refused(mcs):
+    """Scores near such a cap have no probabilities in fp32."""
+    for cap, ok in ((1e20, True), (2e20, False), (1e36, False), (1e-6, True), (5e-7, False)):
+        s, d = mcs.AttnShape(1, 2, 1, 10, 10, 64, cap=cap), mcs.DecodeShape(1, 2, 1, 10, 64, cap=cap)
+        assert (mcs.mcs_attn_workspace_bytes(s, mcs.MCS_OP_DENSE_EX) > 0) == ok
+        assert (mcs.mcs_decode_workspace_bytes(d) > 0) == ok

@@ -552,3 +552,17 @@ def test_missing_tensors_are_refused(mcs):
             with pytest.raises(mcs.MCSError) as e:
                 call(*args[:i], None, *args[i + 1:], *tail)
             assert e.value.code == 1
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale,cap", [(0.125, 1e5), (1e-4, 1000.0), (1e-8, 100.0), (1e-12, 1e6), (1e12, 1e6), (1e12, 1e-6)])
+def test_caps_far_from_the_scale(mcs, scale, cap, d):
+    """Scores on both sides of the cap where scale / cap is far from 1. Each query has one element, so that a product is
+    exact and the bound is the cap's own."""
+    N, B = 150, 2
+    q, k, v, d_o = inputs(B, 2, 1, N, N, d, seed=41)
+    size = torch.linspace(0, 2.5, N, device="cuda")[None, :, None] * (cap / scale) * torch.tensor([1.0, -1.0], device="cuda")
+    q.zero_()
+    q[..., 5] = size.bfloat16()
+    k[..., 5] = torch.tensor([0.125, 0.5, 1.0, 1.5], device="cuda")[torch.arange(N, device="cuda") % 4][None, :, None]
+    both(mcs, B, 2, 1, N, N, d, scale=scale, cap=cap, tensors=(q, k, v, d_o))
