@@ -112,12 +112,17 @@ constexpr int kSms = 148;
 // tile per slot, takes 2 us). The shorter of the two counts of steps wins: with 8
 // heads of 1024 tokens, d = 128, single takes 15.7 us where pairs take 20.7.
 // Pairs win a tie, since they read K and V half as often: 12 heads of 390
-// queries over 32760 keys take 98.5 us in pairs, 101.6 single. Beyond one wave
-// and five query tiles a head, waves blend into one another and pairs lose
-// nothing.
+// queries over 32760 keys take 98.5 us in pairs, 101.6 single. Where single tiles
+// are more than a wave, they have to take at most three quarters of the steps:
+// waves blend into one another and twice the loads show. (d = 128, heads x
+// queries x keys, single and pairs: half the steps, 40 x 868 x 2048: 51 and 76 us;
+// three quarters, 64 x 740 x 2048: 74 and 81; 0.83, 100 x 740 x 740: 69 and 62;
+// 0.97, 100 x 1124 x 1124: 121 and 106.) A causal mask without a long context
+// before the queries makes the jobs' lengths differ, which blends them more: 24 x
+// 2020 x 2020, three quarters: 50 and 43.5; pairs, then.
 constexpr int kJoinSteps = 3;
 
-FwdPlan fwd_plan(int B, int Hkv, int g, int Nq, int Nk, int d) {
+FwdPlan fwd_plan(int B, int Hkv, int g, int Nq, int Nk, int d, bool causal) {
   FwdPlan f;
   f.tpt = 128 / g;
   f.Tq = (Nq + f.tpt - 1) / f.tpt;
@@ -134,7 +139,9 @@ FwdPlan fwd_plan(int B, int Hkv, int g, int Nq, int Nk, int d) {
   };
   int one = 1;
   const long long pairs = cost(false, &f.nsplit);
-  f.single = (heads * f.Tq <= kSms || f.Tq <= 5) && cost(true, &one) < pairs;
+  const long long ones = cost(true, &one);
+  const bool even = !causal || Nk / 2 >= Nq;
+  f.single = heads * f.Tq <= kSms ? ones < pairs : even && 4 * ones <= 3 * pairs;
   if (f.single) f.nsplit = one;
   // K and V of a chunk's heads take half of the 126 MB L2 at most
   const size_t head = static_cast<size_t>(Nk) * d * 4;
@@ -278,7 +285,7 @@ DecodePlan decode_plan(const mcs_decode_shape* s) {
   }
   f.nsplit = (s->C + f.chunk - 1) / f.chunk;
   f.cluster = s->P == 0 && f.nsplit > 1 && f.nsplit <= 8 && f.chunk <= 512 && jobs * f.nsplit <= slots;
-  if (s->P > 0) f.pre = fwd_plan(1, s->Hkv, g, s->B, s->P, s->d);
+  if (s->P > 0) f.pre = fwd_plan(1, s->Hkv, g, s->B, s->P, s->d, false);
   return f;
 }
 
@@ -375,11 +382,10 @@ extern "C" {
 
 size_t mcs_attn_workspace_bytes(const mcs_attn_shape* s, mcs_op op) {
   if (check_attn(s) != MCS_OK) return 0;
-  if (op == MCS_OP_DENSE_EX)
-    return fwd_layout(fwd_plan(s->B, s->Hkv, s->Hq / s->Hkv, s->Nq, s->Nk, s->d), s->B, s->Hkv, s->d).total;
-  if (op == MCS_OP_DENSE_BWD)
-    return bwd_layout(fwd_plan(s->B, s->Hkv, s->Hq / s->Hkv, s->Nq, s->Nk, s->d), s->B, s->Hkv, s->Nk, s->d).total;
-  return 0;
+  if (op != MCS_OP_DENSE_EX && op != MCS_OP_DENSE_BWD) return 0;
+  const FwdPlan f = fwd_plan(s->B, s->Hkv, s->Hq / s->Hkv, s->Nq, s->Nk, s->d, s->flags & MCS_ATTN_CAUSAL);
+  return op == MCS_OP_DENSE_EX ? fwd_layout(f, s->B, s->Hkv, s->d).total
+                               : bwd_layout(f, s->B, s->Hkv, s->Nk, s->d).total;
 }
 
 mcs_status mcs_dense_ex(const mcs_attn_shape* s, const mcs_attn_opts* opts, const void* q, const void* k,
@@ -395,7 +401,7 @@ mcs_status mcs_dense_ex(const mcs_attn_shape* s, const mcs_attn_opts* opts, cons
   if ((st = check_device()) != MCS_OK) return st;
   ExParams p = ex_params(s, opts);
   p.status = static_cast<int*>(ws);
-  const FwdPlan f = fwd_plan(p.B, p.Hkv, p.g, p.Nq, p.Nk, s->d);
+  const FwdPlan f = fwd_plan(p.B, p.Hkv, p.g, p.Nq, p.Nk, s->d, p.causal);
   const FwdWs w = fwd_layout(f, p.B, p.Hkv, s->d);
   uint8_t* base = static_cast<uint8_t*>(ws);
   CUtensorMap tq, tk, tv;
@@ -443,7 +449,7 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
   if ((st = check_device()) != MCS_OK) return st;
   ExParams p = ex_params(s, opts);
   p.status = static_cast<int*>(ws);
-  const FwdPlan f = fwd_plan(p.B, p.Hkv, p.g, p.Nq, p.Nk, s->d);
+  const FwdPlan f = fwd_plan(p.B, p.Hkv, p.g, p.Nq, p.Nk, s->d, p.causal);
   const BwdWs w = bwd_layout(f, p.B, p.Hkv, p.Nk, s->d);
   uint8_t* base = static_cast<uint8_t*>(ws);
   CUtensorMap tq, tg, tk, tv;
