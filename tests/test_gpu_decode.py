@@ -300,3 +300,53 @@ def test_a_load_of_the_prefix_that_never_arrives_is_reported(mcs, d):
     finally:
         debug_set_flags(0)
     assert all(torch.equal(x, y) for x, y in zip(call(0), want))
+
+
+def test_calls_side_by_side(mcs):
+    """Two streams, each with workspaces and outputs of its own, run all four calls at the same time; one of them also
+    from a captured graph."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    Hq, Hkv, N, d, R, P, C = 12, 4, 700, 128, 5, 500, 300
+    q, k, v, d_o = rand(g, 2, N, Hq, d), rand(g, 2, N, Hkv, d), rand(g, 2, N, Hkv, d), rand(g, 2, N, Hq, d)
+    ids = torch.repeat_interleave(torch.arange(3), torch.tensor([30, 600, 70]))[None].repeat(2, 1).int().cuda()
+    q1, kp, vp = rand(g, R, Hq, d), rand(g, P, Hkv, d), rand(g, P, Hkv, d)
+    kc, vc = rand(g, R, C, Hkv, d), rand(g, R, C, Hkv, d)
+    lens = torch.tensor([300, 1, 0, 133, 64], dtype=torch.int32, device="cuda")
+    shape = mcs.AttnShape(2, Hq, Hkv, N, N, d, cap=20.0, causal=True)
+    step, one = mcs.DecodeShape(R, Hq, Hkv, C, d, P=P), mcs.DecodeShape(R, Hq, Hkv, C, d)
+
+    class Caller:
+        def __init__(self):
+            self.ws = [mcs.attn_workspace(shape, op) for op in (mcs.MCS_OP_DENSE_EX, mcs.MCS_OP_DENSE_BWD)]
+            self.ws += [mcs.decode_workspace(s) for s in (step, one)]
+            self.out = [torch.empty_like(t) for t in (q, q, k, v, q1, q1)]
+            self.lse = torch.empty(2, Hq, N, device="cuda")
+
+        def __call__(self):
+            o, dq, dk, dv, o1, o2 = self.out
+            mcs.mcs_dense_ex(shape, q, k, v, o, self.lse, self.ws[0], doc_q=ids, doc_k=ids)
+            mcs.mcs_decode_shared(step, q1, kp, vp, kc, vc, lens, o1, None, self.ws[2])
+            mcs.mcs_dense_bwd(shape, q, k, v, o, self.lse, d_o, dq, dk, dv, self.ws[1], doc_q=ids, doc_k=ids)
+            mcs.mcs_decode(one, q1, kc, vc, lens, o2, None, self.ws[3])
+
+    want = Caller()
+    want()
+    torch.cuda.synchronize()
+    callers, streams = [Caller(), Caller()], [torch.cuda.Stream(), torch.cuda.Stream()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        callers[1]()
+    for c in callers:
+        for t in c.out:
+            t.zero_()
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        with torch.cuda.stream(streams[0]):
+            callers[0]()
+        with torch.cuda.stream(streams[1]):
+            graph.replay()
+    torch.cuda.synchronize()
+    for c in callers:
+        assert all(mcs.mcs_poll_status(w)[0] == 0 for w in c.ws)
+        assert all(torch.equal(x, y) for x, y in zip(c.out, want.out))
