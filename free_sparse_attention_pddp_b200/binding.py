@@ -16,7 +16,7 @@ _lib = None
 MCS_GROUP_SIZE = 128
 MCS_INFO_WORDS = 8
 MCS_OP_GROUP, MCS_OP_ANCHOR, MCS_OP_SPARSE, MCS_OP_DENSE, MCS_OP_DENSE_EX, MCS_OP_DENSE_BWD = 0, 1, 2, 3, 4, 5
-MCS_ATTN_CAUSAL = 1
+MCS_ATTN_CAUSAL, MCS_ATTN_D_FROM_O = 1, 2
 
 
 class MCSError(RuntimeError):
@@ -36,14 +36,16 @@ class Shape(ctypes.Structure):
 
 
 class AttnShape(ctypes.Structure):
-    """mcs_attn_shape: query and KV heads, lengths, scale (<= 0 selects 1/sqrt(d)), score cap (0: none), causal."""
+    """mcs_attn_shape: query and KV heads, lengths, scale (<= 0 selects 1/sqrt(d)), score cap (0: none), causal;
+    d_from_o: the gradients' row sums come from the given o (MCS_ATTN_D_FROM_O, see include/mcs.h)."""
 
     _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("Nq", ctypes.c_int),
                 ("Nk", ctypes.c_int), ("d", ctypes.c_int), ("scale", ctypes.c_float), ("cap", ctypes.c_float),
                 ("flags", ctypes.c_int)]
 
-    def __init__(self, B, Hq, Hkv, Nq, Nk, d, scale=0.0, cap=0.0, causal=False):
-        super().__init__(B, Hq, Hkv, Nq, Nk, d, scale, cap, MCS_ATTN_CAUSAL if causal else 0)
+    def __init__(self, B, Hq, Hkv, Nq, Nk, d, scale=0.0, cap=0.0, causal=False, d_from_o=False):
+        flags = (MCS_ATTN_CAUSAL if causal else 0) | (MCS_ATTN_D_FROM_O if d_from_o else 0)
+        super().__init__(B, Hq, Hkv, Nq, Nk, d, scale, cap, flags)
 
 
 class AttnOpts(ctypes.Structure):
@@ -309,7 +311,7 @@ def mcs_dense_ex(shape, q, k, v, o, lse, ws, slopes=None, prefix=None, doc_q=Non
 
 def mcs_dense_bwd(shape, q, k, v, o, lse, d_o, dq, dk, dv, ws, slopes=None, prefix=None, doc_q=None, doc_k=None,
                   stream=None):
-    """Gradients of mcs_dense_ex with respect to q, k and v, from its o and lse and the gradient d_o of o."""
+    """Gradients of mcs_dense_ex with respect to q, k and v, from its lse (and o: shape.d_from_o) and the gradient d_o of o."""
     import torch
 
     bf16, s = torch.bfloat16, shape

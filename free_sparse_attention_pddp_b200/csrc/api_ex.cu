@@ -31,7 +31,7 @@ mcs_status check_heads(int Hq, int Hkv, int d, float scale, float cap) {
 
 mcs_status check_attn(const mcs_attn_shape* s) {
   if (!s || s->B < 1 || s->Nq < 1 || s->Nk < 1) return MCS_ERR_INVALID_ARG;
-  if ((s->flags & ~MCS_ATTN_CAUSAL) != 0) return MCS_ERR_INVALID_ARG;
+  if ((s->flags & ~(MCS_ATTN_CAUSAL | MCS_ATTN_D_FROM_O)) != 0) return MCS_ERR_INVALID_ARG;
   const mcs_status st = check_heads(s->Hq, s->Hkv, s->d, s->scale, s->cap);
   if (st != MCS_OK) return st;
   if (static_cast<long long>(s->B) * s->Nq >= (1ll << 31) / s->Hq ||
@@ -491,14 +491,9 @@ mcs_status mcs_dense_bwd(const mcs_attn_shape* s, const mcs_attn_opts* opts, con
       t.k_order = k_order;
     }
   }
-  // every row's D from o, then anew in the first tiles of a causal mask, whose rows see few keys; or, where all rows do
-  // or documents may be short, both from one kernel, tile by tile
   t.stats_out = stats;
-  const bool any_tile = p.doc_q || p.Nk <= kFewKeys;
-  t.few_tiles = any_tile   ? f.Tq
-                : p.causal ? std::min(f.Tq, std::max(0, kFewKeys - (p.Nk - p.Nq) + f.tpt - 1) / f.tpt)
-                           : 0;
-  if (!any_tile && launch_ex_row_stats(s->d, t, stream) != cudaSuccess) return MCS_ERR_CUDA;
+  t.d_from_o = (s->flags & MCS_ATTN_D_FROM_O) != 0;
+  if (t.d_from_o && launch_ex_row_stats(s->d, t, stream) != cudaSuccess) return MCS_ERR_CUDA;
   return ok_or_cuda(launch_ex_bwd(s->d, &tq, &tg, &tk, &tv, t, stream));
 }
 

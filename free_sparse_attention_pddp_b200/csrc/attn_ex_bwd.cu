@@ -157,23 +157,30 @@ __device__ __forceinline__ void teardown(volatile int* abort_flag, uint64_t* don
 }
 
 // Per packed row: -lse in log2 units (less slope times the row's token in the tile, which the dK/dV tiles' bias counts
-// on) and D = d_o . o, as [B Hkv, Tq][2][128]; an empty row, like a row whose lse is -inf, gets (-inf, 0), which makes
-// its P zero. o is rounded to bf16, which puts D off by up to 2^-9 |d_o| |o|: little beside dP where a row's P is spread
-// over many keys, but dP - D cancels where it is not. In dQ, by itself, in 64 bits with d = 128 (relative, over all rows):
-//   keys of a row             2       4      16      64     256    1024
-//   scores of spread 1    .0028   .0017   .0008   .0004   .0003   .0002
-//   spread 2              .0043   .0029   .0018   .0014   .0008   .0007
-//   spread 6              .0085   .0061   .0044   .0038   .0033   .0033
-// beside the .0024 that dS in bf16 brings. Rows of up to 256 keys take D from ex_delta_kernel instead, a sweep of two
-// products; for every row it would take 20 to 25 % of a training step (8192 tokens, 12 heads: 2.48 ms instead of 1.97).
-// One CTA per tile, 16 bytes of a row per lane: reading o and d_o once from HBM is the bound.
-template <int D, int THREADS>
-__device__ __forceinline__ void row_stats(const ExTile& p, int bh, int qt) {
+// on) and D, as [B Hkv, Tq][2][128]; an empty row, like a row whose lse is -inf, gets (-inf, 0), which makes its P zero.
+// Two ways to D:
+//   ex_delta_kernel  D = sum_j P dP in fp32, a sweep of two products more (the default);
+//   ex_row_stats     D = d_o . o from the given o, where the caller asks for that.
+// o is rounded to bf16, which puts the second off by up to 2^-9 |d_o| |o|, and dP - D cancels where few keys carry a row's
+// P: because it sees few, because scores are sharp, or because a distance bias leaves the near ones. In dQ, by itself,
+// in 64 bits with d = 128 (relative, over all rows; dS in bf16 brings 0.0017 and so does the result's own rounding):
+//   keys of a row             2       4      16      64     256    1024    4096
+//   scores of spread 1    .0028   .0017   .0008   .0004   .0003   .0002   .0002
+//   spread 2              .0043   .0029   .0018   .0014   .0008   .0007   .0005
+//   spread 6              .0085   .0061   .0044   .0038   .0033   .0033   .0031
+// and 0.0015 with 10 heads' slopes from 0.6 to 0.004 and scores of spread 2, however long the rows are. It saves the sweep:
+// forward and gradients of 8192 tokens, 12 heads, capped, 1.97 instead of 2.48 ms.
+// ex_row_stats: one CTA per tile, 16 bytes of a row per lane; reading o and d_o once from HBM is the bound.
+template <int D>
+__global__ void __launch_bounds__(256) ex_row_stats(const ExTile p) {
+  next_may_start();
+  await_previous();
   constexpr int LANES = D / 8;             // of a row
-  constexpr int PASS = THREADS / LANES;    // rows at a time
+  constexpr int PASS = 256 / LANES;        // rows at a time
+  const int qt = blockIdx.x % p.Tq, bh = blockIdx.x / p.Tq;
   const int b = bh / p.Hkv, hk = bh % p.Hkv;
   const int c = threadIdx.x % LANES;
-  float* out = p.stats_out + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
+  float* out = p.stats_out + static_cast<size_t>(blockIdx.x) * 256;
 #pragma unroll 4
   for (int r0 = 0; r0 < 128; r0 += PASS) {
     const int row = r0 + threadIdx.x / LANES;
@@ -196,17 +203,11 @@ __device__ __forceinline__ void row_stats(const ExTile& p, int bh, int qt) {
     }
 #pragma unroll
     for (int w = LANES / 2; w; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-    if (c == 0 && row < 128) {
+    if (c == 0) {
       out[row] = nl;
       out[128 + row] = s;
     }
   }
-}
-template <int D>
-__global__ void __launch_bounds__(256) ex_row_stats(const ExTile p) {
-  next_may_start();
-  await_previous();
-  row_stats<D, 256>(p, blockIdx.x / p.Tq, blockIdx.x % p.Tq);
 }
 
 }  // namespace
@@ -657,48 +658,6 @@ __device__ __forceinline__ void dkv_tile(const CUtensorMap& tm_q, const CUtensor
   teardown(abort_flag, done, kv_full, n > 0 ? 1 + 4 * C::NS : 0, tmem);
 }
 
-// Whether one of the rows of a query tile sees between one and kFewKeys keys, under a document mask whose bitmap `meet`
-// says which of the key tiles below `hi` to look at. All threads of the CTA call it, five to a row, a fifth of the tiles
-// each; ids are compared one by one only in tiles of several documents. `seen`: 128 shared words, which loads may overwrite
-// afterwards.
-template <typename Limit>
-__device__ __forceinline__ bool any_row_sees_few(const ExTile& p, uint32_t meet, int hi, int b, int qt,
-                                                 const Limit& limit, int* seen) {
-  const int row = threadIdx.x & 127, part = threadIdx.x >> 7, lane = threadIdx.x & 31;
-  const int my_doc = p.q_ids[(static_cast<size_t>(b) * p.Tq + qt) * 128 + row];  // padding: -2, which no key has
-  const int lim = limit(p.Nk - p.Nq + qt * p.tpt + row / p.g);
-  if (part == 0) seen[row] = 0;
-  __syncthreads();
-  int c = 0;
-  for (int t0 = 0; t0 < hi; t0 += 32) {
-    const size_t at = static_cast<size_t>(b) * p.Tk + t0;
-    int4 r = make_int4(0, 1, 0, 0);
-    if (t0 + lane < hi) r = __ldg(p.k_ranges + at + lane);
-    const uint32_t one_doc = __ballot_sync(0xffffffffu, r.x == r.y && !r.z);
-    for (uint32_t todo = lds32(meet + t0 / 8); todo; todo &= todo - 1) {
-      const int t = __ffs(todo) - 1;
-      const int id = __shfl_sync(0xffffffffu, r.x, t), valid = lim - (t0 + t) * 128;
-      if (t % (kThreads / 128) != part) continue;
-      if (one_doc >> t & 1) {
-        c += id == my_doc ? min(max(valid, 0), 128) : 0;
-        continue;
-      }
-      const int4* ids = reinterpret_cast<const int4*>(p.k_ids + (at + t) * 128);
-#pragma unroll 8
-      for (int e = 0; e < 32; ++e) {
-        const int4 x = __ldg(ids + e);
-        c += (x.x == my_doc && 4 * e < valid) + (x.y == my_doc && 4 * e + 1 < valid) +
-             (x.z == my_doc && 4 * e + 2 < valid) + (x.w == my_doc && 4 * e + 3 < valid);
-      }
-    }
-  }
-  atomicAdd(&seen[row], c);  // whole-number sums: their order is free
-  __syncthreads();
-  const bool few = my_doc >= 0 && seen[row] > 0 && seen[row] <= kFewKeys;
-  fence_proxy_async_smem();
-  return __syncthreads_or(few);
-}
-
 template <int D, bool CAP, bool BIAS, bool DOC, bool DELTA>
 __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorMap& tm_g, const CUtensorMap& tm_k,
                                         const CUtensorMap& tm_v, const ExTile& p, int cta) {
@@ -731,9 +690,6 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
   if (DOC && p.order) {
     int part;
     bh = ordered_job(p, p.order, p.Tq, cta, &qt, &part);
-  } else if (DELTA) {
-    qt = cta % p.few_tiles;
-    bh = cta / p.few_tiles;
   } else if (p.causal) {  // the last query tiles see the most keys and go first
     const int per_chunk = p.chunk * p.Tq;
     const int ch = cta / per_chunk, in = cta % per_chunk;
@@ -749,7 +705,6 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
   const int prefix = p.prefix ? p.prefix[b] : 0;
   auto limit = [&](int pos) { return p.causal ? min(p.Nk, max(max(pos + 1, prefix), 0)) : p.Nk; };
   const int hi = (limit(off + min(p.Nq, (qt + 1) * p.tpt) - 1) + 127) >> 7;
-  if (DELTA && !DOC && limit(off + qt * p.tpt) > kFewKeys) return;  // the tile's first row sees the fewest
   const int4 none = make_int4(0x7fffffff, static_cast<int>(0x80000000), 0, 0);
   const int4 mine = DOC ? p.q_ranges[static_cast<size_t>(b) * p.Tq + qt] : none;
   const int rt = p.tpt * p.g;
@@ -835,12 +790,6 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
     n = count[0];
   }
   const TileIter first{DOC ? tiles.meet : 0u, 0u, 0, 0};
-  // A short list is swept at once, which takes no longer than to count its keys.
-  if (DELTA && DOC && n > 4 && !any_row_sees_few(p, tiles.meet, hi, b, qt, limit, reinterpret_cast<int*>(sV))) {
-    row_stats<D, kThreads>(p, bh, qt);
-    teardown(abort_flag, done, qg_full, 0, tmem);
-    return;
-  }
   // TMEM: S | dP 0 | dQ | dP 1
   auto dp_buf = [&](int i) { return tmem + ((i & 1) ? 384u : 128u); };
 
@@ -1062,8 +1011,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   else dq_tile<D, CAP, BIAS, DOC, false>(tm_q, tm_g, tm_k, tm_v, p, blockIdx.x - keys);
 }
 
-// The rows' statistics with D summed from P dP in fp32, for the tiles with a row that sees few keys (see row_stats). Of
-// the other tiles, under a document mask, those of row_stats; without one, ex_row_stats has them.
+// The rows' statistics with D summed from P dP in fp32 (see ex_row_stats).
 template <int D, bool CAP, bool BIAS, bool DOC>
 __global__ void __launch_bounds__(kThreads, 1)
     ex_delta_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_g,
@@ -1108,14 +1056,14 @@ cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUten
   if (e != cudaSuccess) return e;
   const unsigned smem = std::max(DkvCfg<D>::SMEM + (DOC ? (p.Tq + 31) / 32 * 12u : 0u),
                                  DqCfg<D>::SMEM + (DOC ? (p.Tk + 31) / 32 * 12u : 0u));
-  if (p.few_tiles > 0) {
+  if (!p.d_from_o) {
     static KernelReady ready_delta;
     auto delta = ex_delta_kernel<D, CAP, BIAS, DOC>;
     const cudaError_t e2 = make_ready(ready_delta, delta, most_q, 0);
     if (e2 != cudaSuccess) return e2;
     const unsigned smem_delta = DqCfg<D>::SMEM + (DOC ? (p.Tk + 31) / 32 * 12u : 0u);
-    const cudaError_t e3 = launch_in_sequence(delta, p.B * p.Hkv * p.few_tiles, kThreads, smem_delta, s,
-                                              DOC || p.Nk > kFewKeys, *tq, *tg, *tk, *tv, p);
+    const cudaError_t e3 = launch_in_sequence(delta, p.B * p.Hkv * p.Tq, kThreads, smem_delta, s, DOC, *tq, *tg, *tk,
+                                              *tv, p);
     if (e3 != cudaSuccess) return e3;
   }
   const cudaError_t e4 = launch_in_sequence(kern, p.B * p.Hkv * (p.Tk * p.kv_splits + p.Tq), kThreads, smem, s, true, *tq,
@@ -1128,7 +1076,7 @@ cudaError_t launch_bwd(const CUtensorMap* tq, const CUtensorMap* tg, const CUten
 
 cudaError_t launch_ex_row_stats(int d, const ExTile& p, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(p.B) * p.Hkv * p.Tq;
-  return launch_in_sequence(d == 64 ? ex_row_stats<64> : ex_row_stats<128>, grid, 256, 0, s, false, p);
+  return launch_in_sequence(d == 64 ? ex_row_stats<64> : ex_row_stats<128>, grid, 256, 0, s, p.doc_q != nullptr, p);
 }
 
 cudaError_t launch_ex_bwd(int d, const CUtensorMap* tq, const CUtensorMap* tg, const CUtensorMap* tk,

@@ -142,9 +142,6 @@ struct CapFn {
 constexpr float kTanhP0 = -0.333323412f, kTanhP1 = 0.133081745f, kTanhP2 = -0.0519478787f, kTanhP3 = 0.0151953385f;
 constexpr float kTanhR0 = -0.333318822f, kTanhR1 = 0.132776282f, kTanhR2 = -0.0477941821f;  // degree 2, |x| <= 0.4
 
-// A row that sees at most so many keys takes D from P dP (ex_delta_kernel in attn_ex_bwd.cu).
-constexpr int kFewKeys = 256;
-
 // The tile kernels' view of a call (attn_ex_fwd.cu, attn_ex_bwd.cu).
 struct ExTile {
   int B, Hq, Hkv, g, tpt, Nq, Nk;  // tpt: tokens of a packed query tile
@@ -173,7 +170,7 @@ struct ExTile {
   size_t kv_size;                  // elements of dk
   float* part_kv;                  // [2 (dv, dk)][kv_splits][B,Nk,Hkv,d], null unless kv_splits > 1
   float* stats_out;                // where the statistics go
-  int few_tiles;                   // backward: leading query tiles whose rows may see few keys
+  int d_from_o;                    // backward: D is d_o . o, else a sweep sums it from P dP
   uint16_t *dq, *dk, *dv;
   float *part_o, *part_lse;        // [parts][B,Hkv,Tq,128](,d), lse in log2 units
   int* status;

@@ -255,12 +255,13 @@ mcs_status mcs_dense(const mcs_shape* shape, const void* q, const void* k, const
  * Outputs must not overlap inputs. Results are bit-identical from run to run.
  */
 #define MCS_ATTN_CAUSAL 1
+#define MCS_ATTN_D_FROM_O 2 /* mcs_dense_bwd (mcs_dense_ex ignores it): see there */
 
 typedef struct mcs_attn_shape {
   int B, Hq, Hkv, Nq, Nk, d; /* d in {64, 128}; B*Nq*Hq and B*Nk*Hkv < 2^31 */
   float scale;               /* <= 0 selects 1/sqrt(d); else in [1e-12, 1e12] */
   float cap;                 /* score cap, in [1e-6, 1e20]; 0: none */
-  int flags;                 /* MCS_ATTN_CAUSAL or 0 */
+  int flags;                 /* MCS_ATTN_CAUSAL, MCS_ATTN_D_FROM_O, or both, or 0 */
 } mcs_attn_shape;
 
 /* Device arrays, each nullable; 4-byte aligned. Constants of the call: they get no gradient. */
@@ -288,11 +289,14 @@ mcs_status mcs_dense_ex(const mcs_attn_shape* shape, const mcs_attn_opts* opts, 
  * Gradients of mcs_dense_ex: with the forward's inputs, its o and lse, and the
  * gradient d_o of a scalar with respect to o, writes dq, dk and dv (summed over
  * the query heads that share a KV head). No atomics: the sums' order is fixed.
- * o and lse are what mcs_dense_ex gave for the same shape, options and inputs, not
- * a pair joined from several calls: a row that sees at most 256 keys takes
- * D_i = d_o_i . o_i as sum_j P_ij dP_ij, in fp32; the others take it from the given
- * o, whose rounding to bf16 moves dq and dk by 0.0003 (relative) where scores have a
- * spread of 1, and by 0.003 where it is 6.
+ * lse is what mcs_dense_ex gave for the same shape, options and inputs, and
+ * D_i = sum_j P_ij dP_ij is summed in fp32; o is not read. With MCS_ATTN_D_FROM_O,
+ * D_i = d_o_i . o_i comes from the given o instead: for an (o, lse) that was joined
+ * from several calls over parts of the keys, each of which then gets its part of
+ * the gradients, and for speed (a fifth of a long training step). The rounding of o
+ * to bf16 then shows where few keys carry a row's P: dq and dk move by 0.0005
+ * (relative) with 4096 keys and scores of spread 2, by 0.0015 with distance slopes up
+ * to 0.6, by 0.003 with scores of spread 6, by 0.004 with 2 keys.
  */
 mcs_status mcs_dense_bwd(const mcs_attn_shape* shape, const mcs_attn_opts* opts, const void* q, const void* k,
                          const void* v, const void* o, const float* lse, const void* d_o, void* dq, void* dk,

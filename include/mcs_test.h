@@ -22,7 +22,7 @@ extern "C" {
  * mcs_dense_ex's and mcs_dense_bwd's tiles waits 20 us before each tile (the
  * results must not change).
  * Bits 4, 5, 6: as bit 0, but only for mcs_dense_bwd's CTAs of key tiles, its
- * CTAs of query tiles, and its sweep for the rows that see few keys.
+ * CTAs of query tiles, and the sweep that sums D.
  */
 void mcs_debug_set_flags(int flags);
 

@@ -178,3 +178,11 @@ def test_caps_beyond_their_range_are_refused(mcs):
         s, d = mcs.AttnShape(1, 2, 1, 10, 10, 64, cap=cap), mcs.DecodeShape(1, 2, 1, 10, 64, cap=cap)
         assert (mcs.mcs_attn_workspace_bytes(s, mcs.MCS_OP_DENSE_EX) > 0) == ok
         assert (mcs.mcs_decode_workspace_bytes(d) > 0) == ok
+
+
+def test_flags(mcs):
+    for flags, ok in ((0, True), (1, True), (2, True), (3, True), (4, False), (-1, False)):
+        s = mcs.AttnShape(1, 2, 1, 10, 10, 64)
+        s.flags = flags
+        assert (mcs.mcs_attn_workspace_bytes(s, mcs.MCS_OP_DENSE_BWD) > 0) == ok
+    assert mcs.AttnShape(1, 2, 1, 10, 10, 64, causal=True, d_from_o=True).flags == 3

@@ -566,3 +566,71 @@ def test_caps_far_from_the_scale(mcs, scale, cap, d):
     q[..., 5] = size.bfloat16()
     k[..., 5] = torch.tensor([0.125, 0.5, 1.0, 1.5], device="cuda")[torch.arange(N, device="cuda") % 4][None, :, None]
     both(mcs, B, 2, 1, N, N, d, scale=scale, cap=cap, tensors=(q, k, v, d_o))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gain", [2.0, 6.0])
+@pytest.mark.parametrize("opts", [dict(), dict(cap=20.0, causal=True), dict(slopes=True), dict(slopes=True, docs=700, causal=True)],
+                         ids=["plain", "capped", "biased", "documents"])
+def test_row_sums_in_long_calls(mcs, opts, gain, d):
+    """The gradients of every row are held to the bound without o's rounding, whatever carries its P: all keys, a few
+    (sharp scores), the near ones (a distance bias)."""
+    N, Hq, Hkv = 1315, 6, 2
+    q, k, v, d_o = inputs(1, Hq, Hkv, N, N, d, 51, gain)
+    slopes = torch.tensor([2.0 ** (-8 * (h + 1) / Hq) for h in range(Hq)], device="cuda") if "slopes" in opts else None
+    ids = packed_ids(1, N, opts["docs"], 3, 50).cuda() if "docs" in opts else None
+    cap, causal = opts.get("cap", 0.0), opts.get("causal", False)
+    got = run(mcs, mcs.AttnShape(1, Hq, Hkv, N, N, d, cap=cap, causal=causal), q, k, v, d_o, slopes=slopes, doc_q=ids,
+              doc_k=ids)
+    valid = attn_ref.valid_mask(1, N, N, causal, None, ids, ids, "cuda")
+    want = attn_ref.attn(q, k, v, d_o, cap=cap, slopes=slopes, valid=valid, exact_d=True)
+    for name in ("lse", "o", "dv", "dk", "dq"):
+        attn_ref.check(got[name], want[name], name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,Nk,causal,mean", [(1, 4, 2, 200, 200, False, 0), (2, 6, 2, 601, 601, True, 0), (1, 5, 1, 300, 900, True, 0),
+                                                        (2, 4, 4, 700, 700, False, 90), (1, 2, 1, 600, 130, True, 0)])
+def test_row_sums_from_the_given_o(mcs, B, Hq, Hkv, Nq, Nk, causal, mean, d):
+    """MCS_ATTN_D_FROM_O: the gradients within the bound that counts o's rounding, at every length; the forward is the
+    same with the flag."""
+    q, k, v, d_o = inputs(B, Hq, Hkv, Nq, Nk, d, seed=52)
+    slopes = torch.tensor([.1 * (h + 1) for h in range(Hq)], device="cuda")
+    ids = packed_ids(B, Nq, mean, 4, 40).cuda() if mean else None
+    kw = dict(cap=30.0, causal=causal)
+    a, b = (run(mcs, mcs.AttnShape(B, Hq, Hkv, Nq, Nk, d, **kw, d_from_o=f), q, k, v, d_o, slopes=slopes, doc_q=ids, doc_k=ids)
+            for f in (False, True))
+    assert torch.equal(a["o"], b["o"]) and torch.equal(a["lse"], b["lse"]) and not torch.equal(a["dq"], b["dq"])
+    valid = attn_ref.valid_mask(B, Nq, Nk, causal, None, ids, ids, "cuda")
+    want = attn_ref.attn(q, k, v, d_o, cap=30.0, slopes=slopes, valid=valid)
+    for name in ("dv", "dk", "dq"):
+        attn_ref.check(b[name], want[name], name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("parts", [(500, 400), (700, 60, 140)])
+def test_gradients_of_a_joined_pair(mcs, parts, d):
+    """Keys in parts: (o, lse) of each, joined, gives each part its gradients (MCS_ATTN_D_FROM_O); dq is their sum.
+
+    o's parts are rounded, each by at most U of its share of sum P |v|, and the joined o once more, so D is off by at most twice
+    what the bound counts; every part of dq is rounded by itself."""
+    N, Hq, Hkv = 300, 4, 2
+    q, k, v, d_o = inputs(1, Hq, Hkv, N, sum(parts), d, seed=53)
+    pieces = list(zip([x.contiguous() for x in k.split(parts, 1)], [x.contiguous() for x in v.split(parts, 1)]))
+    shapes = [mcs.AttnShape(1, Hq, Hkv, N, n, d, d_from_o=True) for n in parts]
+    each = [run(mcs, s, q, kk, vv) for s, (kk, vv) in zip(shapes, pieces)]
+    lse = torch.logsumexp(torch.stack([e["lse"] for e in each]), 0)
+    o = sum(e["o"].float() * (e["lse"] - lse).exp().transpose(1, 2)[..., None] for e in each).bfloat16()
+    dq, dk, dv = [], [], []
+    for s, (kk, vv) in zip(shapes, pieces):
+        out = [torch.empty_like(t) for t in (q, kk, vv)]
+        ws = mcs.attn_workspace(s, mcs.MCS_OP_DENSE_BWD)
+        mcs.mcs_dense_bwd(s, q, kk, vv, o, lse, d_o, *out, ws)
+        assert mcs.mcs_poll_status(ws)[0] == 0
+        for t, x in zip((dq, dk, dv), out):
+            t.append(x)
+    want = attn_ref.attn(q, k, v, d_o)
+    twice = lambda n, more=0.0: (want[n][0], 2 * want[n][1] + more)  # noqa: E731
+    attn_ref.check(torch.cat(dv, 1), twice("dv"), "dv")
+    attn_ref.check(torch.cat(dk, 1), twice("dk"), "dk")
+    attn_ref.check(sum(x.double() for x in dq), twice("dq", attn_ref.U * sum(x.double().abs() for x in dq)), "dq")
