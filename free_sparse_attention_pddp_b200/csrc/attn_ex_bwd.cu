@@ -881,6 +881,11 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
     const float lse = row_valid ? p.lse_in[(static_cast<size_t>(b) * p.Hq + head) * p.Nq + tok] : -CUDART_INF_F;
     const float negl = lse == -CUDART_INF_F ? lse : -lse * kLog2e, delta = DELTA ? 0.f : st[128 + row];
     uint64_t d2 = 0;  // DELTA: the sum of P dP, over even and odd columns
+    // DELTA: a row with a single key has D = dP to the bit, and so dS = 0 (the products give the same dP whichever operand
+    // it is that stands on the lanes, which the tests check). Such a key's tile is partial for the row: the sum of dP
+    // over the valid keys of partial tiles, and the number of keys (two for a whole tile).
+    float one = 0.f;
+    int keys = 0;
     const uint64_t negl2 = f2_pack(negl, negl), delta2 = f2_pack(delta, delta);
     const int pos = off + tok;
     const int lim = limit(pos) - quarter * 32;
@@ -932,13 +937,16 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
         for (int c = 0; c < 32; c += 2)
           f2_unpack(f2_mul(f2_pack(pv[c], pv[c + 1]), f2_pack(w[c], w[c + 1])), pv[c], pv[c + 1]);
       }
+      int found = 0;  // DELTA: this row's keys of a mixed tile
       if (partial) {
         const int valid = lim - kt * 128;
         if (mixed) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const int i_c = __shfl_sync(0xffffffffu, id, c);  // every lane takes part
-            pv[c] = (c < valid && i_c == my_doc) ? pv[c] : 0.f;
+            const bool in = c < valid && i_c == my_doc;
+            pv[c] = in ? pv[c] : 0.f;
+            if (DELTA) found += in;
           }
         } else {
 #pragma unroll
@@ -958,6 +966,11 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
         for (int c = 0; c < 32; ++c) w[c] = pv[c] == 0.f ? 0.f : w[c];
       }
       if (DELTA) {
+        if (partial) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) one += w[c];
+        }
+        keys += !partial ? 2 : mixed ? found : min(max(lim - kt * 128, 0), 32);
 #pragma unroll
         for (int c = 0; c < 32; c += 2) d2 = f2_fma(f2_pack(pv[c], pv[c + 1]), f2_pack(w[c], w[c + 1]), d2);
       } else {
@@ -981,12 +994,16 @@ __device__ __forceinline__ void dq_tile(const CUtensorMap& tm_q, const CUtensorM
       float even, odd;
       f2_unpack(d2, even, odd);
       sums[quarter * 128 + row] = even + odd;
+      sums[512 + quarter * 128 + row] = one;
+      reinterpret_cast<int*>(sums)[1024 + quarter * 128 + row] = keys;
       named_barrier_sync<2, 512>();
       if (fin && quarter == 0) {
         const bool live = negl != -CUDART_INF_F;  // NaN passes on
         float* out = p.stats_out + (static_cast<size_t>(bh) * p.Tq + qt) * 256;
         out[row] = BIAS && live ? fmaf(-slope_of(p.slopes, head) * kLog2e, static_cast<float>(row / p.g), negl) : negl;
-        out[128 + row] = live ? (sums[row] + sums[128 + row]) + (sums[256 + row] + sums[384 + row]) : 0.f;
+        const int* nk = reinterpret_cast<const int*>(sums) + 1024 + row;
+        const float* from = sums + ((nk[0] + nk[128]) + (nk[256] + nk[384]) == 1 ? 512 : 0) + row;
+        out[128 + row] = live ? (from[0] + from[128]) + (from[256] + from[384]) : 0.f;
       }
     } else if (fin) {
       tc_fence_after();

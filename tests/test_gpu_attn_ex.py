@@ -634,3 +634,28 @@ def test_gradients_of_a_joined_pair(mcs, parts, d):
     attn_ref.check(torch.cat(dv, 1), twice("dv"), "dv")
     attn_ref.check(torch.cat(dk, 1), twice("dk"), "dk")
     attn_ref.check(sum(x.double() for x in dq), twice("dq", attn_ref.U * sum(x.double().abs() for x in dq)), "dq")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("g", [1, 3])
+@pytest.mark.parametrize("kw", [dict(), dict(cap=20.0), dict(slopes=True)], ids=["plain", "capped", "biased"])
+def test_a_single_key_has_no_score_gradient(mcs, kw, g, d):
+    """A row with one key has P = 1 whatever its score: dq is 0 to the bit, and the row adds nothing to dk; in calls with one
+    key, under a causal mask, and in documents of one token, alone or among others."""
+    slopes = torch.tensor([.3 * (h + 1) for h in range(2 * g)], device="cuda") if "slopes" in kw else None
+    shape = lambda n, nk, **k: mcs.AttnShape(2, 2 * g, 2, n, nk, d, cap=kw.get("cap", 0.0), **k)  # noqa: E731
+    for n, nk in ((1, 1), (130, 1)):
+        t = inputs(2, 2 * g, 2, n, nk, d, seed=61)
+        got = run(mcs, shape(n, nk), *t, slopes=slopes)
+        assert not got["dq"].any() and not got["dk"].any() and got["dv"].any()
+    t = inputs(2, 2 * g, 2, 300, 300, d, seed=62)
+    got = run(mcs, shape(300, 300, causal=True), *t, slopes=slopes)
+    assert not got["dq"][:, 0].any() and got["dq"][:, 1].any()
+    ids = torch.arange(300, dtype=torch.int32, device="cuda")[None].repeat(2, 1)
+    got = run(mcs, shape(300, 300), *t, slopes=slopes, doc_q=ids, doc_k=ids)
+    assert not got["dq"].any() and not got["dk"].any()
+    ids[:, 100:250] = 100
+    got = run(mcs, shape(300, 300), *t, slopes=slopes, doc_q=ids, doc_k=ids)
+    alone = torch.ones(300, dtype=torch.bool, device="cuda")
+    alone[100:250] = False
+    assert not got["dq"][:, alone].any() and not got["dk"][:, alone].any() and got["dq"][:, ~alone].any()
