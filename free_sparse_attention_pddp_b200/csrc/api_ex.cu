@@ -104,8 +104,6 @@ struct FwdPlan {
   int tpt, Tq, Tk, single, nsplit, chunk;
 };
 
-constexpr int kSms = 148;
-
 // A CTA takes two query tiles that share their key tiles, or one (single), half
 // of its keys to each slot. While a wave has room the keys are split further and
 // a second launch joins the parts, in about three steps' time (a step, one key

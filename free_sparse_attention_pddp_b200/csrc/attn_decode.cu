@@ -17,7 +17,10 @@
 //
 // 1 request of 75600 keys (8 KV heads, 40 query heads, d = 128): 51 us for 310 MB,
 // 6.1 TB/s of the 6.46 that a copy reaches, and 5 us for the join; 64 requests
-// of ragged lengths run at a copy's rate.
+// of ragged lengths run at a copy's rate. Up to 16 query heads to a KV head take one
+// 16-row tile; up to 32 two, which is arithmetic beyond the loads (16 requests of
+// 16384 keys of one KV head, d = 128: 16 heads 38 us, 32 heads 56); more go to several
+// CTAs, each of which reads the cache (64 heads 89, 128 heads 153 us).
 //
 // P is split into two bf16 terms for P V: the products are free here, and the
 // output keeps fp32 accuracy.

@@ -20,7 +20,7 @@ namespace mcs {
 // Calls f with the head size and the call's options as compile-time constants.
 // One kernel per combination: the options' code in one body overflows the
 // instruction cache (with all of it the capped dK/dV and dQ passes ran 1.29
-// times as long, 5.44 against 4.23 ms on 37 heads of 8192 tokens).
+// times as long on 37 heads of 8192 tokens).
 template <typename F>
 cudaError_t with_options(int d, const ExTile& p, F f) {
   using T = std::true_type;
@@ -46,8 +46,8 @@ cudaError_t with_options(int d, const ExTile& p, F f) {
 // 2 clears padded rows, warp 3 only completes their warpgroup; 16 softmax warps,
 // four to each SM sub-partition, so that one warp's TMEM loads, barriers and
 // dependent arithmetic hide behind the others' exponentials. (37 heads of 8192
-// tokens, d = 128, forward, against 8 softmax warps of twice the columns: plain
-// scores 1001 and 1004 TFLOP/s, capped 716 and 653, biased 833 and 781.) In the
+// tokens, d = 128, forward, against 8 softmax warps of twice the columns, when
+// both were built: capped scores 10 % and biased 7 % faster, plain the same.) In the
 // forward kernel setmaxnreg moves registers from the first warpgroup to the
 // softmax; the gradients' kernel runs at the launch's count.
 constexpr int kExThreads = 640;

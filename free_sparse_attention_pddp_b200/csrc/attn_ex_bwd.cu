@@ -1,9 +1,10 @@
 // Attention with modified scores, gradients (mcs_dense_bwd), on the tensor
-// cores. With P = 2^(s - lse) and D_i = d_o_i . o_i,
+// cores. With P = 2^(s - lse) and D_i = sum_j P_ij dP_ij (= d_o_i . o_i),
 //   dP = d_o V^T,  dS = P (dP - D) (1 - t^2),
 //   dV = P^T d_o,  dK = scale dS^T Q,  dQ = scale dS K.
 //
-// Two kinds of CTAs in one launch: dK and dV are sums over queries, dQ over
+// First D, by a sweep of two products (ex_delta_kernel) or from the given o
+// (ex_row_stats). Then two kinds of CTAs in one launch: dK and dV are sums over queries, dQ over
 // keys, so a single sweep would have to add one of them into global memory from many
 // CTAs, in an order that changes from run to run. Here every sum is one CTA's,
 // in a fixed order, at the price of seven products per tile instead of five.
@@ -27,10 +28,16 @@
 //
 // Four threads work on a row of a tile, 32 of its columns each.
 //
-// What bounds it: the products. 37 heads of 8192 tokens, d = 128: 3.06 to
-// 3.17 ms, 1000 to 1035 TFLOP/s on the formulas' five products, 1400 to 1450 of the 1684 that a plain product
-// reaches on the seven that run; capped scores 3.9 ms; d = 64 2.25 ms (the
+// What bounds it: the products (67 % of the tensor pipe's time in the launch of
+// dK, dV and dQ) and the exponentials (56 % of the special-function unit's in the
+// sweep). 37 heads of 8192 tokens, d = 128: 4.1 ms, 770 TFLOP/s on the formulas'
+// five products, of the 1684 that a plain product reaches; with D from the given o
+// 3.1 to 3.4 ms; capped scores 5.5 and 4.2 ms, d = 64 3.1 and 2.35 (the
 // exponentials and the roundings of P and dS are as many for half the products).
+//
+// P and dS are rounded to bf16, the products' operand type: each value by up to
+// 2^-8 of itself, 0.0017 (relative, rms) in dV, and in dK and dQ, which with the
+// results' own rounding makes 0.0024.
 #include <algorithm>
 
 #include "attn_ex.cuh"

@@ -32,9 +32,14 @@
 // 2130, of which the exponentials are 1550 where the special-function unit needs
 // 1083; O += P V and S 512 each; hand-overs 570) and two slots overlap, so the
 // tensor pipe works 2048 of them. 37 heads of 8192 tokens, d = 128, on GPUs at
-// their power limit: 1.06 to 1.09 ms, 1165 to 1195 TFLOP/s of the 1684 that a
-// plain product reaches; capped scores 1.50 to 1.67, biased 1.3 to 1.5; d = 64,
-// where the exponentials are as many for half the products, 1.07 to 1.10 ms.
+// their power limit: 1.06 to 1.26 ms, 1010 to 1200 TFLOP/s of the 1684 that a
+// plain product reaches; capped scores 1.44 to 1.6, biased 1.17 to 1.4; d = 64,
+// where the exponentials are as many for half the products, 0.95 to 1.12 ms.
+//
+// P is rounded to bf16, the products' operand type: each value by up to 2^-8 of
+// itself, which moves o by up to 0.0012 (relative, sharp scores; less where many
+// terms average it) beside the 0.0017 of o's own rounding. The row sums l take P
+// before it.
 #include "attn_ex.cuh"
 
 namespace mcs {
@@ -55,9 +60,8 @@ constexpr float kRescale = 4.0f;
 __device__ __forceinline__ bool apart_pays(int n, int n0, int n1) {
   return 4 * n > 5 * max(n0, n1) && min(n0, n1) > 0;
 }
-// Pairs of query tiles beyond half of an SM's share of all steps, of which there are fewer than this (two on each of
-// 148 SMs), are cut.
-constexpr int kMostCuts = 296;
+// Pairs of query tiles beyond half of an SM's share of all steps, of which there are fewer than this, are cut.
+constexpr int kMostCuts = 2 * kSms;
 
 // 2^x for x <= 2^21 on the FMA pipe. t = x + 1.5 2^23, rounded down, holds n =
 // floor(x) in its low bits; 2^(x - n) is a polynomial of degree 5 with p(0) = 1,

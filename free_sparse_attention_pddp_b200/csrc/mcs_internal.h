@@ -129,6 +129,8 @@ struct ExParams {
   int* status;
 };
 
+constexpr int kSms = 148;  // of a B200: the sizes of workspaces and launches follow from the shape alone
+
 // The score cap: y(s) = cap log2(e) tanh(k pre s), k pre = scale / cap, for products s = q . k (cap_scores in
 // attn_ex.cuh). pre is 1, or the power of two that brings k near 1 where the coefficients would leave fp32's range.
 struct CapFn {
