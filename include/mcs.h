@@ -290,7 +290,8 @@ mcs_status mcs_dense_ex(const mcs_attn_shape* shape, const mcs_attn_opts* opts, 
  * gradient d_o of a scalar with respect to o, writes dq, dk and dv (summed over
  * the query heads that share a KV head). No atomics: the sums' order is fixed.
  * lse is what mcs_dense_ex gave for the same shape, options and inputs, and
- * D_i = sum_j P_ij dP_ij is summed in fp32; o is not read. With MCS_ATTN_D_FROM_O,
+ * D_i = sum_j P_ij dP_ij is summed in fp32; o is checked like the others, but not
+ * read. With MCS_ATTN_D_FROM_O,
  * D_i = d_o_i . o_i comes from the given o instead: for an (o, lse) that was joined
  * from several calls over parts of the keys, each of which then gets its part of
  * the gradients, and for speed (a fifth of a long training step). The rounding of o
