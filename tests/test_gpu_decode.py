@@ -350,3 +350,42 @@ def test_calls_side_by_side(mcs):
     for c in callers:
         assert all(mcs.mcs_poll_status(w)[0] == 0 for w in c.ws)
         assert all(torch.equal(x, y) for x, y in zip(c.out, want.out))
+
+
+def test_streams_as_arguments(mcs):
+    """A stream given to the call, as torch's object or its handle, is the one that it runs on."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    N, Hq, Hkv, d, P = 300, 4, 2, 64, 200
+    q, k, v, d_o = rand(g, 1, N, Hq, d), rand(g, 1, N, Hkv, d), rand(g, 1, N, Hkv, d), rand(g, 1, N, Hq, d)
+    q1, kp, vp = rand(g, 1, Hq, d), rand(g, P, Hkv, d), rand(g, P, Hkv, d)
+    lens = torch.tensor([250], dtype=torch.int32, device="cuda")
+    shape, one, behind = mcs.AttnShape(1, Hq, Hkv, N, N, d), mcs.DecodeShape(1, Hq, Hkv, N, d), mcs.DecodeShape(1, Hq, Hkv, N, d, P=P)
+    ws = [mcs.attn_workspace(shape, op) for op in (mcs.MCS_OP_DENSE_EX, mcs.MCS_OP_DENSE_BWD)]
+    ws += [mcs.decode_workspace(s) for s in (one, behind)]
+
+    def call(stream, inputs):
+        q, k, v, d_o, q1 = inputs
+        o, dq, dk, dv, a, b = (torch.zeros_like(t) for t in (q, q, k, v, q1, q1))
+        lse = torch.zeros(1, Hq, N, device="cuda")
+        return [o, dq, dk, dv, a, b], [
+            lambda: mcs.mcs_dense_ex(shape, q, k, v, o, lse, ws[0], stream=stream),
+            lambda: mcs.mcs_dense_bwd(shape, q, k, v, o, lse, d_o, dq, dk, dv, ws[1], stream=stream),
+            lambda: mcs.mcs_decode(one, q1, k, v, lens, a, None, ws[2], stream=stream),
+            lambda: mcs.mcs_decode_shared(behind, q1, kp, vp, k, v, lens, b, None, ws[3], stream=stream)]
+
+    want, calls = call(None, (q, k, v, d_o, q1))
+    for f in calls:
+        f()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        late = [torch.zeros_like(t) for t in (q, k, v, d_o, q1)]
+        got, calls = call(stream, late)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):  # the inputs come late on that stream: another one would read zeros
+            torch.cuda._sleep(20_000_000)
+            for t, s in zip(late, (q, k, v, d_o, q1)):
+                t.copy_(s)
+        for f in calls:
+            f()
+        side.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
